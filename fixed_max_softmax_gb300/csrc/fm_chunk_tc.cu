@@ -52,6 +52,7 @@
 #include <mutex>
 
 #include "fm_internal.h"
+#include "fm_tc.cuh"
 
 namespace fm {
 namespace {
@@ -64,7 +65,6 @@ constexpr int kTileBytes = kBK * kHD * 2;     // 32 KiB
 constexpr int kPanelBytes = 128 * 64 * 2;     // 128 rows x 64 bf16 (one 128-byte swizzle span)
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazyRescale = 8.0f;          // online path: rescale when the max grows by > 2^8
 
 // shared memory map (offsets from a 1024-byte aligned base)
 constexpr int kOffQ = 0;
@@ -90,314 +90,8 @@ constexpr int kPStages = kStages - 1;
 constexpr int kOffPStage = kOffKV + kPStages * kTileBytes;
 constexpr int kBoxBytes = kBQ * 128;  // 32 fp32 columns x 128 rows
 
-// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator (bits 4-5 = 1),
-// A and B bf16 (bits 7-9 = 1, bits 10-12 = 1), A K-major, B K-major (bit 16 = 0) or
-// MN-major (bit 16 = 1), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
-constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-constexpr uint32_t kIdescQK = idesc_bf16(kBQ, kBK, false);  // S = Q K^T: K is [keys, D], K-major
-constexpr uint32_t kIdescPV = idesc_bf16(kBQ, kHD, true);   // O = P V:   V is [keys, D], MN-major
-
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void fence_mbar_init() {
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-// Slow path of wait_phase: poll until the phase completes, the time limit passes or, if
-// `abort_flag` is given, another role of the CTA has already given up.  On expiry the
-// first failing wait of the launch records itself in err[0..5]: role code, `tag`
-// (barrier index << 16 | tile index j), block x, y, z and thread, and raises the CTA's
-// abort flag.
-__device__ __noinline__ bool wait_phase_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                             unsigned long long timeout_ns, unsigned int *err,
-                                             unsigned int code, unsigned int tag) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_test(bar, parity)) return true;
-    if ((it & 31) == 0) {
-      if (abort_flag && *abort_flag) return false;
-      if (globaltimer() - t0 > timeout_ns) {
-        if (abort_flag) *abort_flag = 1;
-        if (atomicCAS(err, 0u, code) == 0u) {
-          err[1] = tag;
-          err[2] = blockIdx.x;
-          err[3] = blockIdx.y;
-          err[4] = blockIdx.z;
-          err[5] = threadIdx.x;
-        }
-        return false;
-      }
-    }
-  }
-}
-// Wait for the phase of `bar` with parity `parity`; false when the wait gave up.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                           unsigned long long timeout_ns, unsigned int *err,
-                                           unsigned int code, unsigned int tag = 0) {
-  if (mbar_test(bar, parity)) return true;
-  return wait_phase_slow(bar, parity, abort_flag, timeout_ns, err, code, tag);
-}
-__device__ __forceinline__ unsigned int wtag(int bar_index, int j) {
-  return ((unsigned int)bar_index << 16) | ((unsigned int)j & 0xFFFFu);
-}
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0,
-                                            int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
-// L2 eviction priorities for bulk copies (createpolicy): evict_last for data read again soon
-// (an accumulator that the next chunk adds into, when it fits in L2), evict_first for data
-// read once (a Q tile of the persistent schedule).
-__device__ __forceinline__ uint64_t policy_evict_last() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-__device__ __forceinline__ uint64_t policy_evict_normal() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-__device__ __forceinline__ uint64_t policy_evict_first() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-__device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0, int c1,
-                                                 int c2, int c3, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(pol)
-      : "memory");
-}
-
-// O of one Q tile from shared memory into the fp32 accumulator (3-D map over [B*H, Sq, D]):
-// added to it (reduce) or written over it (store), with the L2 priority `pol`.  Rows past Sq
-// are clipped by the map.
-__device__ __forceinline__ void tma_acc_3d(const CUtensorMap *tm, uint32_t src, int c0, int c1, int c2, bool add,
-                                           uint64_t pol) {
-  if (add)
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group.L2::cache_hint"
-                 " [%0, {%2, %3, %4}], [%1], %5;" ::"l"(reinterpret_cast<uint64_t>(tm)),
-                 "r"(src), "r"(c0), "r"(c1), "r"(c2), "l"(pol)
-                 : "memory");
-  else
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint"
-                 " [%0, {%2, %3, %4}], [%1], %5;" ::"l"(reinterpret_cast<uint64_t>(tm)),
-                 "r"(src), "r"(c0), "r"(c1), "r"(c2), "l"(pol)
-                 : "memory");
-}
-// acc += v (4 consecutive fp32) as one reduction in the memory system: the same fp32 add
-// as the registers would do, without reading the accumulator through the SM.
-__device__ __forceinline__ void red_add_v4(float *dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
-// Commit the bulk operations issued so far and wait until they have read their shared-memory
-// source, so that it may be reused or released; their global writes complete with the grid,
-// before the next kernel in the stream (or its griddepcontrol.wait) proceeds.
-__device__ __forceinline__ void bulk_commit_and_wait_smem_read() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// Shared-memory writes of this thread become visible to the bulk-copy (async) proxy.
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void named_barrier(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-// Named barrier over `count` threads that also returns the AND of their `v`.
-__device__ __forceinline__ bool named_barrier_and(int id, int count, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred pin, pout;\n\t"
-      "setp.ne.u32 pin, %1, 0;\n\t"
-      "bar.red.and.pred pout, %2, %3, pin;\n\t"
-      "selp.u32 %0, 1, 0, pout;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-// D[tmem] (+)= A[smem desc] * B[smem desc]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem desc]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
-// Shared-memory matrix descriptor: start, leading and stride byte offsets (>> 4), the
-// fixed version bits (46-48 = 0b001) and the 128-byte swizzle mode (bits 61-63 = 2).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo & 0x3FFFFu) >> 4) << 16) |
-         ((uint64_t)((sbo & 0x3FFFFu) >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-#define FM_R8(i) "=r"(r[i + 0]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
-                 "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-// 32 consecutive 32-bit TMEM columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-      "[%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : FM_R8(0), FM_R8(8), FM_R8(16), FM_R8(24)
-      : "r"(taddr)
-      : "memory");
-}
-// 16 columns of this warp's 32 TMEM lanes (one fp32 column per register), waited for.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : FM_R8(0), FM_R8(8)
-      : "r"(taddr)
-      : "memory");
-}
-// The same load without waiting: the registers are valid only after tmem_ld_wait(r).
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-      "[%32];"
-      : FM_R8(0), FM_R8(8), FM_R8(16), FM_R8(24)
-      : "r"(taddr)
-      : "memory");
-}
-#undef FM_R8
-#define FM_W8(i) "+r"(r[i + 0]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), \
-                 "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
-// Wait for this thread's TMEM loads.  `r` (the destination of the last one) passes through
-// the instruction, so the compiler cannot schedule a use of it before the wait.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : FM_W8(0), FM_W8(8), FM_W8(16), FM_W8(24) : : "memory");
-}
-// Ties `r` (the destination of an earlier load covered by a tmem_ld_wait just before)
-// to this point, so that no use of it is scheduled above that wait.
-__device__ __forceinline__ void tmem_reg_tie(uint32_t (&r)[32]) {
-  asm volatile("" : FM_W8(0), FM_W8(8), FM_W8(16), FM_W8(24) : : "memory");
-}
-#undef FM_W8
-// Two fp32 lanes in one 64-bit register (Blackwell's packed fp32x2 arithmetic).
-__device__ __forceinline__ uint64_t f2_pack(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
-      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
-      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// two fp32 -> one bf16x2 word, `lo` in the low half (the lower column index)
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
+constexpr uint32_t kIdescQK = idesc_f16(kBQ, kBK, false, true);  // S = Q K^T: K is [keys, D], K-major
+constexpr uint32_t kIdescPV = idesc_f16(kBQ, kHD, true, true);   // O = P V:   V is [keys, D], MN-major
 
 // The lane index, read where it is used: arithmetic on it cannot be hoisted out of an enclosing
 // loop (IN_LOOP: the epilogue helpers run once per item inside the persistent kernel's item
@@ -613,22 +307,6 @@ __device__ __forceinline__ void acc_merge_warp(uint8_t *slab, uint32_t tO, int l
   }
 }
 
-// p = 2^(alpha*s - bias) for 32 scores of one full chunk, two at a time with fp32x2 FMA and
-// adds; the row sum goes to two pair accumulators, P to 16 bf16x2 words pk[OFF..OFF+16).
-template <int OFF, int NPK>
-__device__ __forceinline__ void exp_chunk_full(const uint32_t (&s)[32], uint64_t a2, uint64_t nb2, uint64_t &acc0,
-                                               uint64_t &acc1, uint32_t (&pk)[NPK]) {
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    float z0, z1;
-    f2_unpack(f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), a2, nb2), z0, z1);
-    const float p0 = ex2(z0), p1 = ex2(z1);
-    const uint64_t pp = f2_pack(__float_as_uint(p0), __float_as_uint(p1));
-    if (e & 1) acc1 = f2_add(acc1, pp); else acc0 = f2_add(acc0, pp);
-    pk[OFF + e] = pack_bf16(p0, p1);
-  }
-}
-
 // The smallest key sink of the head's list (in shared memory: ascending int32, INT_MAX
 // pads) above `g`, or INT_MAX.
 __device__ __forceinline__ int sink_after_key(const int32_t *ssk, int g) {
@@ -674,127 +352,6 @@ __device__ __noinline__ void mask_tile(uint32_t tS, int nvalid, int g0, const in
     tmem_st32(tS + 32 * c, sc);
   }
   tmem_st_wait();
-}
-
-// Fixed-m softmax of one 128x128 S tile for this thread's row; P overwrites S.  The four
-// 32-column TMEM loads are double-buffered: chunk c+1 is in flight while chunk c is
-// exponentiated.  Key columns to leave out hold -inf (mask_tile) and give p = 0.  P leaves in
-// 16-column stores, one per chunk, or with WIDE (the fixed-m tile loop, which has the
-// registers) in one 32-column store per 64 keys: fewer TMEM stores, measured faster there.
-template <bool WIDE>
-__device__ __forceinline__ void softmax_fixed_tile(uint32_t tS, float alpha, float nbias, float (&l)[4]) {
-  constexpr int NPK = WIDE ? 32 : 16;
-  uint32_t sa[32], sb[32];
-  uint32_t pk[NPK];
-  tmem_ld32_async(tS, sa);
-  tmem_ld_wait(sa);
-  const uint64_t a2 = f2_pack(__float_as_uint(alpha), __float_as_uint(alpha));
-  const uint64_t nb2 = f2_pack(__float_as_uint(nbias), __float_as_uint(nbias));
-  uint64_t acc0 = 0, acc1 = 0;  // +0.0f pairs
-  // P columns [16c, 16c+16) of chunk c lie in S columns already read
-  tmem_ld32_async(tS + 32, sb);
-  exp_chunk_full<0>(sa, a2, nb2, acc0, acc1, pk);
-  if constexpr (!WIDE) tmem_st16(tS + 0, pk);
-  tmem_ld_wait(sb);
-  tmem_ld32_async(tS + 64, sa);
-  if constexpr (WIDE) {
-    exp_chunk_full<16>(sb, a2, nb2, acc0, acc1, pk);
-    tmem_st32(tS + 0, pk);
-  } else {
-    exp_chunk_full<0>(sb, a2, nb2, acc0, acc1, pk);
-    tmem_st16(tS + 16, pk);
-  }
-  tmem_ld_wait(sa);
-  tmem_ld32_async(tS + 96, sb);
-  exp_chunk_full<0>(sa, a2, nb2, acc0, acc1, pk);
-  if constexpr (!WIDE) tmem_st16(tS + 32, pk);
-  tmem_ld_wait(sb);
-  if constexpr (WIDE) {
-    exp_chunk_full<16>(sb, a2, nb2, acc0, acc1, pk);
-    tmem_st32(tS + 32, pk);
-  } else {
-    exp_chunk_full<0>(sb, a2, nb2, acc0, acc1, pk);
-    tmem_st16(tS + 48, pk);
-  }
-  float x0, x1, y0, y1;
-  f2_unpack(acc0, x0, x1);
-  f2_unpack(acc1, y0, y1);
-  l[0] += x0;
-  l[1] += x1;
-  l[2] += y0;
-  l[3] += y1;
-}
-
-// max(a, b, c) in one instruction (the three-input form of max.f32; a NaN operand is ignored,
-// as fmaxf does).
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// The max of 64 scores in four independent chains (one chain would put every max
-// operation on the tile's critical path), two new scores per instruction.
-__device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (&b)[32], float mx) {
-  float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < 32; e += 4) {
-    m0 = max3f(m0, __uint_as_float(a[e]), __uint_as_float(a[e + 2]));
-    m1 = max3f(m1, __uint_as_float(a[e + 1]), __uint_as_float(a[e + 3]));
-    m2 = max3f(m2, __uint_as_float(b[e]), __uint_as_float(b[e + 2]));
-    m3 = max3f(m3, __uint_as_float(b[e + 1]), __uint_as_float(b[e + 3]));
-  }
-  return max3f(m0, m1, fmaxf(m2, m3));
-}
-
-// Online softmax of one S tile for this thread's row, in two passes over TMEM: the first
-// takes the row max of the 128 scores (two column halves, 64 registers), the second
-// exponentiates exactly like the fixed-m tile (double-buffered 32-column loads) with the
-// running max as the shift.  The tile max updates the running max `run` (base-2 units)
-// lazily: only when it grows by more than 2^8, or on the first tile.  The row sum is
-// rescaled before the new terms are added, and O in TMEM after P is out.  The rescale
-// decision is per row but tcgen05.ld/st are warp-collective, so the warp rescales when any
-// of its rows needs it and the other rows use a scale of 1.  Columns to leave out (past the
-// chunk's end, key sinks) hold -inf (mask_tile): they drop out of the max and give p = 0;
-// while every key so far was left out, run stays -inf and the shift used is 0.
-__device__ __forceinline__ void softmax_online_tile(uint32_t tS, uint32_t tO, float alpha, bool have_o, float &run,
-                                                    float (&l)[4]) {
-  float mx;
-  {
-    uint32_t sa[32], sb[32];
-    tmem_ld32_async(tS, sa);
-    tmem_ld32_async(tS + 32, sb);
-    tmem_ld_wait(sa);
-    tmem_reg_tie(sb);
-    mx = max64(sa, sb, -INFINITY);
-    tmem_ld32_async(tS + 64, sa);
-    tmem_ld32_async(tS + 96, sb);
-    tmem_ld_wait(sa);
-    tmem_reg_tie(sb);
-    mx = max64(sa, sb, mx);
-  }
-  const float zmax = mx * alpha;
-  const bool need = run == -INFINITY || zmax > run + kLazyRescale;
-  const bool any = __any_sync(0xffffffffu, need);
-  float sc = 1.0f;
-  if (any) {
-    const float nr = need ? fmaxf(run, zmax) : run;
-    // O holds earlier tiles only when j > 0, and nothing but zeros while run is -inf
-    if (have_o && need) sc = run == -INFINITY ? 0.f : ex2(run - nr);
-    run = nr;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) l[i] *= sc;
-  }
-  softmax_fixed_tile<false>(tS, alpha, run == -INFINITY ? 0.f : -run, l);
-  if (any && have_o) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      tmem_ld32(tO + c * 32, o);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sc);
-      tmem_st32(tO + c * 32, o);
-    }
-  }
 }
 
 // One CTA per work item (grid (pairs, H, B)): the schedule every launch takes unless the
