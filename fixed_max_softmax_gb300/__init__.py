@@ -11,9 +11,12 @@ Functions with the ABI's names (same arguments, torch tensors in place of pointe
 ``fm_attn_chunk_final``, ``fm_attn_chunks``, ``fm_fold_sinks``, ``fm_finalize``,
 ``fm_finalize_lse``, ``fm_sync_status``,
 ``fm_probe_wait_timeout``,
-``fm_last_error``, ``fm_version``.
+``fm_last_error``, ``fm_version``; and for requests of different lengths
+``fm_attn_seqs_workspace_size``, ``fm_attn_varlen``, ``fm_attn_paged``, ``fm_paged_extend``,
+``fm_paged_write``.
 
-``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
+``attention_varlen()`` is the one-call form of packed prompts, ``PagedKVCache`` owns a paged
+cache with its bookkeeping (extend, write, attention).  ``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
 (bounds, one ``fm_attn_chunk`` per KV chunk, finalize); ``attention()`` is the
 one-call form.
 
@@ -21,6 +24,7 @@ There is no CPU path: if the library is not built, ``load()`` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -41,10 +45,13 @@ ERROR_NAMES = {0: "FM_OK", 1: "FM_ERR_ARG", 2: "FM_ERR_SHAPE", 3: "FM_ERR_DTYPE"
 ABI_SYMBOLS = ("fm_bounds_workspace_size", "fm_bounds", "fm_attn_chunk", "fm_finalize", "fm_sync_status",
                "fm_last_error", "fm_version", "fm_bounds_noalloc", "fm_finalize_lse", "fm_probe_wait_timeout",
                "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
-               "fm_bounds_local", "fm_bounds_combine", "fm_attention_host")
+               "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
+               "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write")
 FM_MAX_CHUNKS = 8
 FM_MAX_SINKS = 8
 FM_NOALLOC_SCRATCH_BYTES = 4 << 20
+FM_MAX_GROUP = 64
+FM_MAX_SEQS = 8192
 
 
 class FMError(RuntimeError):
@@ -87,6 +94,23 @@ class fm_host_buffers(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class fm_seqs_opts(ctypes.Structure):
+    _fields_ = [("softmax_scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32)]
+
+
+class fm_seqs(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int64), ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int64)]
+
+
+class fm_page_state(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int64), ("page_size", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int64),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("kv_len_out", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -116,6 +140,11 @@ def load(path: str | None = None):
     lib.fm_bounds_local.argtypes = [P, P, P, i64, i64, P, P, P, P, P, ctypes.c_size_t, P]
     lib.fm_bounds_combine.argtypes = [P, ctypes.c_int, P, P, P]
     lib.fm_attention_host.argtypes = [P, P, P, P, ctypes.c_int, P, ctypes.c_int, P, P, P]
+    lib.fm_attn_seqs_workspace_size.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.fm_attn_varlen.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.fm_attn_paged.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.fm_paged_extend.argtypes = [P, P, P, i64, P, P, P, P, P]
+    lib.fm_paged_write.argtypes = [P, P, P, P, P, P]
     lib.fm_sync_status.argtypes = [P]
     lib.fm_last_error.restype = ctypes.c_char_p
     lib.fm_last_error.argtypes = []
@@ -123,7 +152,8 @@ def load(path: str | None = None):
     for name in ("fm_bounds_workspace_size", "fm_bounds", "fm_attn_chunk", "fm_finalize", "fm_sync_status",
                  "fm_version", "fm_bounds_noalloc", "fm_finalize_lse", "fm_probe_wait_timeout",
                  "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
-                 "fm_bounds_local", "fm_bounds_combine", "fm_attention_host"):
+                 "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
+                 "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -438,3 +468,184 @@ class HostPipeline:
         st = (ctypes.c_void_p * 3)(*[s.cuda_stream for s in self.streams])
         return _check(load().fm_attention_host(qs, ks, vs, os_, n, lens, len(chunks), ctypes.byref(self.fa.opt),
                                                ctypes.byref(self.dev), st))
+
+
+# ---- requests of different lengths, and a paged key/value cache ------------------------------------
+def seqs_opts(causal: bool = True, window: int = 0, softmax_scale: float = 0.0) -> fm_seqs_opts:
+    return fm_seqs_opts(float(softmax_scale), int(bool(causal)), int(window))
+
+
+def _rows(t: torch.Tensor) -> fm_tensor:
+    """Describe packed rows: a [T, H, D] tensor, or a [1, H, T, D] one (any strides)."""
+    if t.dim() == 3:
+        st = t.stride()
+        return fm_tensor(t.data_ptr() or None, _DTYPES.get(t.dtype, -1), 0, 1, t.shape[1], t.shape[0], t.shape[2],
+                         (ctypes.c_int64 * 4)(0, st[1], st[0], st[2]))
+    return tensor(t)
+
+
+def _on_device(device: int, **tensors):
+    """Every tensor on the given CUDA device: the kernels get raw pointers."""
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device.index != device):
+            raise FMError(FM_ERR_ARG, f"{name} must be on the current CUDA device (cuda:{device}), not {t.device}")
+
+
+def _ints(t, dtype, numel, name):
+    """Data pointer of a contiguous int tensor of at least numel elements."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
+        raise FMError(FM_ERR_ARG, f"{name} must be a contiguous {dtype} tensor of at least {numel} elements, got "
+                                  f"{tuple(t.shape)} {t.dtype}")
+    return t.data_ptr() or None
+
+
+def _table(t, n):
+    if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise FMError(FM_ERR_ARG, f"block_table must be a 2-D int32 tensor of at least {n} rows with adjacent "
+                                  f"entries, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr() or None, t.stride(0), t.shape[1]
+
+
+def fm_attn_seqs_workspace_size(n_seqs: int, T: int, Hq: int, Hk: int, D: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().fm_attn_seqs_workspace_size(n_seqs, T, Hq, Hk, D, ctypes.byref(n)))
+    return n.value
+
+
+def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream):
+    tq, to = _rows(q), _rows(o_out)
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != tq.H * tq.S):
+        raise FMError(FM_ERR_ARG, f"lse must be a contiguous float32 [{tq.H}, {tq.S}] tensor, got {tuple(lse.shape)}")
+    return _check(fn(ctypes.byref(tq), ctypes.byref(k), ctypes.byref(v), ctypes.byref(seqs), ctypes.byref(opt),
+                     ctypes.byref(to), _ptr(lse), _ptr(workspace),
+                     0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def fm_attn_varlen(q, k, v, cu_q, cu_k, opt: fm_seqs_opts, o_out, lse=None, workspace=None, stream=None):
+    """Attention of packed requests: q, o_out [T, Hq, D], k, v [Tk, Hk, D] (or [1, H, T, D]); request i
+    owns rows cu[i] .. cu[i+1]-1 of each.  lse [Hq, T]; see include/fm.h."""
+    _on_device(torch.cuda.current_device(), q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o_out=o_out, lse=lse,
+               workspace=workspace)
+    n = cu_q.numel() - 1
+    seqs = fm_seqs(n, _ints(cu_q, torch.int32, 1, "cu_q"), _ints(cu_k, torch.int32, n + 1, "cu_k"), None, None, 0, 0)
+    return _attn_seqs(load().fm_attn_varlen, q, _rows(k), _rows(v), seqs, opt, o_out, lse, workspace, stream)
+
+
+def fm_attn_paged(q, k_cache, v_cache, cu_q, kv_len, block_table, opt: fm_seqs_opts, o_out, lse=None, workspace=None,
+                  stream=None):
+    """Attention of each request's new tokens (q, o_out [T, Hq, D], packed by cu_q) over its pages:
+    caches [pages, Hk, page_size, D] (any strides), block_table int32 [n, width], kv_len int32 [n]
+    with the new tokens counted; see include/fm.h."""
+    _on_device(torch.cuda.current_device(), q=q, k_cache=k_cache, v_cache=v_cache, cu_q=cu_q, kv_len=kv_len,
+               block_table=block_table, o_out=o_out, lse=lse, workspace=workspace)
+    n = cu_q.numel() - 1
+    table, stride, width = _table(block_table, n)
+    seqs = fm_seqs(n, _ints(cu_q, torch.int32, 1, "cu_q"), None, _ints(kv_len, torch.int32, n, "kv_len"), table, stride,
+                   width)
+    return _attn_seqs(load().fm_attn_paged, q, tensor(k_cache), tensor(v_cache), seqs, opt, o_out, lse, workspace, stream)
+
+
+def fm_paged_extend(new_len, release, kv_len, kv_len_out, block_table, free_pages, free_count, free_count_out,
+                    page_size: int, cu_q, slots, positions, status, stream=None):
+    """Room in the pages for new_len[i] more tokens of every request (release[i] != 0: the row's
+    request has ended and gives its pages back first).  kv_len_out and free_count_out may be kv_len
+    and free_count.  Fills cu_q [n+1], slots and positions [max tokens], status [1]; see include/fm.h."""
+    _on_device(torch.cuda.current_device(), new_len=new_len, release=release, kv_len=kv_len, kv_len_out=kv_len_out,
+               block_table=block_table, free_pages=free_pages, free_count=free_count, free_count_out=free_count_out,
+               cu_q=cu_q, slots=slots, positions=positions, status=status)
+    n, i32 = new_len.numel(), torch.int32
+    table, stride, width = _table(block_table, n)
+    st = fm_page_state(n, int(page_size), free_pages.numel(), table, stride, width,
+                       _ints(free_pages, i32, 0, "free_pages"), _ints(free_count, i32, 1, "free_count"),
+                       _ints(free_count_out, i32, 1, "free_count_out"), _ints(kv_len, i32, n, "kv_len"),
+                       _ints(kv_len_out, i32, n, "kv_len_out"))
+    rel = None if release is None else _ints(release, torch.uint8, n, "release")
+    cap = slots.numel()
+    return _check(load().fm_paged_extend(ctypes.byref(st), _ints(new_len, i32, n, "new_len"), rel, cap,
+                                         _ints(cu_q, i32, n + 1, "cu_q"), _ints(slots, torch.int64, cap, "slots"),
+                                         _ints(positions, i32, cap, "positions"), _ints(status, i32, 1, "status"),
+                                         _stream(stream)))
+
+
+def fm_paged_write(k, v, slots, k_cache, v_cache, stream=None):
+    """k, v rows [T, H, D] (or [1, H, T, D]) put at their slots of the caches [pages, H, page_size, D]."""
+    _on_device(torch.cuda.current_device(), k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
+    tk = _rows(k)
+    return _check(load().fm_paged_write(ctypes.byref(tk), ctypes.byref(_rows(v)), _ints(slots, torch.int64, tk.S, "slots"),
+                                        ctypes.byref(tensor(k_cache)), ctypes.byref(tensor(v_cache)), _stream(stream)))
+
+
+def _on_stream(stream):
+    """Context whose current stream is `stream` (None: as it is), so that what it allocates belongs to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def attention_varlen(q, k, v, cu_q, cu_k=None, causal=True, window=0, softmax_scale=0.0, out_dtype=None, with_lse=False,
+                     stream=None):
+    """One-call attention of packed requests: returns o [T, Hq, D] (and lse [Hq, T]).  q [T, Hq, D],
+    k, v [Tk, Hk, D], cu_q and cu_k int32 [n+1] (cu_k None: the same as cu_q)."""
+    T, Hq, D = q.shape
+    with _on_stream(stream):
+        o = torch.zeros(T, Hq, D, dtype=out_dtype or q.dtype, device=q.device)  # rows behind the last request stay zero
+        lse = torch.full((Hq, T), float("-inf"), dtype=torch.float32, device=q.device) if with_lse else None
+        ws = torch.empty(fm_attn_seqs_workspace_size(cu_q.numel() - 1, T, Hq, k.shape[1], D), dtype=torch.uint8,
+                         device=q.device)
+        fm_attn_varlen(q, k, v, cu_q, cu_q if cu_k is None else cu_k, seqs_opts(causal, window, softmax_scale), o, lse, ws)
+    return (o, lse) if with_lse else o
+
+
+class PagedKVCache:
+    """A paged key/value cache of one layer and the bookkeeping of up to max_seqs requests.
+
+    extend(new_len, release) makes room for the next tokens and fills cu_q, slots, positions and
+    kv_len; write(k, v) puts their rows into the pages; attention(q) attends over them.  Everything
+    stays on the device: nothing here waits for the GPU, and status (0: the last extend fitted) is read
+    when the caller chooses.  Several layers share one bookkeeping by sharing it: PagedKVCache(...,
+    shared=first) keeps pages of its own and uses the first layer's tables."""
+
+    def __init__(self, num_pages, page_size, kv_heads, head_dim, max_seqs, max_pages_per_seq, max_tokens,
+                 dtype=torch.bfloat16, device="cuda", shared: "PagedKVCache | None" = None):
+        make = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        self.page_size = int(page_size)
+        pages = torch.empty(2, num_pages, page_size, kv_heads, head_dim, dtype=dtype, device=device)
+        self.k, self.v = pages[0].transpose(1, 2), pages[1].transpose(1, 2)  # [pages, heads, page_size, D]
+        if shared is not None:
+            if (shared.page_size, shared.free_pages.numel()) != (self.page_size, num_pages):
+                raise FMError(FM_ERR_SHAPE, "layers that share tables need the same pages")
+            for name in ("block_table", "free_pages", "free_count", "kv_len", "cu_q", "slots", "positions", "status"):
+                setattr(self, name, getattr(shared, name))
+        else:
+            self.block_table = make(max_seqs, max_pages_per_seq)
+            self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+            self.free_count = make(1).fill_(num_pages)
+            self.kv_len, self.cu_q, self.status = make(max_seqs), make(max_seqs + 1), make(1)
+            self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+            self.positions = make(max_tokens).fill_(-1)
+
+    def extend(self, new_len, release=None, stream=None):
+        """new_len int32 [max_seqs] (0: no new token in that row), release uint8 [max_seqs] or None."""
+        if new_len.numel() != self.kv_len.numel():
+            raise FMError(FM_ERR_SHAPE, f"new_len must have one entry for each of the {self.kv_len.numel()} rows")
+        fm_paged_extend(new_len, release, self.kv_len, self.kv_len, self.block_table, self.free_pages, self.free_count,
+                        self.free_count, self.page_size, self.cu_q, self.slots, self.positions, self.status, stream)
+
+    def write(self, k, v, stream=None):
+        """k, v [T, H, D], T <= max_tokens: the rows of the last extend, in its order (rows behind its
+        last token are skipped)."""
+        fm_paged_write(k, v, self.slots, self.k, self.v, stream)
+
+    def attention(self, q, out=None, lse=None, causal=True, window=0, softmax_scale=0.0, stream=None):
+        """q [T, Hq, D], the new tokens' queries in the order of the last extend; returns o [T, Hq, D]
+        (rows behind the last token are left as they were in `out`, zero without one)."""
+        T, Hq, D = q.shape
+        with _on_stream(stream):
+            if out is None:
+                out = torch.zeros(T, Hq, D, dtype=q.dtype, device=q.device)
+            # from the allocator each time: a captured graph keeps its own, and no two calls share one
+            ws = torch.empty(fm_attn_seqs_workspace_size(self.kv_len.numel(), T, Hq, self.k.shape[1], D),
+                             dtype=torch.uint8, device=q.device)
+            fm_attn_paged(q, self.k, self.v, self.cu_q, self.kv_len, self.block_table,
+                          seqs_opts(causal, window, softmax_scale), out, lse, ws)
+        return out

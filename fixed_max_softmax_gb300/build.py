@@ -18,7 +18,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfm.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
-SOURCES = ["fm_api.cu", "fm_bounds.cu", "fm_chunk_simt.cu", "fm_chunk_tc.cu", "fm_finalize.cu"]
+SOURCES = ["fm_api.cu", "fm_bounds.cu", "fm_chunk_simt.cu", "fm_chunk_tc.cu", "fm_finalize.cu",
+           "fm_paged.cu", "fm_seqs_api.cu", "fm_seqs_plan.cu", "fm_seqs_simt.cu"]
+HEADERS = ["fm_internal.h", "fm_seqs.cuh", "fm_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 
@@ -39,7 +41,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     build_dir = BUILD_DEBUG if debug else BUILD
     lib = os.path.join(build_dir, "libfm.so")
     os.makedirs(build_dir, exist_ok=True)
-    headers = [os.path.join(CSRC, "fm_internal.h"), os.path.join(ROOT, "include", "fm.h")]
+    headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "fm.h")]
     objs = []
     jobs = []
     for src in SOURCES:

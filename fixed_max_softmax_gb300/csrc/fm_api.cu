@@ -21,9 +21,9 @@ namespace fm {
 constexpr int kErrWords = 8;
 __device__ unsigned int g_dev_error[kErrWords];
 
-namespace {
+static thread_local std::string t_err;
 
-thread_local std::string t_err;
+void clear_error() { t_err.clear(); }
 
 int fail(int code, const char *fmt, ...) {
   char buf[512];
@@ -53,6 +53,19 @@ unsigned int *dev_error_ptr() {
   return ptrs[dev];
 }
 
+// Limit of one pipeline wait inside a kernel: kWaitTimeoutNs, or FM_WAIT_TIMEOUT_MS
+// milliseconds from the environment (1 ms to 60 s).
+unsigned long long wait_timeout_ns() {
+  const char *s = getenv("FM_WAIT_TIMEOUT_MS");
+  if (s && *s) {
+    const long long ms = atoll(s);
+    if (ms >= 1 && ms <= 60000) return (unsigned long long)ms * 1000000ull;
+  }
+  return kWaitTimeoutNs;
+}
+
+namespace {
+
 // ceil(log2 n) for n >= 1 (0 for n <= 1): the number of bits of n - 1.
 int ceil_log2_i64(int64_t n) {
   if (n <= 1) return 0;
@@ -66,17 +79,6 @@ int ceil_log2_i64(int64_t n) {
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Limit of one pipeline wait inside a kernel: kWaitTimeoutNs, or FM_WAIT_TIMEOUT_MS
-// milliseconds from the environment (1 ms to 60 s).
-unsigned long long wait_timeout_ns() {
-  const char *s = getenv("FM_WAIT_TIMEOUT_MS");
-  if (s && *s) {
-    const long long ms = atoll(s);
-    if (ms >= 1 && ms <= 60000) return (unsigned long long)ms * 1000000ull;
-  }
-  return kWaitTimeoutNs;
-}
 
 // Validate one fm_tensor and turn it into a View.  `what` names it in messages.
 int to_view(const fm_tensor *t, const char *what, View *v) {
@@ -162,7 +164,7 @@ using namespace fm;
 
 extern "C" {
 
-int fm_version(void) { return (1 << 16) | 2; }
+int fm_version(void) { return (1 << 16) | 3; }
 
 const char *fm_last_error(void) { return t_err.c_str(); }
 
@@ -696,6 +698,19 @@ int fm_sync_status(fm_stream_t stream) {
   if (w[0] != 0) {
     const unsigned int zero[kErrWords] = {};
     cudaMemcpyToSymbol(g_dev_error, zero, sizeof zero);
+    if (w[0] == kDevErrPage)
+      return fail(FM_ERR_INDEX,
+                  "a page table entry of request %u (table position %u) lies outside the cache: %d; the outputs that "
+                  "read it are invalid",
+                  w[1], w[2], (int)w[3]);
+    if (w[0] == kDevErrSlot)
+      return fail(FM_ERR_INDEX, "the slot of token %u lies outside the cache (%lld); its rows were not written", w[1],
+                  (long long)((unsigned long long)w[2] | ((unsigned long long)w[3] << 32)));
+    if (w[0] == kDevErrLength)
+      return fail(FM_ERR_INDEX,
+                  "the lengths of request %u do not fit the tensors (query rows %d to %d, %d keys) and were clamped; "
+                  "outputs are invalid",
+                  w[1], (int)w[2], (int)w[3], (int)w[4]);
     if (w[0] == kDevErrDebugIndex)
       return fail(FM_ERR_INDEX,
                   "a debug build's index check failed and skipped the access (site %u, index %llu, block %u, "

@@ -21,6 +21,9 @@ enum : unsigned int {
   kDevErrTimeoutProbe = 5,
   kDevErrTimeoutBounds = 6,
   kDevErrDebugIndex = 7,  // debug builds: an index check failed (the access was skipped)
+  kDevErrPage = 8,        // a page table entry outside the cache (request, position, entry)
+  kDevErrSlot = 9,        // a cache slot outside the cache (token, slot low and high word)
+  kDevErrLength = 10,     // request lengths that do not fit the tensors (request, rows, keys)
 };
 
 // Debug builds (nvcc -DFM_DEBUG): FM_DCHECK(ok, err, site, index) is false when `ok` is, and then
@@ -145,7 +148,90 @@ cudaError_t launch_fold_sinks_final(const View &q, float alpha, const int32_t *s
                                     const float *sink_v, float *acc_o, float *acc_sum, float *acc_max, const View &o,
                                     float *lse, cudaStream_t st);
 
+// ---- requests of different lengths (fm_seqs_*.cu, fm_paged.cu) ---------------
+constexpr int kMaxSeqs = FM_MAX_SEQS;  // requests of one call: their prefix sums are kept in shared memory
+
+// One attention call over n requests: packed query rows against packed keys (varlen) or the
+// pages of a cache (paged).
+struct SeqsArgs {
+  View q, k, v, o;       // q, o [1,Hq,T,D]; k, v [1,Hk,Tk,D] or [pages,Hk,page_size,D]
+  bool paged;
+  int64_t n;
+  const int32_t *cu_q;   // [n+1]
+  const int32_t *cu_k;   // [n+1], varlen
+  const int32_t *kv_len; // [n], paged
+  const int32_t *table;  // [n, table_width] rows table_stride apart, paged
+  int64_t table_stride, table_width;
+  float alpha;           // softmax_scale * log2(e)
+  int causal, window;
+  float *lse;            // [Hq, T] or nullptr
+  void *ws;
+  unsigned int *err;
+  unsigned long long timeout_ns;
+};
+
+// How a call's rows and keys are cut.  A unit is `tq` tokens of one request with the `group`
+// query heads of one key head (rows = tq * group, token by token); keys go in tiles of `bk`.
+struct SeqsGeom {
+  int group, tq, bk;
+  int slot_rows;  // rows of one partial result
+  int n_slots;    // partial results that fit the workspace
+  int ctas;       // CTAs that the work is spread over
+  int min_tiles;  // a unit is not cut into pieces shorter than this
+};
+
+// One piece of work: a unit against its keys [key0, key1).
+struct __align__(16) SeqsItem {
+  int b, h;       // request (-1: no more work) and key head
+  int nt;         // tokens of the unit
+  int qrow0;      // its first query row
+  int pos0;       // that row's position among the request's keys
+  int kv;         // keys of the request
+  int key0, key1; // keys of this piece (key0 a multiple of the tile from key 0; key1 <= key0: none)
+  int krow0;      // varlen: row of the request's key 0
+  int slot;       // partial result to write, -1: the unit's only piece
+  int pad[2];
+};
+// A unit that was cut: pieces slot0, slot0 + stride, ...
+struct __align__(16) SeqsMerge {
+  int h, nt, qrow0, slot0, stride, nseg;
+  int pad[2];
+};
+// Workspace of an attention call (offsets in bytes).
+struct SeqsSpace {
+  size_t counters, req, items, merges, part_o, part_ml, total;
+  int64_t max_items;
+};
+SeqsGeom seqs_geom_simt(int64_t T, int group);
+SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group);
+SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_t D);
+// Work list of the call into its workspace; then one of the attention kernels; then the merge.
+cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+cudaError_t launch_seqs_simt(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+
+struct PagedExtendArgs {
+  int64_t n, page_size, num_pages, table_stride, table_width, max_tokens;
+  const int32_t *new_len;
+  const uint8_t *release;
+  const int32_t *kv_len;
+  int32_t *kv_out, *table, *free_pages;
+  const int32_t *free_count;
+  int32_t *free_out, *cu_q;
+  int64_t *slots;
+  int32_t *positions, *status;
+};
+cudaError_t launch_paged_extend(const PagedExtendArgs &a, cudaStream_t st);
+cudaError_t launch_paged_write(const View &k, const View &v, const int64_t *slots, const View &kc, const View &vc,
+                               unsigned int *err, cudaStream_t st);
+
 // ---- helpers shared by host code -------------------------------------------
+// The calling thread's error message: cleared at every entry point, set by fail().
+void clear_error();
+int fail(int code, const char *fmt, ...);
+int cuda_fail(cudaError_t e, const char *what);
+unsigned int *dev_error_ptr();         // this device's error word (nullptr: no device)
+unsigned long long wait_timeout_ns();  // limit of one pipeline wait
 int current_device_sm_count();
 // L2 cache size of the current device in bytes (0 if unknown).
 int current_device_l2_bytes();

@@ -1,0 +1,374 @@
+// fm_seqs_plan.cu -- the work list of one attention call over requests of different lengths, and
+// the merge of units that were cut along their keys.
+//
+// Lengths live on the device, so the list is made there: one CTA reads them, decides how far
+// to cut, and writes one entry per piece of work; the attention kernel's CTAs take entries in
+// order from a counter.  Order: request, key head, range of keys, and the unit of queries
+// running fastest (longest first), so that the CTAs at work at one moment mostly read the same
+// key tiles, from L2.  A unit is cut into equal ranges of keys when it holds more than 1 / 3 of
+// an even share of the work, so that no CTA is left with a long piece at the end; a cut unit's
+// pieces leave unnormalised sums (o, max, sum) that seqs_merge_kernel joins in key order, so the
+// result does not depend on which CTA did what.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "fm_seqs.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanArgs {
+  const int32_t *cu_q, *cu_k, *kv_len;
+  int64_t n, T, Tk, cap_keys;  // cap_keys: keys that a row of the page table can hold
+  int paged, Hk, causal, window;
+  SeqsGeom g;
+  unsigned int *counters;
+  int4 *req;  // per request: {first query row, queries, keys, first key row}, {units, tiles a piece, pieces, slot base}
+  SeqsItem *items;
+  SeqsMerge *merges;
+  unsigned int *err;
+};
+
+// Exclusive prefix sum of v over the CTA in thread order; `total` gets the sum.
+__device__ __forceinline__ long long block_scan(long long v, long long *warp_sum, long long &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += u;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += u;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  const long long before = warp > 0 ? warp_sum[warp - 1] : 0;
+  total = warp_sum[kPlanWarps - 1];
+  __syncthreads();
+  return before + inc - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int32_t pre[];  // [n + 1] entries before request i, pieces without keys among them
+  __shared__ long long warp_sum[kPlanWarps];
+  const int tid = threadIdx.x, n = (int)a.n, tq = a.g.tq, bk = a.g.bk;
+  // 1. lengths, clamped to the tensors (a length that does not fit is reported), and the tiles of work
+  long long w = 0, rows = 0;
+  for (int b = tid; b < n; b += kPlanThreads) {
+    const int r0 = a.cu_q[b], r1 = a.cu_q[b + 1];
+    const int q0 = (int)max((int64_t)0, min((int64_t)r0, a.T)), q1 = (int)max((int64_t)q0, min((int64_t)r1, a.T));
+    int k0 = 0, kv;
+    bool bad = q0 != r0 || q1 != r1;
+    if (a.paged) {
+      const int x = a.kv_len[b];
+      kv = (int)max((int64_t)0, min((int64_t)x, a.cap_keys));
+      bad |= kv != x;
+    } else {
+      const int x0 = a.cu_k[b], x1 = a.cu_k[b + 1];
+      k0 = (int)max((int64_t)0, min((int64_t)x0, a.Tk));
+      const int k1 = (int)max((int64_t)k0, min((int64_t)x1, a.Tk));
+      bad |= k0 != x0 || k1 != x1;
+      kv = k1 - k0;
+    }
+    if (bad && a.err && atomicCAS(a.err, 0u, (unsigned)kDevErrLength) == 0u) {
+      a.err[1] = (unsigned)b;
+      a.err[2] = (unsigned)r0;
+      a.err[3] = (unsigned)r1;
+      a.err[4] = (unsigned)kv;
+    }
+    const int q = q1 - q0, nt = (q + tq - 1) / tq;
+    rows += q;
+    a.req[2 * b] = make_int4(q0, q, kv, k0);
+    int longest = 0;
+    if (nt > 0) {
+      const TileRange f = unit_tiles(kv - q, min(tq, q), kv, bk, a.causal, a.window);
+      const TileRange l = unit_tiles(kv - q + (nt - 1) * tq, q - (nt - 1) * tq, kv, bk, a.causal, a.window);
+      // without a window a unit's tiles never shrink with its position; a window bounds them
+      longest = max(f.e - f.a, l.e - l.a);
+      if (a.window > 0) {
+        const long long most = ((long long)a.window + tq + 2 * bk - 3) / bk + 1;
+        longest = (int)min(most, (long long)(kv + bk - 1) / bk);
+      }
+      w += (long long)nt * (f.e - f.a + l.e - l.a + 1) / 2;
+    }
+    a.req[2 * b + 1] = make_int4(nt, longest, 1, 0);
+  }
+  long long work, all_rows;
+  block_scan(w, warp_sum, work);
+  block_scan(rows, warp_sum, all_rows);
+  work *= a.Hk;
+  if (all_rows > a.T) {  // starts that run backwards: the requests overlap, and nothing is computed
+    if (tid == 0) {
+      if (a.err && atomicCAS(a.err, 0u, (unsigned)kDevErrLength) == 0u) a.err[2] = a.err[3] = a.err[4] = 0u;
+      a.counters[0] = a.counters[1] = a.counters[2] = 0;
+    }
+    return;
+  }
+  // 2. tiles a piece: a third of an even share, doubled until the partial results fit their space
+  long long cut = max((long long)a.g.min_tiles, (work + 3 * a.g.ctas - 1) / (3 * a.g.ctas));
+  long long slots, entries;
+  for (;; cut *= 2) {
+    long long s_carry = 0, e_carry = 0;
+    for (int c0 = 0; c0 < n; c0 += kPlanThreads) {
+      const int b = c0 + tid;
+      long long es = 0, ss = 0;
+      int4 r = {0, 0, 0, 0};
+      if (b < n) {
+        r = a.req[2 * b + 1];
+        // (y is the longest unit's tiles on the first pass, w its copy for the next)
+        const int longest = r.w ? r.w : max(r.y, 1);
+        const int pieces = (int)((longest + cut - 1) / cut);
+        r.w = longest;
+        r.z = pieces;
+        r.y = (longest + pieces - 1) / pieces;
+        es = (long long)a.Hk * r.x * pieces;
+        ss = pieces > 1 ? es : 0;
+      }
+      long long et, st;
+      const long long e0 = block_scan(es, warp_sum, et), s0 = block_scan(ss, warp_sum, st);
+      if (b < n) {
+        pre[b] = (int)(e_carry + e0);
+        a.req[2 * b + 1] = r;
+        // slot bases are kept beside the prefix until the cut is settled
+        pre[n + 1 + b] = (int)min(s_carry + s0, (long long)INT_MAX);
+      }
+      s_carry += st;
+      e_carry += et;
+    }
+    slots = s_carry;
+    entries = e_carry;
+    if (slots <= a.g.n_slots) break;
+  }
+  if (tid == 0) pre[n] = (int)entries;
+  __syncthreads();
+  // 3. the entries, pieces without keys left out (a unit without any key keeps one)
+  long long n_items = 0, n_merges = 0;
+  for (long long c0 = 0; c0 < entries; c0 += kPlanThreads) {
+    const long long e = c0 + tid;
+    bool keep = false, cuts = false;
+    SeqsItem it;
+    SeqsMerge mg;
+    if (e < entries) {
+      int lo = 0, hi = n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= e) lo = mid; else hi = mid;
+      }
+      const int4 r0 = a.req[2 * lo], r1 = a.req[2 * lo + 1];
+      const int nt = r1.x, pieces = r1.z, per = r1.y;
+      int x = (int)(e - pre[lo]);
+      const int t = nt - 1 - x % nt;
+      x /= nt;
+      const int s = x % pieces, h = x / pieces;
+      it.b = lo;
+      it.h = h;
+      it.nt = min(tq, r0.y - t * tq);
+      it.qrow0 = r0.x + t * tq;
+      it.pos0 = r0.z - r0.y + t * tq;
+      it.kv = r0.z;
+      it.krow0 = r0.w;
+      const TileRange u = unit_tiles(it.pos0, it.nt, it.kv, bk, a.causal, a.window);
+      const int tiles = u.e - u.a;
+      const int mine = max(1, (tiles + per - 1) / per);  // pieces of this unit
+      keep = s < mine;
+      it.key0 = (u.a + s * per) * bk;
+      it.key1 = tiles > 0 ? min((u.a + min((s + 1) * per, tiles)) * bk, u.hi) : it.key0;
+      const int slot0 = pre[n + 1 + lo] + h * pieces * nt + t;
+      it.slot = mine > 1 ? slot0 + s * nt : -1;
+      it.pad[0] = it.pad[1] = 0;
+      cuts = s == 0 && mine > 1;
+      mg.h = h;
+      mg.nt = it.nt;
+      mg.qrow0 = it.qrow0;
+      mg.slot0 = slot0;
+      mg.stride = nt;
+      mg.nseg = mine;
+      mg.pad[0] = mg.pad[1] = 0;
+    }
+    long long ki, mi;
+    const long long both = (keep ? 1ll : 0ll) | (cuts ? 1ll << 32 : 0ll);
+    long long sum;
+    const long long at = block_scan(both, warp_sum, sum);
+    ki = n_items + (at & 0xffffffffll);
+    mi = n_merges + (at >> 32);
+    if (keep) a.items[ki] = it;
+    if (cuts) a.merges[mi] = mg;
+    n_items += sum & 0xffffffffll;
+    n_merges += sum >> 32;
+  }
+  if (tid == 0) {
+    a.counters[0] = 0;
+    a.counters[1] = (unsigned)n_items;
+    a.counters[2] = (unsigned)n_merges;
+  }
+}
+
+// ---------------------------------------------------------------- merge of cut units
+struct MergeArgs {
+  const unsigned int *counters;
+  const SeqsMerge *merges;
+  const float *part_o;
+  const float2 *part_ml;
+  int slot_rows, group;
+  int64_t T;
+  float *lse;
+  View o;
+};
+
+template <typename E>
+__device__ __forceinline__ E to_out(float x);
+template <>
+__device__ __forceinline__ float to_out<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half to_out<__half>(float x) { return __float2half_rn(x); }
+
+// One warp a row: with piece s holding (o_s, m_s, l_s), M = max m_s and c_s = 2^(m_s - M),
+//   o = sum c_s o_s / sum c_s l_s,  lse = ln2 (M + log2 sum c_s l_s),
+// pieces taken in key order.  Bound by reading the partial results, which are still in L2.
+template <typename E, int D>
+__global__ void __launch_bounds__(256) seqs_merge_kernel(const MergeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int EPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const unsigned n_merges = a.counters[2];
+  const unsigned groups = (unsigned)(a.slot_rows + 7) / 8;
+  for (unsigned x = blockIdx.x; x < n_merges * groups; x += gridDim.x) {
+    const SeqsMerge m = a.merges[x / groups];
+    const int row = (int)(x % groups) * 8 + (threadIdx.x >> 5);
+    if (row >= m.nt * a.group) continue;
+    float M = -INFINITY;
+    for (int s = lane; s < m.nseg; s += 32)
+      M = fmaxf(M, a.part_ml[(int64_t)(m.slot0 + s * m.stride) * a.slot_rows + row].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float l = 0.f, o[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+    for (int s = 0; s < m.nseg; ++s) {
+      const int64_t at = (int64_t)(m.slot0 + s * m.stride) * a.slot_rows + row;
+      const float2 ml = a.part_ml[at];
+      const float c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      l = fmaf(ml.y, c, l);
+      const float *src = a.part_o + at * D + lane * EPL;
+      if constexpr (EPL == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        o[0] = fmaf(v.x, c, o[0]);
+        o[1] = fmaf(v.y, c, o[1]);
+        o[2] = fmaf(v.z, c, o[2]);
+        o[3] = fmaf(v.w, c, o[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        o[0] = fmaf(v.x, c, o[0]);
+        o[1] = fmaf(v.y, c, o[1]);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: zeros, lse = -inf
+    const int head = m.h * a.group + row % a.group;
+    const int64_t tok = m.qrow0 + row / a.group;
+    E *dst = reinterpret_cast<E *>(const_cast<void *>(a.o.ptr)) + head * a.o.sH + tok * a.o.sS + lane * EPL * a.o.sD;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) dst[e * a.o.sD] = to_out<E>(o[e] * inv);
+    if (a.lse && lane == 0) a.lse[head * a.T + tok] = l == 0.f ? -INFINITY : 0.69314718055994531f * (M + log2f(l));
+  }
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_t D) {
+  SeqsSpace s;
+  // a piece for every unit, and the pieces of cut units beyond their first
+  s.max_items = (T / g.tq + n) * Hk + g.n_slots;
+  size_t at = 0;
+  s.counters = at;
+  at += 256;
+  s.req = at;
+  at = up(at + (size_t)n * 32);
+  s.items = at;
+  at = up(at + (size_t)s.max_items * sizeof(SeqsItem));
+  s.merges = at;
+  at = up(at + (size_t)g.n_slots * sizeof(SeqsMerge));
+  s.part_ml = at;
+  at = up(at + (size_t)g.n_slots * (size_t)g.slot_rows * 8);
+  s.part_o = at;
+  at = up(at + (size_t)g.n_slots * (size_t)g.slot_rows * (size_t)D * 4);
+  s.total = at;
+  return s;
+}
+
+cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st) {
+  uint8_t *ws = static_cast<uint8_t *>(a.ws);
+  PlanArgs p;
+  p.cu_q = a.cu_q;
+  p.cu_k = a.cu_k;
+  p.kv_len = a.kv_len;
+  p.n = a.n;
+  p.T = a.q.S;
+  p.Tk = a.paged ? 0 : a.k.S;
+  p.cap_keys = a.paged ? a.table_width * a.k.S : 0;
+  if (p.cap_keys > ((int64_t)1 << 30)) p.cap_keys = (int64_t)1 << 30;
+  p.paged = a.paged;
+  p.Hk = (int)a.k.H;
+  p.causal = a.causal;
+  p.window = a.window;
+  p.g = g;
+  p.counters = reinterpret_cast<unsigned int *>(ws + s.counters);
+  p.req = reinterpret_cast<int4 *>(ws + s.req);
+  p.items = reinterpret_cast<SeqsItem *>(ws + s.items);
+  p.merges = reinterpret_cast<SeqsMerge *>(ws + s.merges);
+  p.err = a.err;
+  const size_t smem = (size_t)(2 * a.n + 2) * 4;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(seqs_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kMaxSeqs + 2) * 4);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  return launch_pdl(seqs_plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, p);
+}
+
+cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st) {
+  const uint8_t *ws = static_cast<const uint8_t *>(a.ws);
+  MergeArgs m;
+  m.counters = reinterpret_cast<const unsigned int *>(ws + s.counters);
+  m.merges = reinterpret_cast<const SeqsMerge *>(ws + s.merges);
+  m.part_o = reinterpret_cast<const float *>(ws + s.part_o);
+  m.part_ml = reinterpret_cast<const float2 *>(ws + s.part_ml);
+  m.slot_rows = g.slot_rows;
+  m.group = g.group;
+  m.T = a.q.S;
+  m.lse = a.lse;
+  m.o = a.o;
+  const dim3 grid((unsigned)current_device_sm_count() * 4), threads(256);
+  if (a.o.D == 128) {
+    if (a.o.dtype == FM_F32) return launch_pdl(seqs_merge_kernel<float, 128>, grid, threads, 0, st, m);
+    if (a.o.dtype == FM_BF16) return launch_pdl(seqs_merge_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, m);
+    return launch_pdl(seqs_merge_kernel<__half, 128>, grid, threads, 0, st, m);
+  }
+  if (a.o.dtype == FM_F32) return launch_pdl(seqs_merge_kernel<float, 64>, grid, threads, 0, st, m);
+  if (a.o.dtype == FM_BF16) return launch_pdl(seqs_merge_kernel<__nv_bfloat16, 64>, grid, threads, 0, st, m);
+  return launch_pdl(seqs_merge_kernel<__half, 64>, grid, threads, 0, st, m);
+}
+
+}  // namespace fm

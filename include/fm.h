@@ -53,9 +53,10 @@ extern "C" {
 /* Same type as cudaStream_t; NULL is the legacy default stream. */
 typedef struct CUstream_st *fm_stream_t;
 
-/* Element types.  Only FM_F32 and FM_BF16 are accepted: [PR477]'s commit message
+/* Element types.  The fixed-m calls accept only FM_F32 and FM_BF16: [PR477]'s commit message
  * rejects fp16 (and fp8) because 2^C-scale terms overflow their exponent range
- * (Q = K = 0, V = 1 gives inf instead of 1.0); here they fail with FM_ERR_DTYPE. */
+ * (Q = K = 0, V = 1 gives inf instead of 1.0); here they fail with FM_ERR_DTYPE.  The calls over
+ * requests of different lengths (end of this file) keep a running row max and take FM_F16 too. */
 enum { FM_F32 = 0, FM_BF16 = 1, FM_F16 = 2, FM_F8E4M3 = 3, FM_F8E5M2 = 4 };
 
 /* Return codes. */
@@ -68,7 +69,9 @@ enum {
   FM_ERR_BOUNDS_MISMATCH = 5, /* bounds do not belong to this call (see fm_attn_chunk) */
   FM_ERR_CUDA = 6,            /* a CUDA runtime call or kernel launch failed */
   FM_ERR_TIMEOUT = 7,         /* a kernel's pipeline wait ran past its limit */
-  FM_ERR_INDEX = 8            /* debug builds only (FM_DEBUG): a kernel's index check failed */
+  FM_ERR_INDEX = 8            /* fm_sync_status: an index in device memory was out of range (a page
+                                 table entry, a cache slot, request lengths), and in debug builds
+                                 (FM_DEBUG) a kernel's index check failed */
 };
 
 #define FM_BOUNDS_MAGIC 0x314D4246u /* tag written by fm_bounds ("FBM1") */
@@ -300,7 +303,8 @@ FM_API int fm_fold_sinks(const fm_tensor *q, fm_bounds_out *bounds, const fm_opt
 
 /* fm_sync_status -- synchronise `stream`, then report and clear this GPU's device
  * error word: FM_ERR_TIMEOUT if a kernel gave up on a pipeline wait (its outputs are
- * then invalid), FM_ERR_INDEX if a debug build's index check failed (the library built with
+ * then invalid), FM_ERR_INDEX if a paged call met a page table entry, slot or length outside its
+ * tensors or a debug build's index check failed (the library built with
  * -DFM_DEBUG: the chunk kernels check their epilogue accesses to the accumulators and o, skip
  * a failing one and record the first), FM_ERR_CUDA on an asynchronous CUDA error, else FM_OK. */
 FM_API int fm_sync_status(fm_stream_t stream);
@@ -318,7 +322,8 @@ FM_API int fm_probe_wait_timeout(unsigned int timeout_ms, fm_stream_t stream);
 FM_API const char *fm_last_error(void);
 
 /* ABI version of this header: (major << 16) | minor.  1.2 added fm_opts.schedule,
- * fm_bounds_out.next_key_offset and the ring bounds calls. */
+ * fm_bounds_out.next_key_offset and the ring bounds calls; 1.3 the calls over requests of
+ * different lengths and the paged cache. */
 FM_API int fm_version(void);
 
 /* ---- The bounds of a ring of ranks ---------------------------------------------------------
@@ -431,6 +436,111 @@ FM_API int fm_attention_host(const fm_tensor *q_host, const fm_tensor *k_host, c
  * than FM_NOALLOC_SCRATCH_BYTES (nothing is enqueued then). */
 FM_API int fm_bounds_noalloc(const fm_tensor *q, const fm_tensor *k_full, const fm_tensor *v_full,
                              const fm_opts *opts, fm_bounds_out *out, fm_stream_t stream);
+
+/* ---- Requests of different lengths, and a paged key/value cache ------------------------------
+ * Attention for serving causal models: n requests, each with its own number of queries and keys,
+ * in one call.  Not fixed-m (the pages' bound is per dense call): every row keeps a running max.
+ *   - Packed tensors hold every request's rows one after another: [1, H, T, D], request i owning
+ *     rows cu[i] .. cu[i+1]-1 (cu int32 [n+1], cu[0] = 0, ascending).  Rows behind the last
+ *     request are neither read nor written.
+ *   - A paged cache is [num_pages, H, page_size, D]; position p of request i lies in page
+ *     block_table[i][p / page_size], row p % page_size.  Table entries past a request's last key
+ *     are not read.  Any strides; a page is shared by requests when their tables say so.
+ *   - Query heads share key heads: head h reads key head h / (Hq / Hk); Hq a multiple of Hk, at
+ *     most FM_MAX_GROUP to one.
+ *   - With q_i queries and s_i keys, query t of request i stands at position p = s_i - q_i + t.
+ *     causal: it sees keys j <= p; window > 0 (needs causal): only j > p - window.  A row that sees
+ *     no key gets o = 0 and lse = -inf.
+ *   - FM_F32, FM_BF16 or FM_F16, one type for q, k, v; sums, the row max and the normalise are fp32;
+ *     for 16-bit inputs the weights p are rounded to that type before they meet v.
+ *   - Keys and values past a request's end (the rest of its last page, its neighbours' rows) may
+ *     hold anything, NaN too: they change nothing.  A value row that some query of the request
+ *     sees must be finite: a NaN or infinity there may reach that request's other rows.
+ *   - All lengths are read on the device: nothing waits for them, calls can be captured into a
+ *     graph and replayed with other lengths (the first call on a device comes before any
+ *     capture).  Lengths that do not fit the tensors are clamped, a table entry outside
+ *     [0, num_pages) reads as zeros, and the next fm_sync_status returns FM_ERR_INDEX.
+ *   - The workspace is scratch: its contents need no preparation and mean nothing afterwards.  Calls
+ *     that may run at the same time need one each. */
+#define FM_MAX_GROUP 64
+#define FM_MAX_SEQS 8192
+
+typedef struct {
+  float softmax_scale; /* <= 0 selects 1/sqrt(D) */
+  int32_t causal;      /* 1 or 0 */
+  int32_t window;      /* 0: none */
+} fm_seqs_opts;
+
+/* Device arrays of one attention call (host struct). */
+typedef struct {
+  int64_t n_seqs;             /* 0 .. FM_MAX_SEQS */
+  const int32_t *cu_q;        /* [n+1] */
+  const int32_t *cu_k;        /* [n+1], fm_attn_varlen */
+  const int32_t *kv_len;      /* [n] keys of each request with its new tokens, fm_attn_paged */
+  const int32_t *block_table; /* [n] rows of table_width entries, table_stride apart, fm_attn_paged */
+  int64_t table_stride, table_width;
+} fm_seqs;
+
+/* Scratch bytes of fm_attn_varlen / fm_attn_paged for n requests, T packed query rows and the given
+ * heads.  Never less for more requests or rows. */
+FM_API int fm_attn_seqs_workspace_size(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hk, int64_t D, size_t *bytes);
+
+/* fm_attn_varlen -- attention over packed keys: whole prompts of different lengths.
+ *   q [1, Hq, T, D];  k, v [1, Hk, Tk, D];  seqs: n_seqs, cu_q, cu_k
+ *   o_out [1, Hq, T, D], q's type or FM_F32;  lse f32 [Hq, T] contiguous or NULL (natural log)
+ *   workspace of fm_attn_seqs_workspace_size bytes, 16-byte aligned
+ * Deterministic: the same call gives the same bits.  Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE,
+ * FM_ERR_UNSUPPORTED (D not 64 or 128, too many heads to a key head, requests or rows), FM_ERR_CUDA. */
+FM_API int fm_attn_varlen(const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
+                          const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace,
+                          size_t workspace_bytes, fm_stream_t stream);
+
+/* fm_attn_paged -- the same over a paged cache that already holds the new tokens' keys and values:
+ * one query a request (decoding), chunks of a prompt, or both in one call.
+ *   k_cache, v_cache [num_pages, Hk, page_size, D];  seqs: n_seqs, cu_q, kv_len, block_table */
+FM_API int fm_attn_paged(const fm_tensor *q, const fm_tensor *k_cache, const fm_tensor *v_cache, const fm_seqs *seqs,
+                         const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace,
+                         size_t workspace_bytes, fm_stream_t stream);
+
+/* The state of a paged cache's bookkeeping (host struct of device arrays). */
+typedef struct {
+  int64_t n_seqs, page_size, num_pages;
+  int32_t *block_table; /* [n] rows of table_width entries, table_stride apart */
+  int64_t table_stride, table_width;
+  int32_t *free_pages;       /* [num_pages]: the free pages are its first free_count entries */
+  const int32_t *free_count; /* [1] */
+  int32_t *free_count_out;   /* [1], may be free_count */
+  const int32_t *kv_len;     /* [n] tokens that each request holds */
+  int32_t *kv_len_out;       /* [n], may be kv_len */
+} fm_page_state;
+
+/* fm_paged_extend -- room for the next tokens of every request, in one launch.
+ *   new_len   int32 [n]  tokens to come (0: none)
+ *   release   uint8 [n] or NULL: 1 = the request that held row i has ended: its pages go back to
+ *             the list first, and new_len[i] tokens begin a new request in that row
+ *   max_tokens  length of slots and positions
+ *   cu_q      int32 [n+1] written: prefix sums of new_len
+ *   slots     int64 [max_tokens] written: page * page_size + row of each new token, in request
+ *             order, -1 behind the last
+ *   positions int32 [max_tokens] written: its position in its request, -1 behind the last
+ *   status    int32 [1] written: 0, or the number of pages that the list is short of, or -1 (a
+ *             negative length, lengths that the table row, max_tokens or 31 bits do not hold, a
+ *             free_count outside the list).  Unless 0 the call changes nothing: lengths, count,
+ *             table and list stay, cu_q is all 0 and slots and positions all -1, so that the
+ *             cache write and the attention that follow do nothing.
+ * Pages given back are put on the list's end in request and table order; new pages are taken from
+ * its end.  Errors: FM_ERR_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+FM_API int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const uint8_t *release,
+                           int64_t max_tokens, int32_t *cu_q, int64_t *slots, int32_t *positions, int32_t *status,
+                           fm_stream_t stream);
+
+/* fm_paged_write -- k and v rows [1, H, T, D] put at their slots of the caches [num_pages, H,
+ * page_size, D] (one dtype, any strides).  slots int64 [T]: a negative one skips its row, one past the
+ * cache is skipped and reported by fm_sync_status (FM_ERR_INDEX).  Slots are distinct (of rows with
+ * one slot, either may remain in each piece).  Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE,
+ * FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+FM_API int fm_paged_write(const fm_tensor *k, const fm_tensor *v, const int64_t *slots, const fm_tensor *k_cache,
+                          const fm_tensor *v_cache, fm_stream_t stream);
 
 #ifdef __cplusplus
 }
