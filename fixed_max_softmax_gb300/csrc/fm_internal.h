@@ -208,6 +208,9 @@ SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_
 // Work list of the call into its workspace; then one of the attention kernels; then the merge.
 cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 cudaError_t launch_seqs_simt(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+bool seqs_tc_supported(const SeqsArgs &a);
+// cudaErrorNotSupported, launching nothing, when the tensor maps cannot be encoded.
+cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 
 struct PagedExtendArgs {

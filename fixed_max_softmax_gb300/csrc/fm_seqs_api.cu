@@ -47,7 +47,8 @@ int check_group(int64_t Hq, int64_t Hk) {
 size_t space_bytes(int64_t n, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
   const int group = (int)(Hq / Hk);
   const size_t simt = seqs_space(seqs_geom_simt(T, group), n, T, Hk, D).total;
-  return simt;
+  const size_t tc = seqs_space(seqs_geom_tc(T, n, group), n, T, Hk, D).total;
+  return simt > tc ? simt : tc;
 }
 
 // The call behind fm_attn_varlen and fm_attn_paged.
@@ -115,11 +116,19 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   a.timeout_ns = wait_timeout_ns();
   if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const SeqsGeom g = seqs_geom_simt(a.q.S, group);
-  const SeqsSpace s = seqs_space(g, a.n, a.q.S, a.k.H, a.q.D);
-  cudaError_t e = launch_seqs_plan(a, g, s, st);
-  if (e == cudaSuccess) e = launch_seqs_simt(a, g, s, st);
-  if (e == cudaSuccess) e = launch_seqs_merge(a, g, s, st);
+  // the work list, the attention, the merge of what was cut
+  auto run = [&](const SeqsGeom &g, cudaError_t (*attend)(const SeqsArgs &, const SeqsGeom &, const SeqsSpace &, cudaStream_t)) {
+    const SeqsSpace s = seqs_space(g, a.n, a.q.S, a.k.H, a.q.D);
+    cudaError_t e = launch_seqs_plan(a, g, s, st);
+    if (e == cudaSuccess) e = attend(a, g, s, st);
+    if (e == cudaSuccess) e = launch_seqs_merge(a, g, s, st);
+    return e;
+  };
+  cudaError_t e = cudaErrorNotSupported;
+  if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group), launch_seqs_tc);
+  // fp32, and layouts that the tensor-core kernel or the tensor-map encoder does not take (a work
+  // list made for it then goes unused)
+  if (e == cudaErrorNotSupported) e = run(seqs_geom_simt(a.q.S, group), launch_seqs_simt);
   if (e != cudaSuccess) return cuda_fail(e, paged ? "fm_attn_paged launch" : "fm_attn_varlen launch");
   return FM_OK;
 }

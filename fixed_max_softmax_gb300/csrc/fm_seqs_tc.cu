@@ -1,0 +1,622 @@
+// fm_seqs_tc.cu -- attention over requests of different lengths on the tensor cores (sm_103a):
+// packed prompts, chunks over a paged cache, and decoding, for bf16 and fp16, D = 64 or 128.
+//
+//   S = Q K^T   tcgen05.mma, Q and K from swizzled shared memory (TMA), fp32 in tensor memory
+//   P           online softmax of the rows (running max, rescaled lazily), rounded to 16 bits
+//               over S in tensor memory; sums in fp32 registers
+//   O += P V    tcgen05.mma, P from tensor memory, V from shared memory
+//
+// Rows.  A tile's 128 rows are floor(128 / G) tokens x the G query heads of one key head, token by
+// token, so that the heads that share a key head read it once and a decoding request fills G rows
+// with one pass over its keys.  One 3-D TMA box {64, G, tokens} per 64 columns gathers a tile.
+// Keys.  A tile's 128 keys are one TMA box per 64 columns (packed, or pages of 128 keys and more)
+// or 128 / page_size boxes, one lane of the producer warp a box; pages past the request's end are
+// asked for at a page that does not exist, which TMA fills with zeros.
+// Work.  A CTA a SM takes pieces from the list in order (a counter).  A piece is a unit of queries
+// -- two row tiles, or one when its tokens fit one (decoding, the rest of a chunk) -- against a
+// range of keys.  The tensor core always alternates between two softmax groups of four warps:
+//   two row tiles   group g has row tile g, both against the same key tile
+//   one row tile    group g has the key tiles of parity g, with an O and a max of its own, joined
+//                   at the end: a decoding request's tiles go through both groups at once
+// MMA order for step s of a piece (group s mod 2):  S(s), P V(s - 1): one group's softmax runs
+// under the other's two MMAs.
+// 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM; it zeroes the V rows past the request's end,
+// which meet p = 0 but may hold NaN), 2 Q loads, 3 fetches work, 4-7 and 8-11 softmax.
+// TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
+// Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include <mutex>
+
+#include "fm_seqs.cuh"
+#include "fm_tc.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kPanel = 128 * 128;  // 128 rows of 64 16-bit columns: one 128-byte swizzle span
+
+template <typename E, int D>
+struct Cfg {
+  static constexpr int PN = D / 64;          // panels of a tile
+  static constexpr int kTile = PN * kPanel;  // bytes
+  static constexpr int NS = 10 / PN;         // K/V ring: 160 KiB
+  static constexpr int offQ = 0;
+  static constexpr int offKV = 2 * kTile;
+  static constexpr int offStat = offKV + NS * kTile;  // (max, sum) of group 1's rows
+  static constexpr int offItems = offStat + 128 * 8;
+  static constexpr int offBar = offItems + 2 * (int)sizeof(SeqsItem);
+  // barriers
+  static constexpr int QFull = 0, QEmpty = 2, SFull = 3, PReady = 5, ODone = 7, Drain = 9, ItemFull = 10, ItemEmpty = 12,
+                       Stat = 14, EpiDone = 15, KVFull = 16, KVEmpty = KVFull + NS, kBars = KVEmpty + NS;
+  static constexpr int offTmem = offBar + kBars * 8;
+  static constexpr int offAbort = offTmem + 8;
+  static constexpr int kSmem = offAbort + 8 + 1024;  // slack for aligning the base
+  static_assert(kSmem <= 232448, "shared memory of an SM");
+  static constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
+  static constexpr uint32_t idescQK = idesc_f16(128, 128, false, bf16);  // K [keys, D]: K-major
+  static constexpr uint32_t idescPV = idesc_f16(128, D, true, bf16);     // V [keys, D]: MN-major
+};
+constexpr int kItemReaders = 11;  // arrivals that free an item slot: warps 0, 1, 2 and the 8 softmax warps
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+struct Params {
+  int group, tq1;  // heads of a key head, tokens of a row tile
+  int causal, window;
+  float alpha;
+  int paged, ps, box_rows, num_pages;
+  const int32_t *table;
+  int64_t table_stride;
+  unsigned int *counters;
+  const SeqsItem *items;
+  float *part_o;
+  float2 *part_ml;
+  int slot_rows;
+  void *out;
+  int out_f32;
+  int64_t osH, osS;
+  float *lse;
+  int64_t T;
+  unsigned int *err;
+  unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Scores outside [lo, hi) of the row's keys become -inf; kb is the tile's first key, and the
+// warp's rows all see [max_lo, min_hi), so that column blocks inside it are left alone.
+__device__ __noinline__ void mask_rows(uint32_t tS, int kb, int lo, int hi, int max_lo, int min_hi) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int k0 = kb + 32 * c;
+    if (k0 >= max_lo && k0 + 32 <= min_hi) continue;
+    uint32_t s[32];
+    tmem_ld32(tS + 32 * c, s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (k0 + e < lo || k0 + e >= hi) s[e] = 0xff800000u;  // -inf
+    tmem_st32(tS + 32 * c, s);
+  }
+  tmem_st_wait();
+}
+
+// 32 columns of one row to memory: 16-bit elements or fp32, 16-byte stores.
+template <typename E>
+__device__ __forceinline__ void store32(void *dst, bool f32, const float (&x)[32]) {
+  uint4 *p = reinterpret_cast<uint4 *>(dst);
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                        __float_as_uint(x[4 * i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = make_uint4(pack_half<E>(x[8 * i], x[8 * i + 1]), pack_half<E>(x[8 * i + 2], x[8 * i + 3]),
+                        pack_half<E>(x[8 * i + 4], x[8 * i + 5]), pack_half<E>(x[8 * i + 6], x[8 * i + 7]));
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    seqs_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  using C = Cfg<E, D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *gbase = smem_raw + (base - raw);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + C::offAbort);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + C::offTmem);
+  SeqsItem *item_ring = reinterpret_cast<SeqsItem *>(gbase + C::offItems);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return base + (uint32_t)(C::offBar + 8 * i); };
+  auto wait = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
+    return wait_phase(bar(i), parity, abort_flag, p.timeout_ns, p.err, code, wtag(i, tag));
+  };
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C::kBars; ++i) {
+      const int count = (i == C::PReady || i == C::PReady + 1 || i == C::Stat || i == C::EpiDone) ? 128
+                        : (i == C::ItemEmpty || i == C::ItemEmpty + 1)                            ? kItemReaders
+                                                                                                  : 1;
+      mbar_init(bar(i), count);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the work list, and whatever the caller's earlier kernels wrote
+  pdl_trigger();
+
+  // The k-th piece of this CTA, read by every lane of the calling warp from the two-slot ring.
+  // False when there is none left (or a wait gave up: ok says which).
+  auto next_item = [&](uint32_t k, unsigned code, bool &ok, SeqsItem &it) -> bool {
+    const int slot = (int)(k & 1u);
+    ok = wait(C::ItemFull + slot, (k >> 1) & 1u, code, (int)k);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it = item_ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::ItemEmpty + slot));
+    return it.b >= 0;
+  };
+  auto tiles_of = [](const SeqsItem &it) { return it.key1 > it.key0 ? (it.key1 - it.key0 + 127) >> 7 : 0; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K/V producer
+    const int boxes = 128 / p.box_rows * C::PN;  // of one tile; this lane's: panel pn of page pg
+    const int pn = lane % C::PN, pg = lane / C::PN;
+    uint32_t n = 0;  // tiles loaded into the ring so far
+    bool ok = true;
+    SeqsItem it;
+    for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutProducer, ok, it); ++k) {
+      const int tiles = tiles_of(it);
+      // coordinates of this lane's box: row and page (packed: row of the tensor, batch 0)
+      auto coords = [&](int kb, int &row, int &page) {
+        if (!p.paged) {
+          row = it.krow0 + kb;
+          page = 0;
+          return;
+        }
+        const int key = kb + pg * p.box_rows;
+        row = p.ps > 128 ? key % p.ps : 0;
+        page = p.num_pages;  // past the end: zeros
+        if (lane < boxes && key < it.kv) {
+          const int at = key / p.ps;
+          page = p.table[it.b * p.table_stride + at];
+          if (page < 0 || page >= p.num_pages) {
+            if (pn == 0) report_bad_page(p.err, it.b, at, page);
+            page = p.num_pages;
+          }
+        }
+      };
+      int row, page;
+      if (tiles > 0) coords(it.key0, row, page);
+      for (int j = 0; j < tiles && ok; ++j) {
+        int row_next = 0, page_next = 0;  // the next tile's table entry, asked for a tile ahead
+        if (j + 1 < tiles) coords(it.key0 + (j + 1) * 128, row_next, page_next);
+        for (int w = 0; w < 2 && ok; ++w, ++n) {
+          const int st = (int)(n % C::NS);
+          ok = wait(C::KVEmpty + st, ((n / C::NS) & 1u) ^ 1u, kDevErrTimeoutProducer, j);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(bar(C::KVFull + st), C::kTile);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_4d(base + C::offKV + st * C::kTile + pn * kPanel + pg * p.box_rows * 128, w ? &maps.v : &maps.k,
+                        bar(C::KVFull + st), pn * 64, row, it.h, page);
+        }
+        row = row_next;
+        page = page_next;
+      }
+    }
+    if (!ok) {
+      // every copy already issued lands before the CTA can exit: the last NS loads cover the rest
+      for (uint32_t i = n > C::NS ? n - C::NS : 0; i < n; ++i)
+        wait_phase(bar(C::KVFull + (int)(i % C::NS)), (i / C::NS) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain,
+                   wtag(C::KVFull, 0));
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ Q loads
+    const uint32_t q_bytes = (uint32_t)(C::PN * p.group * p.tq1 * 128);
+    uint32_t loads = 0, loads1 = 0;
+    bool ok = true;
+    SeqsItem it;
+    for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutProducer, ok, it); ++k) {
+      const int tiles = tiles_of(it);
+      if (tiles == 0) continue;
+      if (loads > 0) ok = wait(C::QEmpty, (loads - 1) & 1u, kDevErrTimeoutProducer, (int)k);  // the last piece's S MMAs
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int nq = it.nt > p.tq1 ? 2 : 1;
+      if (lane == 0) {
+        for (int t = 0; t < nq; ++t) {
+          mbar_expect_tx(bar(C::QFull + t), q_bytes);
+          for (int pn = 0; pn < C::PN; ++pn)
+            tma_load_3d(base + C::offQ + t * C::kTile + pn * kPanel, &maps.q, bar(C::QFull + t), pn * 64, it.h * p.group,
+                        it.qrow0 + t * p.tq1);
+        }
+      }
+      ++loads;
+      loads1 += nq - 1;
+    }
+    if (!ok) {
+      if (loads > 0)
+        wait_phase(bar(C::QFull), (loads - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain, wtag(C::QFull, 0));
+      if (loads1 > 0)
+        wait_phase(bar(C::QFull + 1), (loads1 - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain,
+                   wtag(C::QFull + 1, 0));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    auto q_desc = [&](int t, int kk) {
+      return smem_desc(base + C::offQ + t * C::kTile + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024);
+    };
+    auto k_desc = [&](int s, int kk) {
+      return smem_desc(base + C::offKV + s * C::kTile + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024);
+    };
+    auto v_desc = [&](int s, int kk) { return smem_desc(base + C::offKV + s * C::kTile + kk * 2048, kPanel, 1024); };
+    uint32_t n = 0;                  // ring tiles of earlier pieces
+    uint32_t loads = 0, loads1 = 0;  // Q tiles 0 and 1 used
+    uint32_t steps[2] = {0, 0};      // softmax steps of each group in earlier pieces
+    bool ok = true;
+    SeqsItem it;
+    for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutMma, ok, it); ++k) {
+      const int tiles = tiles_of(it);
+      if (tiles == 0) continue;
+      const bool dual = it.nt > p.tq1;
+      const int nsub = dual ? 2 * tiles : tiles;
+      const int valid = it.kv - (it.key0 + (tiles - 1) * 128);  // rows of the last tile that are the request's
+      ok = wait(C::QFull, loads & 1u, kDevErrTimeoutMma, (int)k);
+      // P V of step s: V has landed, the group's P is ready
+      auto pv = [&](int s) -> bool {
+        const int g = s & 1, kt = dual ? s >> 1 : s;
+        const uint32_t v = n + 2 * kt + 1;
+        const int st = (int)(v % C::NS);
+        if (!dual || g == 0) {
+          if (!__all_sync(0xffffffffu, wait(C::KVFull + st, (v / C::NS) & 1u, kDevErrTimeoutMma, kt))) return false;
+          if (kt == tiles - 1 && valid < 128) {
+            uint8_t *tile = gbase + C::offKV + st * C::kTile;
+            for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
+#pragma unroll
+              for (int pn = 0; pn < C::PN; ++pn)
+                *reinterpret_cast<uint4 *>(tile + pn * kPanel + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!__all_sync(0xffffffffu, wait(C::PReady + g, (steps[g] + (uint32_t)(s >> 1)) & 1u, kDevErrTimeoutMma, s)))
+          return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + 256 + g * 128, tmem + g * 128 + kk * 8, v_desc(st, kk), C::idescPV, (s >= 2 || kk > 0));
+          if (!dual || g == 1) mma_commit(bar(C::KVEmpty + st));
+          if (s + 2 >= nsub) mma_commit(bar(C::ODone + g));
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int s = 0; s < nsub && ok; ++s) {
+        const int g = s & 1, kt = dual ? s >> 1 : s, qt = dual ? g : 0;
+        const uint32_t kx = n + 2 * kt;
+        const int st = (int)(kx % C::NS);
+        if (!dual || g == 0) ok = wait(C::KVFull + st, (kx / C::NS) & 1u, kDevErrTimeoutMma, kt);
+        if (ok && dual && s == 1) ok = wait(C::QFull + 1, loads1 & 1u, kDevErrTimeoutMma, (int)k);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + g * 128, q_desc(qt, kk), k_desc(st, kk), C::idescQK, kk > 0);
+          mma_commit(bar(C::SFull + g));
+          if (!dual || g == 1) mma_commit(bar(C::KVEmpty + st));
+          if (s == nsub - 1) mma_commit(bar(C::QEmpty));
+        }
+        __syncwarp();
+        if (s > 0) ok = pv(s - 1);
+      }
+      if (ok) ok = pv(nsub - 1);
+      n += 2 * tiles;
+      ++loads;
+      loads1 += dual ? 1 : 0;
+      steps[0] += (uint32_t)((nsub + 1) >> 1);
+      steps[1] += (uint32_t)(nsub >> 1);
+    }
+    if (!ok && lane == 0) {
+      // every MMA issued so far must finish reading shared memory and TMEM before exit
+      mma_commit(bar(C::Drain));
+      wait_phase(bar(C::Drain), 0, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain, wtag(C::Drain, 0));
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ work
+    if (lane == 0) {
+      const unsigned n_items = p.counters[1];
+      bool more = true;
+      for (uint32_t k = 0; more; ++k) {
+        const unsigned e = atomicAdd(&p.counters[0], 1u);
+        SeqsItem it;
+        more = e < n_items;
+        if (more) it = p.items[e];
+        else it.b = -1;
+        const int slot = (int)(k & 1u);
+        if (!wait(C::ItemEmpty + slot, ((k >> 1) & 1u) ^ 1u, kDevErrTimeoutProducer, (int)k)) break;
+        item_ring[slot] = it;
+        mbar_arrive(bar(C::ItemFull + slot));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax groups
+    const int g = (warp - 4) >> 2;  // group
+    const int wq = warp & 3;        // TMEM lane quarter of this warp
+    const int r = wq * 32 + lane;   // row of the tile
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + (uint32_t)(g * 128);
+    const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(g * 128);
+    float2 *stat = reinterpret_cast<float2 *>(gbase + C::offStat);
+    const int tok = r / p.group, hd = r - tok * p.group;              // this row's token and head
+    const int tok0 = (wq * 32) / p.group, tok1 = (wq * 32 + 31) / p.group;  // tokens of the warp's rows
+    const bool row_used = tok < p.tq1;
+    uint32_t steps = 0, pieces[2] = {0, 0}, singles = 0;  // phases: S steps, O-done of both groups, Stat / EpiDone
+    bool ok = true;
+    SeqsItem it;
+    for (uint32_t k = 0; next_item(k, kDevErrTimeoutSoftmax, ok, it); ++k) {
+      const int tiles = tiles_of(it);
+      const bool dual = it.nt > p.tq1;
+      const int nsub = dual ? 2 * tiles : tiles;
+      const int mine = (nsub - g + 1) >> 1;  // steps of this group
+      const int first_tok = dual ? g * p.tq1 : 0;
+      const int left = min(p.tq1, it.nt - first_tok);  // tokens of this group's row tile
+      const bool active = tok0 < left;                 // some row of this warp is a token's
+      const bool row_ok = row_used && tok < left;
+      const int pos = it.pos0 + first_tok + tok;
+      int lo = 0, hi = 0;
+      if (row_ok) seen_keys(pos, it.kv, p.causal, p.window, lo, hi);
+      // what every (used) row of the warp sees, for the tiles that need no mask
+      int max_lo, min_hi, unused;
+      seen_keys(it.pos0 + first_tok + min(tok1, left - 1), it.kv, p.causal, p.window, max_lo, unused);
+      seen_keys(it.pos0 + first_tok + tok0, it.kv, p.causal, p.window, unused, min_hi);
+      float run = -INFINITY;
+      float l[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < mine; ++i) {
+        ok = ok && wait(C::SFull + g, (steps + (uint32_t)i) & 1u, kDevErrTimeoutSoftmax, i);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          const int kb = it.key0 + (dual ? i : 2 * i + g) * 128;
+          if (kb < max_lo || kb + 128 > min_hi) mask_rows(tS, kb, lo, hi, max_lo, min_hi);
+          softmax_online_tile<E, D>(tS, tO, p.alpha, i > 0, run, l);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(C::PReady + g));
+      }
+      steps += (uint32_t)mine;
+      float lsum = (l[0] + l[1]) + (l[2] + l[3]);
+      // what the sums carry: 2^(bias - run) (see p_bias)
+      if (!dual && g == 1) {
+        // the other group joins the two results: it needs this group's max and sums, and O1 until
+        // it says that it has read it
+        stat[r] = make_float2(run, lsum);
+        mbar_arrive(bar(C::Stat));
+        ok = ok && wait(C::EpiDone, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        pieces[0] += nsub > 0;
+        pieces[1] += nsub > 1;
+        ++singles;
+        continue;
+      }
+      float c0 = 1.f, c1 = 0.f;
+      if (mine > 0) ok = ok && wait(C::ODone + g, pieces[g] & 1u, kDevErrTimeoutSoftmax, (int)k);
+      if (!dual) {
+        // (group 1's arrival also says that it has seen O1 of its earlier pieces done, so that the
+        // phase waited for next is the one after those)
+        ok = ok && wait(C::Stat, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
+        if (nsub > 1) ok = ok && wait(C::ODone + 1, pieces[1] & 1u, kDevErrTimeoutSoftmax, (int)k);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      pieces[0] += nsub > 0;
+      pieces[1] += nsub > 1;
+      if (!dual) {
+        const float2 o = stat[r];
+        const float m = fmaxf(run, o.x);
+        c0 = run == -INFINITY ? 0.f : ex2(run - m);
+        c1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
+        lsum = lsum * c0 + o.y * c1;
+        run = m;
+        ++singles;
+      }
+      if (active) {
+        const bool whole = it.slot < 0;
+        const float inv = !whole ? 1.f : (lsum == 0.f ? 0.f : 1.0f / lsum);  // no key seen: zeros, lse = -inf
+        const float s0 = c0 * inv, s1 = c1 * inv;
+        const int64_t qrow = (int64_t)it.qrow0 + first_tok + tok;
+        const int head = it.h * p.group + hd;
+        const int64_t slot_row = (int64_t)it.slot * p.slot_rows + (first_tok + tok) * p.group + hd;
+        const bool f32 = !whole || p.out_f32;
+        uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) + (head * p.osH + qrow * p.osS) * (p.out_f32 ? 4 : 2)
+                             : reinterpret_cast<uint8_t *>(p.part_o + slot_row * D);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float x[32];
+          if (mine > 0) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = c0 == 0.f ? 0.f : __uint_as_float(o[e]) * s0;
+            if (!dual && nsub > 1) {
+              tmem_ld32(tO + 128 + c * 32, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = c1 == 0.f ? x[e] : fmaf(__uint_as_float(o[e]), s1, x[e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          }
+          if (row_ok) store32<E>(dst + c * 32 * (f32 ? 4 : 2), f32, x);
+        }
+        if (row_ok) {
+          // acc = sum 2^(z - run + bias): the bias leaves o as it is and comes off the log
+          const float mx = run == -INFINITY ? run : run - p_bias<E>();
+          if (!whole) p.part_ml[slot_row] = make_float2(mx, lsum);
+          else if (p.lse)
+            p.lse[head * p.T + qrow] = lsum == 0.f ? -INFINITY : 0.69314718055994531f * (mx + log2f(lsum));
+        }
+      }
+      if (!dual) {
+        tc_fence_before();
+        mbar_arrive(bar(C::EpiDone));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+bool encode(CUtensorMap *map, const View &t, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return enc(map, t.dtype == FM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+             const_cast<void *>(t.ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Byte stride of a dimension; one of size 1 is never stepped and gets a well-formed value.
+cuuint64_t step(int64_t s, int64_t n, int64_t other) { return (cuuint64_t)(n > 1 ? s : other) * 2; }
+
+// q [1, Hq, T, D] as (D, Hq, T), box {64, group, tokens}.
+bool encode_q(CUtensorMap *map, const View &t, int group, int tq1) {
+  const cuuint64_t dims[3] = {(cuuint64_t)t.D, (cuuint64_t)t.H, (cuuint64_t)t.S};
+  const cuuint64_t strides[2] = {step(t.sH, t.H, t.D), step(t.sS, t.S, t.H * t.D)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tq1};
+  return encode(map, t, 3, dims, strides, box);
+}
+// k or v [B, Hk, S, D] (pages, or one batch of packed rows) as (D, S, Hk, B), box {64, rows, 1, 1}.
+bool encode_kv(CUtensorMap *map, const View &t, int rows) {
+  const cuuint64_t dims[4] = {(cuuint64_t)t.D, (cuuint64_t)t.S, (cuuint64_t)t.H, (cuuint64_t)t.B};
+  const cuuint64_t strides[3] = {step(t.sS, t.S, t.D), step(t.sH, t.H, t.S * t.D), step(t.sB, t.B, t.H * t.S * t.D)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  return encode(map, t, 4, dims, strides, box);
+}
+
+bool rows16(const View &x, int64_t es) {
+  auto ok = [&](int64_t s, int64_t n) { return n <= 1 || (s > 0 && (s * es) % 16 == 0 && s * es < ((int64_t)1 << 40)); };
+  return x.sD == 1 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && ok(x.sS, x.S) && ok(x.sH, x.H) && ok(x.sB, x.B);
+}
+
+template <typename E, int D>
+cudaError_t launch_typed(const Maps &maps, const Params &p, cudaStream_t st) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(seqs_tc_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<E, D>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  return launch_pdl(seqs_tc_kernel<E, D>, dim3((unsigned)current_device_sm_count()), dim3(kThreads), Cfg<E, D>::kSmem, st,
+                    maps, p);
+}
+
+}  // namespace
+
+// The tensor-core kernel takes 16-bit types whose rows a tensor map describes, and pages that
+// divide its key tiles or are made of them.
+bool seqs_tc_supported(const SeqsArgs &a) {
+  if (a.q.dtype == FM_F32) return false;
+  if (a.k.S < 1 || a.k.B < 1) return false;
+  const int64_t ps = a.k.S;
+  if (a.paged && !(ps == 8 || ps == 16 || ps == 32 || ps == 64 || ps % 128 == 0)) return false;
+  return rows16(a.q, 2) && rows16(a.k, 2) && rows16(a.v, 2) && rows16(a.o, a.o.dtype == FM_F32 ? 4 : 2);
+}
+
+SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
+  SeqsGeom g;
+  g.group = group;
+  g.tq = 2 * (128 / group);
+  g.bk = 128;
+  g.slot_rows = (int)(g.tq < T ? g.tq : T) * group;
+  g.ctas = current_device_sm_count();
+  g.n_slots = 8 * g.ctas;
+  g.min_tiles = 4;
+  return g;
+}
+
+cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st) {
+  uint8_t *ws = static_cast<uint8_t *>(a.ws);
+  Maps maps;
+  memset(&maps, 0, sizeof maps);
+  Params p;
+  p.group = g.group;
+  p.tq1 = g.tq / 2;
+  p.box_rows = a.paged && a.k.S < 128 ? (int)a.k.S : 128;
+  if (!encode_q(&maps.q, a.q, p.group, p.tq1) || !encode_kv(&maps.k, a.k, p.box_rows) ||
+      !encode_kv(&maps.v, a.v, p.box_rows))
+    return cudaErrorNotSupported;
+  p.causal = a.causal;
+  p.window = a.window;
+  p.alpha = a.alpha;
+  p.paged = a.paged;
+  p.ps = a.paged ? (int)a.k.S : 1;
+  p.num_pages = a.paged ? (int)a.k.B : 0;
+  p.table = a.table;
+  p.table_stride = a.table_stride;
+  p.counters = reinterpret_cast<unsigned int *>(ws + s.counters);
+  p.items = reinterpret_cast<const SeqsItem *>(ws + s.items);
+  p.part_o = reinterpret_cast<float *>(ws + s.part_o);
+  p.part_ml = reinterpret_cast<float2 *>(ws + s.part_ml);
+  p.slot_rows = g.slot_rows;
+  p.out = const_cast<void *>(a.o.ptr);
+  p.out_f32 = a.o.dtype == FM_F32;
+  p.osH = a.o.sH;
+  p.osS = a.o.sS;
+  p.lse = a.lse;
+  p.T = a.q.S;
+  p.err = a.err;
+  p.timeout_ns = a.timeout_ns;
+  if (a.q.dtype == FM_BF16)
+    return a.q.D == 128 ? launch_typed<__nv_bfloat16, 128>(maps, p, st) : launch_typed<__nv_bfloat16, 64>(maps, p, st);
+  return a.q.D == 128 ? launch_typed<__half, 128>(maps, p, st) : launch_typed<__half, 64>(maps, p, st);
+}
+
+}  // namespace fm
