@@ -20,8 +20,8 @@
 //                   at the end: a decoding request's tiles go through both groups at once
 // MMA order for step s of a piece (group s mod 2):  S(s), P V(s - 1): one group's softmax runs
 // under the other's two MMAs.
-// 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM; it zeroes the V rows past the request's end,
-// which meet p = 0 but may hold NaN), 2 Q loads, 3 fetches work, 4-7 and 8-11 softmax.
+// 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM), 2 Q loads and the zeroing of V rows past the
+// request's end (they meet p = 0, but may hold NaN), 3 fetches work, 4-7 and 8-11 softmax.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
 // Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
 #include <cudaTypedefs.h>
@@ -50,7 +50,8 @@ struct Cfg {
   static constexpr int offBar = offItems + 2 * (int)sizeof(SeqsItem);
   // barriers
   static constexpr int QFull = 0, QEmpty = 2, SFull = 3, PReady = 5, ODone = 7, Drain = 9, ItemFull = 10, ItemEmpty = 12,
-                       Stat = 14, EpiDone = 15, KVFull = 16, KVEmpty = KVFull + NS, kBars = KVEmpty + NS;
+                       VNeed = 14, VFix = 15, Stat = 16, EpiDone = 17, KVFull = 18, KVEmpty = KVFull + NS,
+                       kBars = KVEmpty + NS;
   static constexpr int offTmem = offBar + kBars * 8;
   static constexpr int offAbort = offTmem + 8;
   static constexpr int kSmem = offAbort + 8 + 1024;  // slack for aligning the base
@@ -162,13 +163,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the work list, and whatever the caller's earlier kernels wrote
   pdl_trigger();
 
+  // A wait of a whole warp of which one lane polls: 32 polling lanes take the time of 32 tests.
+  auto wait_warp = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
+    bool ok = true;
+    if (lane == 0) ok = wait(i, parity, code, tag);
+    return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+  };
+  // A wait that may last as long as a piece of work, by a warp whose polling would take issue
+  // slots from the softmax warps: it sleeps between looks.  (One thread.)
+  auto wait_long = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
+    for (int look = 0; look < 20000; ++look) {
+      if (mbar_test(bar(i), parity)) return true;
+      __nanosleep(100);
+    }
+    return wait(i, parity, code, tag);
+  };
+
   // The k-th piece of this CTA, read by every lane of the calling warp from the two-slot ring.
   // False when there is none left (or a wait gave up: ok says which).
   auto next_item = [&](uint32_t k, unsigned code, bool &ok, SeqsItem &it) -> bool {
     const int slot = (int)(k & 1u);
-    ok = wait(C::ItemFull + slot, (k >> 1) & 1u, code, (int)k);
-    ok = __all_sync(0xffffffffu, ok);
+    ok = true;
+    if (lane == 0) ok = wait_long(C::ItemFull + slot, (k >> 1) & 1u, code, (int)k);
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     if (!ok) return false;
+    __syncwarp();  // what lane 0 has waited for is visible to the others
     it = item_ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::ItemEmpty + slot));
@@ -211,8 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < tiles) coords(it.key0 + (j + 1) * 128, row_next, page_next);
         for (int w = 0; w < 2 && ok; ++w, ++n) {
           const int st = (int)(n % C::NS);
-          ok = wait(C::KVEmpty + st, ((n / C::NS) & 1u) ^ 1u, kDevErrTimeoutProducer, j);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = wait_warp(C::KVEmpty + st, ((n / C::NS) & 1u) ^ 1u, kDevErrTimeoutProducer, j);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(bar(C::KVFull + st), C::kTile);
           __syncwarp();
@@ -231,16 +249,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                    wtag(C::KVFull, 0));
     }
   } else if (warp == 2) {
-    // ------------------------------------------------------------ Q loads
+    // ------------------------------------------------------------ Q loads, V rows past the end
     const uint32_t q_bytes = (uint32_t)(C::PN * p.group * p.tq1 * 128);
-    uint32_t loads = 0, loads1 = 0;
+    uint32_t n = 0, loads = 0, loads1 = 0, fixes = 0;
     bool ok = true;
     SeqsItem it;
     for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutProducer, ok, it); ++k) {
       const int tiles = tiles_of(it);
       if (tiles == 0) continue;
-      if (loads > 0) ok = wait(C::QEmpty, (loads - 1) & 1u, kDevErrTimeoutProducer, (int)k);  // the last piece's S MMAs
-      ok = __all_sync(0xffffffffu, ok);
+      if (loads > 0 && lane == 0) ok = wait_long(C::QEmpty, (loads - 1) & 1u, kDevErrTimeoutProducer, (int)k);  // the last piece's S MMAs
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       if (!ok) break;
       const int nq = it.nt > p.tq1 ? 2 : 1;
       if (lane == 0) {
@@ -253,6 +271,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++loads;
       loads1 += nq - 1;
+      n += 2 * tiles;
+      const int valid = it.kv - (it.key0 + (tiles - 1) * 128);  // rows of the last tile that are the request's
+      if (valid < 128) {
+        // the MMA warp says when that tile's V has landed (its stage may be rounds ahead of this warp)
+        const uint32_t v = n - 1;
+        const int st = (int)(v % C::NS);
+        if (lane == 0)
+          ok = wait_long(C::VNeed, fixes & 1u, kDevErrTimeoutProducer, (int)k) &&
+               wait(C::KVFull + st, (v / C::NS) & 1u, kDevErrTimeoutProducer, (int)k);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (!ok) break;
+        ++fixes;
+        __syncwarp();
+        uint8_t *tile = gbase + C::offKV + st * C::kTile;
+        for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
+#pragma unroll
+          for (int pn = 0; pn < C::PN; ++pn)
+            *reinterpret_cast<uint4 *>(tile + pn * kPanel + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::VFix));
+      }
     }
     if (!ok) {
       if (loads > 0)
@@ -263,80 +303,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    auto q_desc = [&](int t, int kk) {
-      return smem_desc(base + C::offQ + t * C::kTile + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024);
-    };
-    auto k_desc = [&](int s, int kk) {
-      return smem_desc(base + C::offKV + s * C::kTile + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024);
-    };
-    auto v_desc = [&](int s, int kk) { return smem_desc(base + C::offKV + s * C::kTile + kk * 2048, kPanel, 1024); };
-    uint32_t n = 0;                  // ring tiles of earlier pieces
-    uint32_t loads = 0, loads1 = 0;  // Q tiles 0 and 1 used
-    uint32_t steps[2] = {0, 0};      // softmax steps of each group in earlier pieces
+    // One thread, and as few instructions as can be between a group's arrival and the MMA that waits
+    // for it: descriptors are sums of constants and a stage's offset (the address field of a
+    // descriptor does not carry), ring positions are stepped, not divided.
+    constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride of 8 rows, version, 128-byte swizzle
+    const uint32_t q_lo = ((base + C::offQ) >> 4) | (1u << 16), k_lo = ((base + C::offKV) >> 4) | (1u << 16);
+    const uint32_t v_lo = ((base + C::offKV) >> 4) | ((uint32_t)(kPanel >> 4) << 16);
+    auto desc = [](uint32_t lo) -> uint64_t { return ((uint64_t)kDescHi << 32) | lo; };
+    int kst = 0;                      // ring stage of the next K tile, and its phase
+    uint32_t kph = 0;
+    uint32_t loads = 0, loads1 = 0;   // Q tiles 0 and 1 used
+    uint32_t steps0 = 0, steps1 = 0;  // softmax steps of each group so far
+    uint32_t fixes = 0;
     bool ok = true;
     SeqsItem it;
     for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutMma, ok, it); ++k) {
-      const int tiles = tiles_of(it);
-      if (tiles == 0) continue;
-      const bool dual = it.nt > p.tq1;
-      const int nsub = dual ? 2 * tiles : tiles;
-      const int valid = it.kv - (it.key0 + (tiles - 1) * 128);  // rows of the last tile that are the request's
-      ok = wait(C::QFull, loads & 1u, kDevErrTimeoutMma, (int)k);
-      // P V of step s: V has landed, the group's P is ready
-      auto pv = [&](int s) -> bool {
-        const int g = s & 1, kt = dual ? s >> 1 : s;
-        const uint32_t v = n + 2 * kt + 1;
-        const int st = (int)(v % C::NS);
-        if (!dual || g == 0) {
-          if (!__all_sync(0xffffffffu, wait(C::KVFull + st, (v / C::NS) & 1u, kDevErrTimeoutMma, kt))) return false;
-          if (kt == tiles - 1 && valid < 128) {
-            uint8_t *tile = gbase + C::offKV + st * C::kTile;
-            for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
-#pragma unroll
-              for (int pn = 0; pn < C::PN; ++pn)
-                *reinterpret_cast<uint4 *>(tile + pn * kPanel + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
+      if (lane == 0 && tiles_of(it) > 0) {
+        const int tiles = tiles_of(it);
+        const bool dual = it.nt > p.tq1;
+        const bool ragged = it.kv - (it.key0 + (tiles - 1) * 128) < 128;  // rows of the last tile are not the request's
+        auto next = [](int &st, uint32_t &ph) {
+          if (++st == C::NS) {
+            st = 0;
+            ph ^= 1u;
           }
-        }
-        if (!__all_sync(0xffffffffu, wait(C::PReady + g, (steps[g] + (uint32_t)(s >> 1)) & 1u, kDevErrTimeoutMma, s)))
-          return false;
-        tc_fence_after();
-        if (lane == 0) {
+        };
+        auto mma_s = [&](int g, int qt, int st) {
+          const uint32_t a = q_lo + (uint32_t)(qt * (C::kTile >> 4)), b = k_lo + (uint32_t)(st * (C::kTile >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + 256 + g * 128, tmem + g * 128 + kk * 8, v_desc(st, kk), C::idescPV, (s >= 2 || kk > 0));
-          if (!dual || g == 1) mma_commit(bar(C::KVEmpty + st));
-          if (s + 2 >= nsub) mma_commit(bar(C::ODone + g));
-        }
-        __syncwarp();
-        return true;
-      };
-      for (int s = 0; s < nsub && ok; ++s) {
-        const int g = s & 1, kt = dual ? s >> 1 : s, qt = dual ? g : 0;
-        const uint32_t kx = n + 2 * kt;
-        const int st = (int)(kx % C::NS);
-        if (!dual || g == 0) ok = wait(C::KVFull + st, (kx / C::NS) & 1u, kDevErrTimeoutMma, kt);
-        if (ok && dual && s == 1) ok = wait(C::QFull + 1, loads1 & 1u, kDevErrTimeoutMma, (int)k);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + g * 128, q_desc(qt, kk), k_desc(st, kk), C::idescQK, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (uint32_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + g * 128, desc(a + o), desc(b + o), C::idescQK, kk > 0);
+          }
           mma_commit(bar(C::SFull + g));
-          if (!dual || g == 1) mma_commit(bar(C::KVEmpty + st));
-          if (s == nsub - 1) mma_commit(bar(C::QEmpty));
+        };
+        auto mma_pv = [&](int g, bool first, int st) {
+          const uint32_t b = v_lo + (uint32_t)(st * (C::kTile >> 4));
+          mma_ts(tmem + 256 + g * 128, tmem + g * 128, desc(b), C::idescPV, !first);
+#pragma unroll
+          for (int kk = 1; kk < 8; ++kk)
+            mma_ts(tmem + 256 + g * 128, tmem + g * 128 + kk * 8, desc(b + kk * 128), C::idescPV, 1);
+        };
+        // V of the piece's tile j has landed; the rows past the request's end in its last one are zero
+        auto v_ready = [&](int j, int st, uint32_t ph) -> bool {
+          if (!wait(C::KVFull + st, ph, kDevErrTimeoutMma, j)) return false;
+          if (!ragged || j < tiles - 1) return true;
+          mbar_arrive(bar(C::VNeed));
+          return wait(C::VFix, fixes++ & 1u, kDevErrTimeoutMma, j);
+        };
+        ok = wait(C::QFull, loads++ & 1u, kDevErrTimeoutMma, (int)k);
+        int vst = 0;
+        uint32_t vph = 0;
+        if (dual) {
+          for (int j = 0; j < tiles && ok; ++j) {
+            ok = wait(C::KVFull + kst, kph, kDevErrTimeoutMma, j);
+            if (!ok) break;
+            tc_fence_after();
+            mma_s(0, 0, kst);
+            if (j > 0) {
+              ok = wait(C::PReady + 1, steps1++ & 1u, kDevErrTimeoutMma, j);
+              if (!ok) break;
+              tc_fence_after();
+              mma_pv(1, j == 1, vst);
+              mma_commit(bar(C::KVEmpty + vst));
+            } else {
+              ok = wait(C::QFull + 1, loads1++ & 1u, kDevErrTimeoutMma, (int)k);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            mma_s(1, 1, kst);
+            mma_commit(bar(C::KVEmpty + kst));
+            if (j == tiles - 1) mma_commit(bar(C::QEmpty));
+            next(kst, kph);
+            vst = kst;
+            vph = kph;
+            next(kst, kph);
+            ok = v_ready(j, vst, vph) && wait(C::PReady, steps0++ & 1u, kDevErrTimeoutMma, j);
+            if (!ok) break;
+            tc_fence_after();
+            mma_pv(0, j == 0, vst);
+            if (j == tiles - 1) mma_commit(bar(C::ODone));
+          }
+          if (ok) {
+            ok = wait(C::PReady + 1, steps1++ & 1u, kDevErrTimeoutMma, tiles);
+            if (ok) {
+              tc_fence_after();
+              mma_pv(1, tiles == 1, vst);
+              mma_commit(bar(C::KVEmpty + vst));
+              mma_commit(bar(C::ODone + 1));
+            }
+          }
+        } else {
+          auto pv = [&](int j) -> bool {  // of tile j, group j mod 2
+            const int g = j & 1;
+            if (!v_ready(j, vst, vph) || !wait(C::PReady + g, (g ? steps1++ : steps0++) & 1u, kDevErrTimeoutMma, j))
+              return false;
+            tc_fence_after();
+            mma_pv(g, j < 2, vst);
+            mma_commit(bar(C::KVEmpty + vst));
+            if (j + 2 >= tiles) mma_commit(bar(C::ODone + g));
+            return true;
+          };
+          for (int j = 0; j < tiles && ok; ++j) {
+            ok = wait(C::KVFull + kst, kph, kDevErrTimeoutMma, j);
+            if (!ok) break;
+            tc_fence_after();
+            mma_s(j & 1, 0, kst);
+            mma_commit(bar(C::KVEmpty + kst));
+            if (j == tiles - 1) mma_commit(bar(C::QEmpty));
+            if (j > 0) ok = pv(j - 1);
+            next(kst, kph);
+            vst = kst;
+            vph = kph;
+            next(kst, kph);
+          }
+          if (ok) ok = pv(tiles - 1);
         }
-        __syncwarp();
-        if (s > 0) ok = pv(s - 1);
       }
-      if (ok) ok = pv(nsub - 1);
-      n += 2 * tiles;
-      ++loads;
-      loads1 += dual ? 1 : 0;
-      steps[0] += (uint32_t)((nsub + 1) >> 1);
-      steps[1] += (uint32_t)(nsub >> 1);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
     if (!ok && lane == 0) {
       // every MMA issued so far must finish reading shared memory and TMEM before exit
@@ -355,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) it = p.items[e];
         else it.b = -1;
         const int slot = (int)(k & 1u);
-        if (!wait(C::ItemEmpty + slot, ((k >> 1) & 1u) ^ 1u, kDevErrTimeoutProducer, (int)k)) break;
+        if (!wait_long(C::ItemEmpty + slot, ((k >> 1) & 1u) ^ 1u, kDevErrTimeoutProducer, (int)k)) break;
         item_ring[slot] = it;
         mbar_arrive(bar(C::ItemFull + slot));
       }
@@ -372,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = r / p.group, hd = r - tok * p.group;              // this row's token and head
     const int tok0 = (wq * 32) / p.group, tok1 = (wq * 32 + 31) / p.group;  // tokens of the warp's rows
     const bool row_used = tok < p.tq1;
-    uint32_t steps = 0, pieces[2] = {0, 0}, singles = 0;  // phases: S steps, O-done of both groups, Stat / EpiDone
+    uint32_t steps = 0, pieces0 = 0, pieces1 = 0, singles = 0;  // phases: S steps, O-done of both groups, Stat / EpiDone
     bool ok = true;
     SeqsItem it;
     for (uint32_t k = 0; next_item(k, kDevErrTimeoutSoftmax, ok, it); ++k) {
@@ -418,24 +502,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && wait(C::EpiDone, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        pieces[0] += nsub > 0;
-        pieces[1] += nsub > 1;
+        pieces0 += nsub > 0;
+        pieces1 += nsub > 1;
         ++singles;
         continue;
       }
       float c0 = 1.f, c1 = 0.f;
-      if (mine > 0) ok = ok && wait(C::ODone + g, pieces[g] & 1u, kDevErrTimeoutSoftmax, (int)k);
+      if (mine > 0) ok = ok && wait(C::ODone + g, (g ? pieces1 : pieces0) & 1u, kDevErrTimeoutSoftmax, (int)k);
       if (!dual) {
         // (group 1's arrival also says that it has seen O1 of its earlier pieces done, so that the
         // phase waited for next is the one after those)
         ok = ok && wait(C::Stat, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
-        if (nsub > 1) ok = ok && wait(C::ODone + 1, pieces[1] & 1u, kDevErrTimeoutSoftmax, (int)k);
+        if (nsub > 1) ok = ok && wait(C::ODone + 1, pieces1 & 1u, kDevErrTimeoutSoftmax, (int)k);
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      pieces[0] += nsub > 0;
-      pieces[1] += nsub > 1;
+      pieces0 += nsub > 0;
+      pieces1 += nsub > 1;
       if (!dual) {
         const float2 o = stat[r];
         const float m = fmaxf(run, o.x);
