@@ -195,7 +195,8 @@ struct __align__(16) SeqsItem {
 // A unit that was cut: pieces slot0, slot0 + stride, ...
 struct __align__(16) SeqsMerge {
   int h, nt, qrow0, slot0, stride, nseg;
-  int pad[2];
+  int group0;  // groups of rows of the cut units before it
+  int pad;
 };
 // Workspace of an attention call (offsets in bytes).
 struct SeqsSpace {

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMergeRows = 8;  // warps of a merge CTA
 
 struct PlanArgs {
   const int32_t *cu_q, *cu_k, *kv_len;
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
   if (all_rows > a.T) {  // starts that run backwards: the requests overlap, and nothing is computed
     if (tid == 0) {
       if (a.err && atomicCAS(a.err, 0u, (unsigned)kDevErrLength) == 0u) a.err[2] = a.err[3] = a.err[4] = 0u;
-      a.counters[0] = a.counters[1] = a.counters[2] = 0;
+      a.counters[0] = a.counters[1] = a.counters[2] = a.counters[3] = 0;
     }
     return;
   }
@@ -155,14 +156,17 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
   }
   if (tid == 0) pre[n] = (int)entries;
   __syncthreads();
-  // 3. the entries, pieces without keys left out (a unit without any key keeps one)
-  long long n_items = 0, n_merges = 0;
-  for (long long c0 = 0; c0 < entries; c0 += kPlanThreads) {
-    const long long e = c0 + tid;
+  // 3. the entries, pieces without keys left out (a unit without any key keeps one).  Where no unit
+  // is cut every entry stays, and none has to be counted.
+  const bool all = slots == 0;
+  const int n_entries = (int)entries;
+  int n_items = 0, n_merges = 0, n_groups = 0;
+  for (int c0 = 0; c0 < n_entries; c0 += kPlanThreads) {
+    const int e = c0 + tid;
     bool keep = false, cuts = false;
     SeqsItem it;
     SeqsMerge mg;
-    if (e < entries) {
+    if (e < n_entries) {
       int lo = 0, hi = n;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
       }
       const int4 r0 = a.req[2 * lo], r1 = a.req[2 * lo + 1];
       const int nt = r1.x, pieces = r1.z, per = r1.y;
-      int x = (int)(e - pre[lo]);
+      int x = e - pre[lo];
       const int t = nt - 1 - x % nt;
       x /= nt;
       const int s = x % pieces, h = x / pieces;
@@ -197,23 +201,30 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
       mg.slot0 = slot0;
       mg.stride = nt;
       mg.nseg = mine;
-      mg.pad[0] = mg.pad[1] = 0;
+      mg.pad = 0;
     }
-    long long ki, mi;
-    const long long both = (keep ? 1ll : 0ll) | (cuts ? 1ll << 32 : 0ll);
+    if (all) {
+      if (e < n_entries) a.items[e] = it;
+      continue;
+    }
+    // one scan of three counts, each below 2^21 in 1,024 entries: entries kept, units cut, and the
+    // cut units' groups of kMergeRows rows
+    const int groups = cuts ? (mg.nt * a.g.group + kMergeRows - 1) / kMergeRows : 0;
     long long sum;
-    const long long at = block_scan(both, warp_sum, sum);
-    ki = n_items + (at & 0xffffffffll);
-    mi = n_merges + (at >> 32);
-    if (keep) a.items[ki] = it;
-    if (cuts) a.merges[mi] = mg;
-    n_items += sum & 0xffffffffll;
-    n_merges += sum >> 32;
+    const long long at = block_scan((keep ? 1ll : 0ll) | (cuts ? 1ll << 21 : 0ll) | ((long long)groups << 42), warp_sum, sum);
+    const int mask = (1 << 21) - 1;
+    if (keep) a.items[n_items + (int)(at & mask)] = it;
+    mg.group0 = n_groups + (int)(at >> 42);
+    if (cuts) a.merges[n_merges + (int)((at >> 21) & mask)] = mg;
+    n_items += (int)(sum & mask);
+    n_merges += (int)((sum >> 21) & mask);
+    n_groups += (int)(sum >> 42);
   }
   if (tid == 0) {
     a.counters[0] = 0;
-    a.counters[1] = (unsigned)n_items;
+    a.counters[1] = (unsigned)(all ? n_entries : n_items);
     a.counters[2] = (unsigned)n_merges;
+    a.counters[3] = (unsigned)n_groups;
   }
 }
 
@@ -238,20 +249,29 @@ __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) { return
 template <>
 __device__ __forceinline__ __half to_out<__half>(float x) { return __float2half_rn(x); }
 
-// One warp a row: with piece s holding (o_s, m_s, l_s), M = max m_s and c_s = 2^(m_s - M),
+// One warp a row, kMergeRows rows a CTA and step: with piece s holding (o_s, m_s, l_s), M = max m_s and c_s = 2^(m_s - M),
 //   o = sum c_s o_s / sum c_s l_s,  lse = ln2 (M + log2 sum c_s l_s),
 // pieces taken in key order.  Bound by reading the partial results, which are still in L2.
 template <typename E, int D>
-__global__ void __launch_bounds__(256) seqs_merge_kernel(const MergeArgs a) {
+__global__ void __launch_bounds__(32 * kMergeRows) seqs_merge_kernel(const MergeArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31;
-  const unsigned n_merges = a.counters[2];
-  const unsigned groups = (unsigned)(a.slot_rows + 7) / 8;
-  for (unsigned x = blockIdx.x; x < n_merges * groups; x += gridDim.x) {
-    const SeqsMerge m = a.merges[x / groups];
-    const int row = (int)(x % groups) * 8 + (threadIdx.x >> 5);
+  // this CTA's even share of the groups of kMergeRows rows, found by one search of the list
+  const int n_merges = (int)a.counters[2], n_groups = (int)a.counters[3];
+  const int per = (n_groups + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int g0 = (int)blockIdx.x * per, g1 = min(g0 + per, n_groups);
+  if (g0 >= g1) return;
+  int i = 0;
+  for (int hi = n_merges; hi - i > 1;) {
+    const int mid = (i + hi) >> 1;
+    if (a.merges[mid].group0 <= g0) i = mid; else hi = mid;
+  }
+  SeqsMerge m = a.merges[i];
+  for (int g = g0; g < g1; ++g) {
+    while (g - m.group0 >= (m.nt * a.group + kMergeRows - 1) / kMergeRows) m = a.merges[++i];
+    const int row = (g - m.group0) * kMergeRows + (threadIdx.x >> 5);
     if (row >= m.nt * a.group) continue;
     float M = -INFINITY;
     for (int s = lane; s < m.nseg; s += 32)
@@ -261,6 +281,7 @@ __global__ void __launch_bounds__(256) seqs_merge_kernel(const MergeArgs a) {
     float l = 0.f, o[EPL];
 #pragma unroll
     for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+#pragma unroll 4
     for (int s = 0; s < m.nseg; ++s) {
       const int64_t at = (int64_t)(m.slot0 + s * m.stride) * a.slot_rows + row;
       const float2 ml = a.part_ml[at];
@@ -360,7 +381,7 @@ cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSp
   m.T = a.q.S;
   m.lse = a.lse;
   m.o = a.o;
-  const dim3 grid((unsigned)current_device_sm_count() * 4), threads(256);
+  const dim3 grid((unsigned)current_device_sm_count() * 4), threads(32 * kMergeRows);
   if (a.o.D == 128) {
     if (a.o.dtype == FM_F32) return launch_pdl(seqs_merge_kernel<float, 128>, grid, threads, 0, st, m);
     if (a.o.dtype == FM_BF16) return launch_pdl(seqs_merge_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, m);
