@@ -27,6 +27,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -475,35 +476,60 @@ def seqs_opts(causal: bool = True, window: int = 0, softmax_scale: float = 0.0) 
     return fm_seqs_opts(float(softmax_scale), int(bool(causal)), int(window))
 
 
-def _rows(t: torch.Tensor) -> fm_tensor:
-    """Describe packed rows: a [T, H, D] tensor, or a [1, H, T, D] one (any strides)."""
-    if t.dim() == 3:
-        st = t.stride()
-        return fm_tensor(t.data_ptr() or None, _DTYPES.get(t.dtype, -1), 0, 1, t.shape[1], t.shape[0], t.shape[2],
-                         (ctypes.c_int64 * 4)(0, st[1], st[0], st[2]))
-    return tensor(t)
+# These calls are made once a layer and step, often for a few microseconds of work, so their arguments
+# go to the library as packed bytes (the layouts of fm_tensor, fm_seqs and fm_page_state).
+_TENSOR_BYTES, _SEQS_BYTES, _STATE_BYTES = struct.Struct("=Qii8q").pack, struct.Struct("=q4Q2q").pack, struct.Struct("=3qQ2q5Q").pack
 
 
-def _on_device(device: int, **tensors):
-    """Every tensor on the given CUDA device: the kernels get raw pointers."""
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device.index != device):
-            raise FMError(FM_ERR_ARG, f"{name} must be on the current CUDA device (cuda:{device}), not {t.device}")
+def _rows(t: torch.Tensor, name: str, device: int) -> bytes:
+    """fm_tensor of packed rows: a [T, H, D] tensor, or a [1, H, T, D] one (any strides)."""
+    if t.dim() == 4:
+        return _cache(t, name, device)
+    if t.dim() != 3:
+        raise FMError(FM_ERR_SHAPE, f"{name}: expected a [T, H, D] or [1, H, T, D] tensor, got shape {tuple(t.shape)}")
+    if t.get_device() != device:
+        _not_here(t, name, device)
+    (S, H, D), (sS, sH, sD) = t.shape, t.stride()
+    return _TENSOR_BYTES(t.data_ptr(), _DTYPES.get(t.dtype, -1), 0, 1, H, S, D, 0, sH, sS, sD)
 
 
-def _ints(t, dtype, numel, name):
+def _cache(t: torch.Tensor, name: str, device: int) -> bytes:
+    """fm_tensor of a 4-D [B, H, S, D] tensor (any strides)."""
+    if t.dim() != 4:
+        raise FMError(FM_ERR_SHAPE, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}")
+    if t.get_device() != device:
+        _not_here(t, name, device)
+    return _TENSOR_BYTES(t.data_ptr(), _DTYPES.get(t.dtype, -1), 0, *t.shape, *t.stride())
+
+
+def _not_here(t, name, device):
+    """The kernels get raw pointers: every tensor has to be on the current device."""
+    raise FMError(FM_ERR_ARG, f"{name} must be on the current CUDA device (cuda:{device}), not {t.device}")
+
+
+def _ints(t, dtype, numel, name, device):
     """Data pointer of a contiguous int tensor of at least numel elements."""
     if t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
         raise FMError(FM_ERR_ARG, f"{name} must be a contiguous {dtype} tensor of at least {numel} elements, got "
                                   f"{tuple(t.shape)} {t.dtype}")
-    return t.data_ptr() or None
+    if t.get_device() != device:
+        _not_here(t, name, device)
+    return t.data_ptr()
 
 
-def _table(t, n):
+def _table(t, n, device):
     if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
         raise FMError(FM_ERR_ARG, f"block_table must be a 2-D int32 tensor of at least {n} rows with adjacent "
                                   f"entries, got {tuple(t.shape)} {t.dtype}")
-    return t.data_ptr() or None, t.stride(0), t.shape[1]
+    if t.get_device() != device:
+        _not_here(t, "block_table", device)
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def _stream_handle(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def fm_attn_seqs_workspace_size(n_seqs: int, T: int, Hq: int, Hk: int, D: int) -> int:
@@ -512,23 +538,31 @@ def fm_attn_seqs_workspace_size(n_seqs: int, T: int, Hq: int, Hk: int, D: int) -
     return n.value
 
 
-def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream):
-    tq, to = _rows(q), _rows(o_out)
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != tq.H * tq.S):
-        raise FMError(FM_ERR_ARG, f"lse must be a contiguous float32 [{tq.H}, {tq.S}] tensor, got {tuple(lse.shape)}")
-    return _check(fn(ctypes.byref(tq), ctypes.byref(k), ctypes.byref(v), ctypes.byref(seqs), ctypes.byref(opt),
-                     ctypes.byref(to), _ptr(lse), _ptr(workspace),
-                     0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream, device):
+    if lse is not None:
+        heads, rows = (q.shape[1], q.shape[0]) if q.dim() == 3 else (q.shape[1], q.shape[2])
+        if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != heads * rows:
+            raise FMError(FM_ERR_ARG, f"lse must be a contiguous float32 [{heads}, {rows}] tensor, got {tuple(lse.shape)}")
+        if lse.get_device() != device:
+            _not_here(lse, "lse", device)
+        lse = lse.data_ptr()
+    ws = nbytes = 0
+    if workspace is not None:
+        if workspace.get_device() != device:
+            _not_here(workspace, "workspace", device)
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = fn(_rows(q, "q", device), k, v, seqs, ctypes.byref(opt), _rows(o_out, "o_out", device), lse, ws, nbytes,
+            _stream_handle(stream, device))
+    return rc if rc == FM_OK else _check(rc)
 
 
 def fm_attn_varlen(q, k, v, cu_q, cu_k, opt: fm_seqs_opts, o_out, lse=None, workspace=None, stream=None):
     """Attention of packed requests: q, o_out [T, Hq, D], k, v [Tk, Hk, D] (or [1, H, T, D]); request i
     owns rows cu[i] .. cu[i+1]-1 of each.  lse [Hq, T]; see include/fm.h."""
-    _on_device(torch.cuda.current_device(), q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o_out=o_out, lse=lse,
-               workspace=workspace)
-    n = cu_q.numel() - 1
-    seqs = fm_seqs(n, _ints(cu_q, torch.int32, 1, "cu_q"), _ints(cu_k, torch.int32, n + 1, "cu_k"), None, None, 0, 0)
-    return _attn_seqs(load().fm_attn_varlen, q, _rows(k), _rows(v), seqs, opt, o_out, lse, workspace, stream)
+    dev, n, i32 = torch.cuda.current_device(), cu_q.numel() - 1, torch.int32
+    seqs = _SEQS_BYTES(n, _ints(cu_q, i32, 1, "cu_q", dev), _ints(cu_k, i32, n + 1, "cu_k", dev), 0, 0, 0, 0)
+    return _attn_seqs(load().fm_attn_varlen, q, _rows(k, "k", dev), _rows(v, "v", dev), seqs, opt, o_out, lse, workspace,
+                      stream, dev)
 
 
 def fm_attn_paged(q, k_cache, v_cache, cu_q, kv_len, block_table, opt: fm_seqs_opts, o_out, lse=None, workspace=None,
@@ -536,13 +570,11 @@ def fm_attn_paged(q, k_cache, v_cache, cu_q, kv_len, block_table, opt: fm_seqs_o
     """Attention of each request's new tokens (q, o_out [T, Hq, D], packed by cu_q) over its pages:
     caches [pages, Hk, page_size, D] (any strides), block_table int32 [n, width], kv_len int32 [n]
     with the new tokens counted; see include/fm.h."""
-    _on_device(torch.cuda.current_device(), q=q, k_cache=k_cache, v_cache=v_cache, cu_q=cu_q, kv_len=kv_len,
-               block_table=block_table, o_out=o_out, lse=lse, workspace=workspace)
-    n = cu_q.numel() - 1
-    table, stride, width = _table(block_table, n)
-    seqs = fm_seqs(n, _ints(cu_q, torch.int32, 1, "cu_q"), None, _ints(kv_len, torch.int32, n, "kv_len"), table, stride,
-                   width)
-    return _attn_seqs(load().fm_attn_paged, q, tensor(k_cache), tensor(v_cache), seqs, opt, o_out, lse, workspace, stream)
+    dev, n, i32 = torch.cuda.current_device(), cu_q.numel() - 1, torch.int32
+    table, stride, width = _table(block_table, n, dev)
+    seqs = _SEQS_BYTES(n, _ints(cu_q, i32, 1, "cu_q", dev), 0, _ints(kv_len, i32, n, "kv_len", dev), table, stride, width)
+    return _attn_seqs(load().fm_attn_paged, q, _cache(k_cache, "k_cache", dev), _cache(v_cache, "v_cache", dev), seqs, opt,
+                      o_out, lse, workspace, stream, dev)
 
 
 def fm_paged_extend(new_len, release, kv_len, kv_len_out, block_table, free_pages, free_count, free_count_out,
@@ -550,29 +582,27 @@ def fm_paged_extend(new_len, release, kv_len, kv_len_out, block_table, free_page
     """Room in the pages for new_len[i] more tokens of every request (release[i] != 0: the row's
     request has ended and gives its pages back first).  kv_len_out and free_count_out may be kv_len
     and free_count.  Fills cu_q [n+1], slots and positions [max tokens], status [1]; see include/fm.h."""
-    _on_device(torch.cuda.current_device(), new_len=new_len, release=release, kv_len=kv_len, kv_len_out=kv_len_out,
-               block_table=block_table, free_pages=free_pages, free_count=free_count, free_count_out=free_count_out,
-               cu_q=cu_q, slots=slots, positions=positions, status=status)
-    n, i32 = new_len.numel(), torch.int32
-    table, stride, width = _table(block_table, n)
-    st = fm_page_state(n, int(page_size), free_pages.numel(), table, stride, width,
-                       _ints(free_pages, i32, 0, "free_pages"), _ints(free_count, i32, 1, "free_count"),
-                       _ints(free_count_out, i32, 1, "free_count_out"), _ints(kv_len, i32, n, "kv_len"),
-                       _ints(kv_len_out, i32, n, "kv_len_out"))
-    rel = None if release is None else _ints(release, torch.uint8, n, "release")
-    cap = slots.numel()
-    return _check(load().fm_paged_extend(ctypes.byref(st), _ints(new_len, i32, n, "new_len"), rel, cap,
-                                         _ints(cu_q, i32, n + 1, "cu_q"), _ints(slots, torch.int64, cap, "slots"),
-                                         _ints(positions, i32, cap, "positions"), _ints(status, i32, 1, "status"),
-                                         _stream(stream)))
+    dev, n, cap, i32 = torch.cuda.current_device(), new_len.numel(), slots.numel(), torch.int32
+    table, stride, width = _table(block_table, n, dev)
+    st = _STATE_BYTES(n, page_size, free_pages.numel(), table, stride, width,
+                      _ints(free_pages, i32, 0, "free_pages", dev), _ints(free_count, i32, 1, "free_count", dev),
+                      _ints(free_count_out, i32, 1, "free_count_out", dev), _ints(kv_len, i32, n, "kv_len", dev),
+                      _ints(kv_len_out, i32, n, "kv_len_out", dev))
+    rc = load().fm_paged_extend(st, _ints(new_len, i32, n, "new_len", dev),
+                                None if release is None else _ints(release, torch.uint8, n, "release", dev), cap,
+                                _ints(cu_q, i32, n + 1, "cu_q", dev), _ints(slots, torch.int64, cap, "slots", dev),
+                                _ints(positions, i32, cap, "positions", dev), _ints(status, i32, 1, "status", dev),
+                                _stream_handle(stream, dev))
+    return rc if rc == FM_OK else _check(rc)
 
 
 def fm_paged_write(k, v, slots, k_cache, v_cache, stream=None):
     """k, v rows [T, H, D] (or [1, H, T, D]) put at their slots of the caches [pages, H, page_size, D]."""
-    _on_device(torch.cuda.current_device(), k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
-    tk = _rows(k)
-    return _check(load().fm_paged_write(ctypes.byref(tk), ctypes.byref(_rows(v)), _ints(slots, torch.int64, tk.S, "slots"),
-                                        ctypes.byref(tensor(k_cache)), ctypes.byref(tensor(v_cache)), _stream(stream)))
+    dev = torch.cuda.current_device()
+    rows = k.shape[0] if k.dim() == 3 else k.shape[2]
+    rc = load().fm_paged_write(_rows(k, "k", dev), _rows(v, "v", dev), _ints(slots, torch.int64, rows, "slots", dev),
+                               _cache(k_cache, "k_cache", dev), _cache(v_cache, "v_cache", dev), _stream_handle(stream, dev))
+    return rc if rc == FM_OK else _check(rc)
 
 
 def _on_stream(stream):

@@ -178,6 +178,7 @@ struct SeqsGeom {
   int n_slots;    // partial results that fit the workspace
   int ctas;       // CTAs that the work is spread over
   int min_tiles;  // a unit is not cut into pieces shorter than this
+  int stream;     // 1: the tensor-core kernel cuts the work into one even run per CTA by itself
 };
 
 // One piece of work: a unit against its keys [key0, key1).
@@ -192,11 +193,11 @@ struct __align__(16) SeqsItem {
   int slot;       // partial result to write, -1: the unit's only piece
   int pad[2];
 };
-// A unit that was cut: pieces slot0, slot0 + stride, ...
+// A unit that was cut: its pieces' partial results are slot0, slot1, slot1 + stride, ...
 struct __align__(16) SeqsMerge {
-  int h, nt, qrow0, slot0, stride, nseg;
+  int h, nt, qrow0, nseg;
+  int slot0, slot1, stride;
   int group0;  // groups of rows of the cut units before it
-  int pad;
 };
 // Workspace of an attention call (offsets in bytes).
 struct SeqsSpace {

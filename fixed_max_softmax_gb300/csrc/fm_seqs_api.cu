@@ -119,7 +119,7 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   // the work list, the attention, the merge of what was cut
   auto run = [&](const SeqsGeom &g, cudaError_t (*attend)(const SeqsArgs &, const SeqsGeom &, const SeqsSpace &, cudaStream_t)) {
     const SeqsSpace s = seqs_space(g, a.n, a.q.S, a.k.H, a.q.D);
-    cudaError_t e = launch_seqs_plan(a, g, s, st);
+    cudaError_t e = g.stream ? cudaSuccess : launch_seqs_plan(a, g, s, st);
     if (e == cudaSuccess) e = attend(a, g, s, st);
     if (e == cudaSuccess) e = launch_seqs_merge(a, g, s, st);
     return e;

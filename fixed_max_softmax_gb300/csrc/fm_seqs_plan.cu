@@ -23,9 +23,9 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kMergeRows = 8;  // warps of a merge CTA
 
 struct PlanArgs {
-  const int32_t *cu_q, *cu_k, *kv_len;
-  int64_t n, T, Tk, cap_keys;  // cap_keys: keys that a row of the page table can hold
-  int paged, Hk, causal, window;
+  SeqsLens lens;
+  int64_t n;
+  int Hk, causal, window;
   SeqsGeom g;
   unsigned int *counters;
   int4 *req;  // per request: {first query row, queries, keys, first key row}, {units, tiles a piece, pieces, slot base}
@@ -68,32 +68,13 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
   __shared__ long long warp_sum[kPlanWarps];
   const int tid = threadIdx.x, n = (int)a.n, tq = a.g.tq, bk = a.g.bk;
   // 1. lengths, clamped to the tensors (a length that does not fit is reported), and the tiles of work
-  long long w = 0, rows = 0;
+  long long w = 0;
+  bool back = false;
   for (int b = tid; b < n; b += kPlanThreads) {
-    const int r0 = a.cu_q[b], r1 = a.cu_q[b + 1];
-    const int q0 = (int)max((int64_t)0, min((int64_t)r0, a.T)), q1 = (int)max((int64_t)q0, min((int64_t)r1, a.T));
-    int k0 = 0, kv;
-    bool bad = q0 != r0 || q1 != r1;
-    if (a.paged) {
-      const int x = a.kv_len[b];
-      kv = (int)max((int64_t)0, min((int64_t)x, a.cap_keys));
-      bad |= kv != x;
-    } else {
-      const int x0 = a.cu_k[b], x1 = a.cu_k[b + 1];
-      k0 = (int)max((int64_t)0, min((int64_t)x0, a.Tk));
-      const int k1 = (int)max((int64_t)k0, min((int64_t)x1, a.Tk));
-      bad |= k0 != x0 || k1 != x1;
-      kv = k1 - k0;
-    }
-    if (bad && a.err && atomicCAS(a.err, 0u, (unsigned)kDevErrLength) == 0u) {
-      a.err[1] = (unsigned)b;
-      a.err[2] = (unsigned)r0;
-      a.err[3] = (unsigned)r1;
-      a.err[4] = (unsigned)kv;
-    }
-    const int q = q1 - q0, nt = (q + tq - 1) / tq;
-    rows += q;
-    a.req[2 * b] = make_int4(q0, q, kv, k0);
+    const Request r = request_of(a.lens, b, a.err);
+    const int q = r.q, kv = r.kv, nt = (q + tq - 1) / tq;
+    back |= r.back;
+    a.req[2 * b] = make_int4(r.q0, q, kv, r.k0);
     int longest = 0;
     if (nt > 0) {
       const TileRange f = unit_tiles(kv - q, min(tq, q), kv, bk, a.causal, a.window);
@@ -108,13 +89,11 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
     }
     a.req[2 * b + 1] = make_int4(nt, longest, 1, 0);
   }
-  long long work, all_rows;
+  long long work;
   block_scan(w, warp_sum, work);
-  block_scan(rows, warp_sum, all_rows);
   work *= a.Hk;
-  if (all_rows > a.T) {  // starts that run backwards: the requests overlap, and nothing is computed
+  if (__syncthreads_or(back)) {
     if (tid == 0) {
-      if (a.err && atomicCAS(a.err, 0u, (unsigned)kDevErrLength) == 0u) a.err[2] = a.err[3] = a.err[4] = 0u;
       a.counters[0] = a.counters[1] = a.counters[2] = a.counters[3] = 0;
     }
     return;
@@ -199,9 +178,9 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
       mg.nt = it.nt;
       mg.qrow0 = it.qrow0;
       mg.slot0 = slot0;
+      mg.slot1 = slot0 + nt;
       mg.stride = nt;
       mg.nseg = mine;
-      mg.pad = 0;
     }
     if (all) {
       if (e < n_entries) a.items[e] = it;
@@ -234,7 +213,7 @@ struct MergeArgs {
   const SeqsMerge *merges;
   const float *part_o;
   const float2 *part_ml;
-  int slot_rows, group;
+  int slot_rows, group, per_cta;
   int64_t T;
   float *lse;
   View o;
@@ -253,11 +232,58 @@ __device__ __forceinline__ __half to_out<__half>(float x) { return __float2half_
 //   o = sum c_s o_s / sum c_s l_s,  lse = ln2 (M + log2 sum c_s l_s),
 // pieces taken in key order.  Bound by reading the partial results, which are still in L2.
 template <typename E, int D>
+__device__ __forceinline__ void merge_row(const MergeArgs &a, const SeqsMerge &m, int row, int lane) {
+  constexpr int EPL = D / 32;
+  auto slot = [&](int s) -> int64_t { return s == 0 ? m.slot0 : m.slot1 + (s - 1) * m.stride; };
+  float M = -INFINITY;
+  for (int s = lane; s < m.nseg; s += 32)
+    M = fmaxf(M, a.part_ml[slot(s) * a.slot_rows + row].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float l = 0.f, o[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < m.nseg; ++s) {
+    const int64_t at = slot(s) * a.slot_rows + row;
+    const float2 ml = a.part_ml[at];
+    const float c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    l = fmaf(ml.y, c, l);
+    const float *src = a.part_o + at * D + lane * EPL;
+    if constexpr (EPL == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(src);
+      o[0] = fmaf(v.x, c, o[0]);
+      o[1] = fmaf(v.y, c, o[1]);
+      o[2] = fmaf(v.z, c, o[2]);
+      o[3] = fmaf(v.w, c, o[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2 *>(src);
+      o[0] = fmaf(v.x, c, o[0]);
+      o[1] = fmaf(v.y, c, o[1]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: zeros, lse = -inf
+  const int head = m.h * a.group + row % a.group;
+  const int64_t tok = m.qrow0 + row / a.group;
+  E *dst = reinterpret_cast<E *>(const_cast<void *>(a.o.ptr)) + head * a.o.sH + tok * a.o.sS + lane * EPL * a.o.sD;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) dst[e * a.o.sD] = to_out<E>(o[e] * inv);
+  if (a.lse && lane == 0) a.lse[head * a.T + tok] = l == 0.f ? -INFINITY : 0.69314718055994531f * (M + log2f(l));
+
+}
+
+template <typename E, int D>
 __global__ void __launch_bounds__(32 * kMergeRows) seqs_merge_kernel(const MergeArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31;
+  if (a.per_cta) {  // at most one cut unit begins in each CTA of the attention kernel
+    const SeqsMerge m = a.merges[blockIdx.x];
+    if (m.nseg < 2) return;
+    for (int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5); row < m.nt * a.group; row += gridDim.y * kMergeRows)
+      merge_row<E, D>(a, m, row, lane);
+    return;
+  }
   // this CTA's even share of the groups of kMergeRows rows, found by one search of the list
   const int n_merges = (int)a.counters[2], n_groups = (int)a.counters[3];
   const int per = (n_groups + (int)gridDim.x - 1) / (int)gridDim.x;
@@ -273,40 +299,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) seqs_merge_kernel(const Merge
     while (g - m.group0 >= (m.nt * a.group + kMergeRows - 1) / kMergeRows) m = a.merges[++i];
     const int row = (g - m.group0) * kMergeRows + (threadIdx.x >> 5);
     if (row >= m.nt * a.group) continue;
-    float M = -INFINITY;
-    for (int s = lane; s < m.nseg; s += 32)
-      M = fmaxf(M, a.part_ml[(int64_t)(m.slot0 + s * m.stride) * a.slot_rows + row].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float l = 0.f, o[EPL];
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < m.nseg; ++s) {
-      const int64_t at = (int64_t)(m.slot0 + s * m.stride) * a.slot_rows + row;
-      const float2 ml = a.part_ml[at];
-      const float c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      l = fmaf(ml.y, c, l);
-      const float *src = a.part_o + at * D + lane * EPL;
-      if constexpr (EPL == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        o[0] = fmaf(v.x, c, o[0]);
-        o[1] = fmaf(v.y, c, o[1]);
-        o[2] = fmaf(v.z, c, o[2]);
-        o[3] = fmaf(v.w, c, o[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        o[0] = fmaf(v.x, c, o[0]);
-        o[1] = fmaf(v.y, c, o[1]);
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: zeros, lse = -inf
-    const int head = m.h * a.group + row % a.group;
-    const int64_t tok = m.qrow0 + row / a.group;
-    E *dst = reinterpret_cast<E *>(const_cast<void *>(a.o.ptr)) + head * a.o.sH + tok * a.o.sS + lane * EPL * a.o.sD;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) dst[e * a.o.sD] = to_out<E>(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[head * a.T + tok] = l == 0.f ? -INFINITY : 0.69314718055994531f * (M + log2f(l));
+    merge_row<E, D>(a, m, row, lane);
   }
 }
 
@@ -338,15 +331,8 @@ SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_
 cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st) {
   uint8_t *ws = static_cast<uint8_t *>(a.ws);
   PlanArgs p;
-  p.cu_q = a.cu_q;
-  p.cu_k = a.cu_k;
-  p.kv_len = a.kv_len;
+  p.lens = seqs_lens(a);
   p.n = a.n;
-  p.T = a.q.S;
-  p.Tk = a.paged ? 0 : a.k.S;
-  p.cap_keys = a.paged ? a.table_width * a.k.S : 0;
-  if (p.cap_keys > ((int64_t)1 << 30)) p.cap_keys = (int64_t)1 << 30;
-  p.paged = a.paged;
   p.Hk = (int)a.k.H;
   p.causal = a.causal;
   p.window = a.window;
@@ -378,10 +364,12 @@ cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSp
   m.part_ml = reinterpret_cast<const float2 *>(ws + s.part_ml);
   m.slot_rows = g.slot_rows;
   m.group = g.group;
+  m.per_cta = g.stream;
   m.T = a.q.S;
   m.lse = a.lse;
   m.o = a.o;
-  const dim3 grid((unsigned)current_device_sm_count() * 4), threads(32 * kMergeRows);
+  const dim3 grid = g.stream ? dim3((unsigned)g.ctas, g.slot_rows > 4 * kMergeRows ? 4 : 1) : dim3((unsigned)(4 * g.ctas));
+  const dim3 threads(32 * kMergeRows);
   if (a.o.D == 128) {
     if (a.o.dtype == FM_F32) return launch_pdl(seqs_merge_kernel<float, 128>, grid, threads, 0, st, m);
     if (a.o.dtype == FM_BF16) return launch_pdl(seqs_merge_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, m);

@@ -269,8 +269,9 @@ SeqsGeom seqs_geom_simt(int64_t T, int group) {
   g.bk = kK;
   g.slot_rows = (int)(g.tq < T ? g.tq : T) * group;
   g.ctas = 2 * current_device_sm_count();
-  g.n_slots = 8 * g.ctas;
+  g.n_slots = 4 * g.ctas;
   g.min_tiles = 2;
+  g.stream = 0;
   return g;
 }
 

@@ -9,10 +9,15 @@
 // Rows.  A tile's 128 rows are floor(128 / G) tokens x the G query heads of one key head, token by
 // token, so that the heads that share a key head read it once and a decoding request fills G rows
 // with one pass over its keys.  One 3-D TMA box {64, G, tokens} per 64 columns gathers a tile.
-// Keys.  A tile's 128 keys are one TMA box per 64 columns (packed, or pages of 128 keys and more)
-// or 128 / page_size boxes, one lane of the producer warp a box; pages past the request's end are
-// asked for at a page that does not exist, which TMA fills with zeros.
-// Work.  A CTA a SM takes pieces from the list in order (a counter).  A piece is a unit of queries
+// Keys.  A tile's 128 keys are one TMA box (packed, or pages of 128 keys and more: 64-column panels
+// of 128 rows) or one box a page, one lane of the producer warp a box.  A page's box brings its
+// 64-column panels for each 8 keys together ({64, 8, panels, page_size / 8}), so that a tile's
+// groups of 8 keys are evenly spaced whatever the page size, which a matrix descriptor needs: one
+// box a page and panel was bound by the number of boxes (16-key pages: 1.73 us a tile of K and V,
+// 32-key pages 1.40, the rate of HBM).  Pages past the request's end are asked for at a page that
+// does not exist, which TMA fills with zeros.
+// Work.  A CTA a SM takes pieces from the list in order (a counter), or, where requests have few
+// queries, an even run of all units' key tiles.  A piece is a unit of queries
 // -- two row tiles, or one when its tokens fit one (decoding, the rest of a chunk) -- against a
 // range of keys.  The tensor core always alternates between two softmax groups of four warps:
 //   two row tiles   group g has row tile g, both against the same key tile
@@ -70,10 +75,15 @@ struct Params {
   int causal, window;
   float alpha;
   int paged, ps, box_rows, num_pages;
+  int grouped, page_groups;   // boxes of whole pages, and the groups of 8 keys from one page to the next
+  int panel_step, group_step; // bytes between a tile's 64-column panels, and between its groups of 8 keys
   const int32_t *table;
   int64_t table_stride;
   unsigned int *counters;
   const SeqsItem *items;
+  SeqsMerge *merges;
+  SeqsLens lens;
+  int n, Hk, stream;
   float *part_o;
   float2 *part_ml;
   int slot_rows;
@@ -86,6 +96,17 @@ struct Params {
   unsigned long long timeout_ns;
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0, int c1, int c2, int c3,
+                                            int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0, int c1, int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -159,27 +180,191 @@ __device__ __forceinline__ void store_row32(uint8_t *dst, const float (&x)[32]) 
                       __float_as_uint(x[4 * i + 3]));
 }
 
-// A descriptor's upper half: stride of 8 rows, version, 128-byte swizzle.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+// A descriptor's upper half: stride of 8 rows in 16-byte units, version, 128-byte swizzle.
+__device__ __forceinline__ uint64_t desc(uint32_t step, uint32_t lo) {
+  return ((uint64_t)(step | (1u << 14) | (2u << 29)) << 32) | lo;
+}
 
-// S = Q K^T of one tile pair, then the arrival at `done`; a, b: lower halves of Q's and K's descriptors.
+// S = Q K^T of one tile pair, then the arrival at `done`.  a, b: lower halves of Q's and K's
+// descriptors; panel, group: steps of K's tile in 16-byte units.
 template <typename C>
-__device__ __forceinline__ void mma_scores(uint32_t tS, uint32_t a, uint32_t b, uint32_t done) {
+__device__ __forceinline__ void mma_scores(uint32_t tS, uint32_t a, uint32_t b, uint32_t panel, uint32_t group, uint32_t done) {
 #pragma unroll
   for (int kk = 0; kk < 4 * C::PN; ++kk) {
-    const uint32_t o = (uint32_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4);
-    mma_ss(tS, desc(a + o), desc(b + o), C::idescQK, kk > 0);
+    const uint32_t o = (uint32_t)((kk & 3) * 2);
+    mma_ss(tS, desc(64, a + o + (uint32_t)((kk >> 2) * (kPanel >> 4))), desc(group, b + o + (kk >> 2) * panel), C::idescQK,
+           kk > 0);
   }
   mma_commit(done);
 }
 // O (+)= P V of one tile; b: lower half of V's descriptor.
 template <typename C>
-__device__ __forceinline__ void mma_output(uint32_t tO, uint32_t tP, uint32_t b, uint32_t acc) {
-  mma_ts(tO, tP, desc(b), C::idescPV, acc);
+__device__ __forceinline__ void mma_output(uint32_t tO, uint32_t tP, uint32_t b, uint32_t group, uint32_t acc) {
+  mma_ts(tO, tP, desc(group, b), C::idescPV, acc);
 #pragma unroll
-  for (int kk = 1; kk < 8; ++kk) mma_ts(tO, tP + kk * 8, desc(b + kk * 128), C::idescPV, 1);
+  for (int kk = 1; kk < 8; ++kk) mma_ts(tO, tP + kk * 8, desc(group, b + kk * 2 * group), C::idescPV, 1);
 }
+
+// ---------------------------------------------------------------- one even run per CTA
+// Calls of few queries a request (decoding) take no work list: the units in order of request, key
+// head and queries, each as long as its key tiles and kUnitCost, are one line, and CTA c takes the
+// c-th of equal parts.  A unit that a boundary cuts leaves partial results: a CTA has at most one
+// piece that continues a unit (slot 2c) and one that begins a unit and does not end it (2c + 1).
+constexpr int kUnitCost = 1;   // a piece's start and end, in key tiles
+constexpr int kLeastRun = 4;   // shorter runs would cost more to merge than they save
+
+// This CTA's part [x0, x1) of the line, and the unit that x0 falls in: (b, h, t), starting at u0.
+struct StreamRun {
+  long long total, x0, x1, u0;
+  int parts, b, h, t;
+  Request req;
+};
+
+__device__ __forceinline__ int unit_cost(const Params &p, const Request &r, int t) {
+  const int tq = 2 * p.tq1;
+  const TileRange u = unit_tiles(r.kv - r.q + t * tq, min(tq, r.q - t * tq), r.kv, 128, p.causal, p.window);
+  return u.e - u.a + kUnitCost;
+}
+__device__ __forceinline__ long long request_cost(const Params &p, const Request &r) {  // of one key head
+  long long c = 0;
+  for (int t = 0; t * 2 * p.tq1 < r.q; ++t) c += unit_cost(p, r, t);
+  return c;
+}
+// a * b / c, by a 32-bit division where the product fits (b < 256)
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+  if (a < (1 << 24)) return ((unsigned)a * (unsigned)b) / (unsigned)c;
+  return a * b / c;
+}
+
+// Every thread of the CTA: sums the requests' costs, a run of requests a thread, in one scan, and
+// the thread whose requests hold x0 finds the unit.  A few dependent steps after one round of
+// loads: it stands before the first tile of every call.  `warp_sum`: a long long per warp.
+__device__ __forceinline__ void stream_run(const Params &p, long long *warp_sum, StreamRun *out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (p.n + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(b0 + each, p.n);
+  unsigned int *err = blockIdx.x == 0 ? p.err : nullptr;
+  long long mine = 0;
+  bool back = false;
+  Request r = {0, 0, 0, 0, false};
+  for (int b = b0; b < b1; ++b) {
+    r = request_of(p.lens, b, err);
+    mine += request_cost(p, r) * p.Hk;
+    back |= r.back;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += u;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  const bool none = __syncthreads_or(back);
+  long long start = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) start += warp_sum[w];
+    total += warp_sum[w];
+  }
+  if (none) total = 0;
+  const long long most = (total + kLeastRun - 1) / kLeastRun;
+  const int parts = (int)max(1ll, min((long long)gridDim.x, most)), c = blockIdx.x;
+  const bool works = c < parts && total > 0;
+  const long long x0 = works ? mul_div(total, c, parts) : 0, x1 = works ? mul_div(total, c + 1, parts) : 0;
+  if (tid == 0) {
+    out->total = total;
+    out->parts = parts;
+    out->x0 = x0;
+    out->x1 = x1;
+  }
+  if (x0 < x1 && start <= x0 && x0 < start + mine) {
+    int b = b0;
+    long long per_head = 0;
+    for (;; ++b) {
+      if (each > 1) r = request_of(p.lens, b, nullptr);
+      per_head = request_cost(p, r);
+      if (x0 < start + per_head * p.Hk) break;
+      start += per_head * p.Hk;
+    }
+    const int h = (int)mul_div(x0 - start, 1, per_head);
+    start += h * per_head;
+    int t = 0;
+    for (int u; start + (u = unit_cost(p, r, t)) <= x0; ++t) start += u;
+    out->b = b;
+    out->h = h;
+    out->t = t;
+    out->u0 = start;
+    out->req = r;
+  }
+  __syncthreads();
+}
+
+// One thread: the run's pieces in order.
+struct StreamWalk {
+  StreamRun r;
+  bool merge_told;
+
+  // The next piece; false when the run is at its end (the CTA's merge entry is then written).
+  __device__ __forceinline__ bool next(const Params &p, SeqsItem &it) {
+    const int tq = 2 * p.tq1;
+    bool found = false;
+    while (!found && r.x0 < r.x1 && r.u0 < r.x1) {
+      const int nt = min(tq, r.req.q - r.t * tq), pos0 = r.req.kv - r.req.q + r.t * tq;
+      const TileRange u = unit_tiles(pos0, nt, r.req.kv, 128, p.causal, p.window);
+      const int tiles = u.e - u.a;
+      const int from = (int)max(0ll, r.x0 - r.u0), to = (int)min((long long)tiles, r.x1 - r.u0);
+      found = from < to || (tiles == 0 && from == 0);
+      if (found) {
+        it.b = r.b;
+        it.h = r.h;
+        it.nt = nt;
+        it.qrow0 = r.req.q0 + r.t * tq;
+        it.pos0 = pos0;
+        it.kv = r.req.kv;
+        it.krow0 = r.req.k0;
+        it.key0 = (u.a + from) * 128;
+        it.key1 = tiles > 0 ? min((u.a + to) * 128, u.hi) : it.key0;
+        const bool whole = from == 0 && to >= tiles;
+        it.slot = whole ? -1 : 2 * (int)blockIdx.x + (from == 0 ? 1 : 0);
+        if (!whole && from == 0) {
+          // the CTA that holds the unit's last tile: the last c with total * c / parts <= its place
+          const long long end = r.u0 + tiles;
+          const int last = r.total < (1 << 24) ? (int)(((unsigned)end * (unsigned)r.parts - 1u) / (unsigned)r.total)
+                                               : (int)((end * r.parts - 1) / r.total);
+          SeqsMerge m;
+          m.h = r.h;
+          m.nt = nt;
+          m.qrow0 = it.qrow0;
+          m.nseg = last - (int)blockIdx.x + 1;
+          m.slot0 = it.slot;
+          m.slot1 = 2 * (int)blockIdx.x + 2;
+          m.stride = 2;
+          m.group0 = 0;
+          p.merges[blockIdx.x] = m;
+          merge_told = true;
+        }
+      }
+      r.u0 += tiles + kUnitCost;
+      if (++r.t * tq >= r.req.q) {
+        r.t = 0;
+        if (++r.h == p.Hk) {
+          r.h = 0;
+          do {
+            if (++r.b >= p.n) {
+              r.u0 = r.x1;  // the line ends with the last request
+              break;
+            }
+            r.req = request_of(p.lens, r.b, nullptr);
+          } while (r.req.q == 0);
+        }
+      }
+    }
+    if (!found && !merge_told) {
+      p.merges[blockIdx.x].nseg = 0;
+      merge_told = true;
+    }
+    return found;
+  }
+};
 
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -207,6 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(i), count);
     }
     fence_mbar_init();
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
@@ -215,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the work list, and whatever the caller's earlier kernels wrote
   pdl_trigger();
+  StreamRun *run_of_cta = reinterpret_cast<StreamRun *>(gbase + C::offStat + 128);
+  if (p.stream) stream_run(p, reinterpret_cast<long long *>(gbase + C::offStat), run_of_cta);
 
   // A wait of a whole warp of which one lane polls: 32 polling lanes take the time of 32 tests.
   auto wait_warp = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
@@ -250,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ K/V producer
-    const int boxes = 128 / p.box_rows * C::PN;  // of one tile; this lane's: panel pn of page pg
-    const int pn = lane % C::PN, pg = lane / C::PN;
+    const int boxes = 128 / p.box_rows;  // of one tile; this lane's is its pg-th
+    const int pg = lane;
     uint32_t n = 0;  // tiles loaded into the ring so far
     bool ok = true;
     SeqsItem it;
@@ -271,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int at = key / p.ps;
           page = p.table[it.b * p.table_stride + at];
           if (page < 0 || page >= p.num_pages) {
-            if (pn == 0) report_bad_page(p.err, it.b, at, page);
+            report_bad_page(p.err, it.b, at, page);
             page = p.num_pages;
           }
         }
@@ -287,9 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(bar(C::KVFull + st), C::kTile);
           __syncwarp();
-          if (lane < boxes)
-            tma_load_4d(base + C::offKV + st * C::kTile + pn * kPanel + pg * p.box_rows * 128, w ? &maps.v : &maps.k,
-                        bar(C::KVFull + st), pn * 64, row, it.h, page);
+          if (lane < boxes) {
+            const uint32_t dst = base + C::offKV + st * C::kTile;
+            const CUtensorMap *tm = w ? &maps.v : &maps.k;
+            if (p.grouped) {
+              tma_load_5d(dst + pg * p.box_rows * 128 * C::PN, tm, bar(C::KVFull + st), 0, 0, 0, page * p.page_groups, it.h);
+            } else if (boxes == 1) {
+              tma_load_5d(dst, tm, bar(C::KVFull + st), 0, row, 0, it.h, page);
+            } else {
+              for (int pn = 0; pn < C::PN; ++pn)
+                tma_load_5d(dst + pn * kPanel + pg * p.box_rows * 128, tm, bar(C::KVFull + st), 0, row, pn, it.h, page);
+            }
+          }
         }
         row = row_next;
         page = page_next;
@@ -340,10 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++fixes;
         __syncwarp();
         uint8_t *tile = gbase + C::offKV + st * C::kTile;
-        for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
+        for (int x = valid * 8 + lane; x < 128 * 8; x += 32) {  // 16-byte words of a panel: 64 a group of 8 keys
+          uint8_t *at = tile + (x >> 6) * p.group_step + (x & 63) * 16;
 #pragma unroll
-          for (int pn = 0; pn < C::PN; ++pn)
-            *reinterpret_cast<uint4 *>(tile + pn * kPanel + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          for (int pn = 0; pn < C::PN; ++pn) *reinterpret_cast<uint4 *>(at + pn * p.panel_step) = make_uint4(0u, 0u, 0u, 0u);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::VFix));
@@ -362,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // for it: descriptors are sums of constants and a stage's offset (the address field of a
     // descriptor does not carry), ring positions are stepped, not divided.
     const uint32_t q_lo = ((base + C::offQ) >> 4) | (1u << 16), k_lo = ((base + C::offKV) >> 4) | (1u << 16);
-    const uint32_t v_lo = ((base + C::offKV) >> 4) | ((uint32_t)(kPanel >> 4) << 16);
+    const uint32_t panel = (uint32_t)p.panel_step >> 4, group = (uint32_t)p.group_step >> 4;
+    const uint32_t v_lo = ((base + C::offKV) >> 4) | (panel << 16);
     int kst = 0;                      // ring stage of the next K tile, and its phase
     uint32_t kph = 0;
     uint32_t loads = 0, loads1 = 0;   // Q tiles 0 and 1 used
@@ -383,10 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto mma_s = [&](int g, int qt, int st) {
           mma_scores<C>(tmem + g * 128, q_lo + (uint32_t)(qt * (C::kTile >> 4)), k_lo + (uint32_t)(st * (C::kTile >> 4)),
-                        bar(C::SFull + g));
+                        panel, group, bar(C::SFull + g));
         };
         auto mma_pv = [&](int g, bool first, int st) {
-          mma_output<C>(tmem + 256 + g * 128, tmem + g * 128, v_lo + (uint32_t)(st * (C::kTile >> 4)), !first);
+          mma_output<C>(tmem + 256 + g * 128, tmem + g * 128, v_lo + (uint32_t)(st * (C::kTile >> 4)), group, !first);
         };
         // V of the piece's tile j has landed; the rows past the request's end in its last one are zero
         auto v_ready = [&](int j, int st, uint32_t ph) -> bool {
@@ -474,17 +675,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ work
     if (lane == 0) {
-      const unsigned n_items = p.counters[1];
+      const unsigned n_items = p.stream ? 0u : p.counters[1];
+      StreamWalk walk;
+      walk.merge_told = false;
+      if (p.stream) walk.r = *run_of_cta;
       bool more = true;
       for (uint32_t k = 0; more; ++k) {
         // a piece is claimed when the producer is nearly through with the one before, not earlier:
         // claimed ahead, pieces would wait behind a long one while other CTAs run dry
         if (k > 0 && !wait_long(C::Want, (k - 1) & 1u, kDevErrTimeoutProducer, (int)k)) break;
-        const unsigned e = atomicAdd(&p.counters[0], 1u);
         SeqsItem it;
-        more = e < n_items;
-        if (more) it = p.items[e];
-        else it.b = -1;
+        if (p.stream) {
+          more = walk.next(p, it);
+        } else {
+          const unsigned e = atomicAdd(&p.counters[0], 1u);
+          more = e < n_items;
+          if (more) it = p.items[e];
+        }
+        if (!more) it.b = -1;
         const int slot = (int)(k & 1u);
         if (!wait_long(C::ItemEmpty + slot, ((k >> 1) & 1u) ^ 1u, kDevErrTimeoutProducer, (int)k)) break;
         item_ring[slot] = it;
@@ -648,7 +856,7 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 bool encode(CUtensorMap *map, const View &t, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
   auto enc = get_encode();
   if (!enc) return false;
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   return enc(map, t.dtype == FM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
              const_cast<void *>(t.ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -664,12 +872,31 @@ bool encode_q(CUtensorMap *map, const View &t, int group, int tq1) {
   const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tq1};
   return encode(map, t, 3, dims, strides, box);
 }
-// k or v [B, Hk, S, D] (pages, or one batch of packed rows) as (D, S, Hk, B), box {64, rows, 1, 1}.
+// k or v [B, Hk, S, D] (pages, or one batch of packed rows) as (64, S, panels, Hk, B), a box of `rows`
+// rows of all panels, or of one where a tile takes several boxes.
 bool encode_kv(CUtensorMap *map, const View &t, int rows) {
-  const cuuint64_t dims[4] = {(cuuint64_t)t.D, (cuuint64_t)t.S, (cuuint64_t)t.H, (cuuint64_t)t.B};
-  const cuuint64_t strides[3] = {step(t.sS, t.S, t.D), step(t.sH, t.H, t.S * t.D), step(t.sB, t.B, t.H * t.S * t.D)};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
-  return encode(map, t, 4, dims, strides, box);
+  const cuuint64_t pn = (cuuint64_t)t.D / 64;
+  const cuuint64_t dims[5] = {64, (cuuint64_t)t.S, pn, (cuuint64_t)t.H, (cuuint64_t)t.B};
+  const cuuint64_t strides[4] = {step(t.sS, t.S, t.D), 128, step(t.sH, t.H, t.S * t.D), step(t.sB, t.B, t.H * t.S * t.D)};
+  const cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)(rows == 128 ? pn : 1), 1, 1};
+  return encode(map, t, 5, dims, strides, box);
+}
+// Pages of fewer than 128 rows as (64, 8, panels, groups of 8 rows over all pages, Hk), a box of one
+// page.  Wants pages that lie a whole number of groups apart.
+bool encode_pages(CUtensorMap *map, const View &t) {
+  const int64_t step8 = 8 * t.sS, per_page = t.B > 1 ? t.sB / step8 : t.S / 8;
+  const cuuint64_t pn = (cuuint64_t)t.D / 64;
+  const cuuint64_t dims[5] = {64, 8, pn, (cuuint64_t)((t.B - 1) * per_page + t.S / 8), (cuuint64_t)t.H};
+  const cuuint64_t strides[4] = {(cuuint64_t)t.sS * 2, 128, (cuuint64_t)step8 * 2, step(t.sH, t.H, t.S * t.D)};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)pn, (cuuint32_t)(t.S / 8), 1};
+  return encode(map, t, 5, dims, strides, box);
+}
+// Groups of 8 rows from one page to the next, 0: not a whole number (or too many to index).
+int64_t page_groups(const View &t) {
+  const int64_t step8 = 8 * t.sS;
+  if (t.B > 1 && (t.sB % step8 || t.sB / step8 < t.S / 8)) return 0;
+  const int64_t g = t.B > 1 ? t.sB / step8 : t.S / 8;
+  return (t.B + 1) * g < ((int64_t)1 << 31) ? g : 0;
 }
 
 bool rows16(const View &x, int64_t es) {
@@ -713,6 +940,8 @@ SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
   g.ctas = current_device_sm_count();
   g.n_slots = 8 * g.ctas;
   g.min_tiles = 4;
+  // few queries a request: a tile of rows holds all of most requests' queries of a key head
+  g.stream = T * group <= 128 * n ? 1 : 0;
   return g;
 }
 
@@ -724,8 +953,14 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.group = g.group;
   p.tq1 = g.tq / 2;
   p.box_rows = a.paged && a.k.S < 128 ? (int)a.k.S : 128;
-  if (!encode_q(&maps.q, a.q, p.group, p.tq1) || !encode_kv(&maps.k, a.k, p.box_rows) ||
-      !encode_kv(&maps.v, a.v, p.box_rows))
+  const int64_t groups = p.box_rows < 128 ? page_groups(a.k) : 0;
+  p.grouped = groups > 0 && groups == page_groups(a.v);
+  p.page_groups = (int)groups;
+  p.panel_step = p.grouped ? 1024 : kPanel;
+  p.group_step = p.grouped ? 1024 * (int)(a.k.D / 64) : 1024;
+  if (!encode_q(&maps.q, a.q, p.group, p.tq1) ||
+      !(p.grouped ? encode_pages(&maps.k, a.k) && encode_pages(&maps.v, a.v)
+                  : encode_kv(&maps.k, a.k, p.box_rows) && encode_kv(&maps.v, a.v, p.box_rows)))
     return cudaErrorNotSupported;
   p.causal = a.causal;
   p.window = a.window;
@@ -737,6 +972,11 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.table_stride = a.table_stride;
   p.counters = reinterpret_cast<unsigned int *>(ws + s.counters);
   p.items = reinterpret_cast<const SeqsItem *>(ws + s.items);
+  p.merges = reinterpret_cast<SeqsMerge *>(ws + s.merges);
+  p.lens = seqs_lens(a);
+  p.n = (int)a.n;
+  p.Hk = (int)a.k.H;
+  p.stream = g.stream;
   p.part_o = reinterpret_cast<float *>(ws + s.part_o);
   p.part_ml = reinterpret_cast<float2 *>(ws + s.part_ml);
   p.slot_rows = g.slot_rows;

@@ -458,8 +458,9 @@ FM_API int fm_bounds_noalloc(const fm_tensor *q, const fm_tensor *k_full, const 
  *     sees must be finite: a NaN or infinity there may reach that request's other rows.
  *   - All lengths are read on the device: nothing waits for them, calls can be captured into a
  *     graph and replayed with other lengths (the first call on a device comes before any
- *     capture).  Lengths that do not fit the tensors are clamped, a table entry outside
- *     [0, num_pages) reads as zeros, and the next fm_sync_status returns FM_ERR_INDEX.
+ *     capture).  Lengths that do not fit the tensors are clamped, cu_q that runs backwards computes
+ *     nothing, a table entry outside [0, num_pages) reads as zeros, and the next fm_sync_status
+ *     returns FM_ERR_INDEX.
  *   - The workspace is scratch: its contents need no preparation and mean nothing afterwards.  Calls
  *     that may run at the same time need one each. */
 #define FM_MAX_GROUP 64

@@ -136,6 +136,24 @@ def test_struct_layouts_match_header(tmp_path):
     assert seen == sum(len(c._fields_) + 1 for c in structs.values())
 
 
+def test_packed_arguments_match_the_structs():
+    """What the binding packs is what the ctypes mirrors hold, field by field."""
+    t = torch.empty(7, 3, 2, 64, dtype=torch.float16).transpose(1, 2)
+    got, want = fm.fm_tensor.from_buffer_copy(fm._cache(t, "t", -1)), fm.tensor(t)
+    for f in ("ptr", "dtype", "reserved", "B", "H", "S", "D"):
+        assert getattr(got, f) == getattr(want, f), f
+    assert list(got.stride) == list(want.stride)
+    r = torch.empty(9, 5, 128)[:, 1:3]
+    got, want = fm.fm_tensor.from_buffer_copy(fm._rows(r, "r", -1)), fm.tensor(r.permute(1, 0, 2)[None])
+    assert [got.ptr, got.dtype, got.B, got.H, got.S, got.D] == [want.ptr, want.dtype, 1, 2, 9, 128]
+    assert list(got.stride)[1:] == list(want.stride)[1:]
+    s = fm.fm_seqs.from_buffer_copy(fm._SEQS_BYTES(*range(1, 8)))
+    assert [getattr(s, f) for f, _ in s._fields_] == list(range(1, 8))
+    p = fm.fm_page_state.from_buffer_copy(fm._STATE_BYTES(*range(1, 12)))
+    assert [getattr(p, f) for f, _ in p._fields_] == list(range(1, 12))
+    assert len(fm._STATE_BYTES(*range(11))) == ctypes.sizeof(fm.fm_page_state)
+
+
 def test_constants_match_header():
     text = open(os.path.join(ROOT, "include", "fm.h")).read()
     for name in ("FM_MAX_GROUP", "FM_MAX_SEQS"):
@@ -160,12 +178,12 @@ def test_binding_refuses_host_tensors(lib, monkeypatch):
 
 def test_binding_checks_integer_tensors():
     with pytest.raises(fm.FMError, match="cu_q"):
-        fm._ints(torch.zeros(3, dtype=torch.int64), torch.int32, 1, "cu_q")
+        fm._ints(torch.zeros(3, dtype=torch.int64), torch.int32, 1, "cu_q", 0)
     with pytest.raises(fm.FMError, match="kv_len"):
-        fm._ints(torch.zeros(3, dtype=torch.int32), torch.int32, 4, "kv_len")
+        fm._ints(torch.zeros(3, dtype=torch.int32), torch.int32, 4, "kv_len", 0)
     with pytest.raises(fm.FMError, match="slots"):
-        fm._ints(torch.zeros(6, dtype=torch.int64)[::2], torch.int64, 3, "slots")
+        fm._ints(torch.zeros(6, dtype=torch.int64)[::2], torch.int64, 3, "slots", 0)
     with pytest.raises(fm.FMError, match="block_table"):
-        fm._table(torch.zeros(3, 4, dtype=torch.int32).t(), 3)
+        fm._table(torch.zeros(3, 4, dtype=torch.int32).t(), 3, 0)
     with pytest.raises(fm.FMError, match="block_table"):
-        fm._table(torch.zeros(2, 4, dtype=torch.int32), 3)
+        fm._table(torch.zeros(2, 4, dtype=torch.int32), 3, 0)
