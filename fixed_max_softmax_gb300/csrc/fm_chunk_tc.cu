@@ -93,15 +93,6 @@ constexpr int kBoxBytes = kBQ * 128;  // 32 fp32 columns x 128 rows
 constexpr uint32_t kIdescQK = idesc_f16(kBQ, kBK, false, true);  // S = Q K^T: K is [keys, D], K-major
 constexpr uint32_t kIdescPV = idesc_f16(kBQ, kHD, true, true);   // O = P V:   V is [keys, D], MN-major
 
-// The lane index, read where it is used: arithmetic on it cannot be hoisted out of an enclosing
-// loop (IN_LOOP: the epilogue helpers run once per item inside the persistent kernel's item
-// loop, and their lane-dependent addresses would otherwise stay live across every key tile).
-__device__ __forceinline__ int opaque_laneid() {
-  int l;
-  asm volatile("mov.u32 %0, %%laneid;" : "=r"(l));
-  return l;
-}
-
 // What the debug build (FM_DEBUG) checks a warp's epilogue accesses against; unused otherwise:
 // the flat row index of the warp's first row over [B, H, Sq], the rows of the accumulators, the
 // offset of the warp's first row of o and the span of o, in elements.

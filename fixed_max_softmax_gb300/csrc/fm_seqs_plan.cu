@@ -235,31 +235,40 @@ template <typename E, int D>
 __device__ __forceinline__ void merge_row(const MergeArgs &a, const SeqsMerge &m, int row, int lane) {
   constexpr int EPL = D / 32;
   auto slot = [&](int s) -> int64_t { return s == 0 ? m.slot0 : m.slot1 + (s - 1) * m.stride; };
-  float M = -INFINITY;
-  for (int s = lane; s < m.nseg; s += 32)
-    M = fmaxf(M, a.part_ml[slot(s) * a.slot_rows + row].x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float l = 0.f, o[EPL];
+  // lane s holds piece s's max and sum; 32 pieces at a time
+  float M = -INFINITY, l = 0.f, o[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int s0 = 0; s0 < m.nseg; s0 += 32) {
+    const int n = min(32, m.nseg - s0);
+    const float2 ml = lane < n ? a.part_ml[slot(s0 + lane) * a.slot_rows + row] : make_float2(-INFINITY, 0.f);
+    float mx = ml.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    mx = fmaxf(M, mx);
+    const float keep = M == -INFINITY ? 0.f : exp2f(M - mx);  // of the pieces before these
+    M = mx;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= keep;
+    const float c_mine = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
 #pragma unroll 4
-  for (int s = 0; s < m.nseg; ++s) {
-    const int64_t at = slot(s) * a.slot_rows + row;
-    const float2 ml = a.part_ml[at];
-    const float c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-    l = fmaf(ml.y, c, l);
-    const float *src = a.part_o + at * D + lane * EPL;
-    if constexpr (EPL == 4) {
-      const float4 v = *reinterpret_cast<const float4 *>(src);
-      o[0] = fmaf(v.x, c, o[0]);
-      o[1] = fmaf(v.y, c, o[1]);
-      o[2] = fmaf(v.z, c, o[2]);
-      o[3] = fmaf(v.w, c, o[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2 *>(src);
-      o[0] = fmaf(v.x, c, o[0]);
-      o[1] = fmaf(v.y, c, o[1]);
+    for (int s = 0; s < n; ++s) {
+      const float c = __shfl_sync(0xffffffffu, c_mine, s);
+      l = fmaf(__shfl_sync(0xffffffffu, ml.y, s), c, l);
+      const float *src = a.part_o + (slot(s0 + s) * a.slot_rows + row) * D + lane * EPL;
+      if constexpr (EPL == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        o[0] = fmaf(v.x, c, o[0]);
+        o[1] = fmaf(v.y, c, o[1]);
+        o[2] = fmaf(v.z, c, o[2]);
+        o[3] = fmaf(v.w, c, o[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        o[0] = fmaf(v.x, c, o[0]);
+        o[1] = fmaf(v.y, c, o[1]);
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: zeros, lse = -inf
@@ -289,10 +298,13 @@ __global__ void __launch_bounds__(32 * kMergeRows) seqs_merge_kernel(const Merge
   const int per = (n_groups + (int)gridDim.x - 1) / (int)gridDim.x;
   const int g0 = (int)blockIdx.x * per, g1 = min(g0 + per, n_groups);
   if (g0 >= g1) return;
-  int i = 0;
-  for (int hi = n_merges; hi - i > 1;) {
-    const int mid = (i + hi) >> 1;
-    if (a.merges[mid].group0 <= g0) i = mid; else hi = mid;
+  int i = 0;  // the last entry whose groups start at or before g0: 32 entries looked at a step
+  for (int n = n_merges; n > 1;) {
+    const int step = (n + 31) / 32, at = i + lane * step;
+    const unsigned before = __ballot_sync(0xffffffffu, lane * step < n && a.merges[at].group0 <= g0);
+    const int last = 31 - __clz(before);
+    i += last * step;
+    n = min(step, n - last * step);
   }
   SeqsMerge m = a.merges[i];
   for (int g = g0; g < g1; ++g) {

@@ -30,6 +30,7 @@
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
 // Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <string.h>
 
 #include <mutex>
@@ -43,9 +44,11 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kPanel = 128 * 128;  // 128 rows of 64 16-bit columns: one 128-byte swizzle span
 
-template <typename E, int D>
+template <typename E, int D, bool GROUPED>
 struct Cfg {
   static constexpr int PN = D / 64;          // panels of a tile
+  // bytes between a K or V tile's panels, and between its groups of 8 keys (GROUPED: see encode_pages)
+  static constexpr int kPanelStep = GROUPED ? 1024 : kPanel, kGroupStep = GROUPED ? 1024 * PN : 1024;
   static constexpr int kTile = PN * kPanel;  // bytes
   static constexpr int NS = 10 / PN;         // K/V ring: 160 KiB
   static constexpr int offQ = 0;
@@ -54,8 +57,8 @@ struct Cfg {
   static constexpr int offItems = offStat + 128 * 8;
   static constexpr int offBar = offItems + 2 * (int)sizeof(SeqsItem);
   // barriers
-  static constexpr int QFull = 0, QEmpty = 2, SFull = 3, PReady = 5, ODone = 7, Drain = 9, ItemFull = 10, ItemEmpty = 12,
-                       VNeed = 14, VFix = 15, Stat = 16, EpiDone = 17, Want = 18, KVFull = 19, KVEmpty = KVFull + NS,
+  static constexpr int QFull = 0, QEmpty = 2, SFull = 4, PReady = 6, ODone = 8, ItemFull = 10, ItemEmpty = 12, VNeed = 14,
+                       VFix = 15, Stat = 16, EpiDone = 17, Want = 18, Drain = 19, KVFull = 20, KVEmpty = KVFull + NS,
                        kBars = KVEmpty + NS;
   static constexpr int offTmem = offBar + kBars * 8;
   static constexpr int offAbort = offTmem + 8;
@@ -75,15 +78,14 @@ struct Params {
   int causal, window;
   float alpha;
   int paged, ps, box_rows, num_pages;
-  int grouped, page_groups;   // boxes of whole pages, and the groups of 8 keys from one page to the next
-  int panel_step, group_step; // bytes between a tile's 64-column panels, and between its groups of 8 keys
+  int page_groups;  // groups of 8 keys from one page to the next (GROUPED)
   const int32_t *table;
   int64_t table_stride;
   unsigned int *counters;
   const SeqsItem *items;
   SeqsMerge *merges;
   SeqsLens lens;
-  int n, Hk, stream;
+  int n, Hk;
   float *part_o;
   float2 *part_ml;
   int slot_rows;
@@ -139,12 +141,13 @@ __device__ __noinline__ void mask_rows(uint32_t tS, int kb, int lo, int hi, int 
   tmem_st_wait();
 }
 
-// 32 columns of each of a warp's rows to memory, lane r holding row r (at dst; ok: it is written).
-// 16-bit elements: the 64 bytes of a row go out as one piece, four lanes a row, after a 4 x 4
-// exchange of 16-byte words within each four lanes; lane by lane, a store would touch 32 lines of
-// memory instead of 8, and the store unit takes a line a cycle.
+// 32 columns of each of a warp's rows to memory as 16-bit elements, lane r holding row r.  The 64
+// bytes of a row go out as one piece, four lanes a row, after a 4 x 4 exchange of 16-byte words
+// within each four lanes; lane by lane, a store would touch 32 lines of memory instead of 8, and
+// the store unit takes a line a cycle.  row[i]: this lane's 16 bytes of the i-th of its four lanes'
+// rows, nullptr where that row is not written.
 template <typename E>
-__device__ __forceinline__ void store_rows16(uint8_t *dst, bool ok, const float (&x)[32], int lane) {
+__device__ __forceinline__ void store_rows16(uint8_t *const (&row)[4], int offset, const float (&x)[32], int lane) {
   uint4 w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -164,13 +167,9 @@ __device__ __forceinline__ void store_rows16(uint8_t *dst, bool ok, const float 
   exchange(w[0], w[2], 2);
   exchange(w[1], w[3], 2);
   // w[i] is now word lane % 4 of row (lane & ~3) + i
-  const unsigned rows = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int from = (lane & ~3) + i;
-    uint8_t *d = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
-    if ((rows >> from) & 1u) *reinterpret_cast<uint4 *>(d + (lane & 3) * 16) = w[i];
-  }
+  for (int i = 0; i < 4; ++i)
+    if (row[i]) *reinterpret_cast<uint4 *>(row[i] + offset) = w[i];
 }
 __device__ __forceinline__ void store_row32(uint8_t *dst, const float (&x)[32]) {
   uint4 *p = reinterpret_cast<uint4 *>(dst);
@@ -185,91 +184,112 @@ __device__ __forceinline__ uint64_t desc(uint32_t step, uint32_t lo) {
   return ((uint64_t)(step | (1u << 14) | (2u << 29)) << 32) | lo;
 }
 
-// S = Q K^T of one tile pair, then the arrival at `done`.  a, b: lower halves of Q's and K's
-// descriptors; panel, group: steps of K's tile in 16-byte units.
+// S = Q K^T of one tile pair, then the arrival at `done`; a, b: lower halves of Q's and K's descriptors.
+// Unrolled with constant steps: an MMA has to be issued in less time than it runs, and with steps
+// in registers or a loop around it it is not (1.66 -> 2.4 us a tile).
 template <typename C>
-__device__ __forceinline__ void mma_scores(uint32_t tS, uint32_t a, uint32_t b, uint32_t panel, uint32_t group, uint32_t done) {
+__device__ __forceinline__ void mma_scores(uint32_t tS, uint32_t a, uint32_t b, uint32_t done) {
 #pragma unroll
   for (int kk = 0; kk < 4 * C::PN; ++kk) {
     const uint32_t o = (uint32_t)((kk & 3) * 2);
-    mma_ss(tS, desc(64, a + o + (uint32_t)((kk >> 2) * (kPanel >> 4))), desc(group, b + o + (kk >> 2) * panel), C::idescQK,
-           kk > 0);
+    mma_ss(tS, desc(64, a + o + (uint32_t)((kk >> 2) * (kPanel >> 4))),
+           desc(C::kGroupStep >> 4, b + o + (uint32_t)((kk >> 2) * (C::kPanelStep >> 4))), C::idescQK, kk > 0);
   }
   mma_commit(done);
 }
 // O (+)= P V of one tile; b: lower half of V's descriptor.
 template <typename C>
-__device__ __forceinline__ void mma_output(uint32_t tO, uint32_t tP, uint32_t b, uint32_t group, uint32_t acc) {
-  mma_ts(tO, tP, desc(group, b), C::idescPV, acc);
+__device__ __forceinline__ void mma_output(uint32_t tO, uint32_t tP, uint32_t b, uint32_t acc) {
+  mma_ts(tO, tP, desc(C::kGroupStep >> 4, b), C::idescPV, acc);
 #pragma unroll
-  for (int kk = 1; kk < 8; ++kk) mma_ts(tO, tP + kk * 8, desc(group, b + kk * 2 * group), C::idescPV, 1);
+  for (int kk = 1; kk < 8; ++kk)
+    mma_ts(tO, tP + kk * 8, desc(C::kGroupStep >> 4, b + (uint32_t)(kk * 2 * (C::kGroupStep >> 4))), C::idescPV, 1);
 }
 
 // ---------------------------------------------------------------- one even run per CTA
 // Calls of few queries a request (decoding) take no work list: the units in order of request, key
-// head and queries, each as long as its key tiles and kUnitCost, are one line, and CTA c takes the
+// head and queries, each as long as its key tiles take, are one line, and CTA c takes the
 // c-th of equal parts.  A unit that a boundary cuts leaves partial results: a CTA has at most one
 // piece that continues a unit (slot 2c) and one that begins a unit and does not end it (2c + 1).
-constexpr int kUnitCost = 1;   // a piece's start and end, in key tiles
-constexpr int kLeastRun = 4;   // shorter runs would cost more to merge than they save
+// The line's measure, in about 0.35 us: a key tile of a unit of one row tile (streamed from HBM) and
+// of two (bound by the tensor core and the exponentials), and a unit's start and end.
+constexpr int kTileCost1 = 4, kTileCost2 = 5, kUnitCost1 = 5, kUnitCost2 = 10;
+constexpr int kLeastRun = 12;  // shorter runs would cost more to merge than they save (none is shorter than a tile)
 
 // This CTA's part [x0, x1) of the line, and the unit that x0 falls in: (b, h, t), starting at u0.
 struct StreamRun {
-  long long total, x0, x1, u0;
+  int total, x0, x1, u0;
   int parts, b, h, t;
   Request req;
 };
+// The line is measured in 32 bits: a thread's requests may hold 2^31 / kThreads of it (5.5 million
+// key tiles, more than the GPU's memory), and a call that has more is refused as lengths that do
+// not fit.
+constexpr int kMostOfThread = 0x7fffffff / kThreads;
 
 __device__ __forceinline__ int unit_cost(const Params &p, const Request &r, int t) {
   const int tq = 2 * p.tq1;
-  const TileRange u = unit_tiles(r.kv - r.q + t * tq, min(tq, r.q - t * tq), r.kv, 128, p.causal, p.window);
-  return u.e - u.a + kUnitCost;
+  const int nt = min(tq, r.q - t * tq);
+  const TileRange u = unit_tiles(r.kv - r.q + t * tq, nt, r.kv, 128, p.causal, p.window);
+  return nt > p.tq1 ? (u.e - u.a) * kTileCost2 + kUnitCost2 : (u.e - u.a) * kTileCost1 + kUnitCost1;
 }
 __device__ __forceinline__ long long request_cost(const Params &p, const Request &r) {  // of one key head
   long long c = 0;
+#pragma unroll 1
   for (int t = 0; t * 2 * p.tq1 < r.q; ++t) c += unit_cost(p, r, t);
   return c;
 }
-// a * b / c, by a 32-bit division where the product fits (b < 256)
-__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
-  if (a < (1 << 24)) return ((unsigned)a * (unsigned)b) / (unsigned)c;
-  return a * b / c;
+// a * b / c for a line of length a: 32-bit division where the product fits (b < 256)
+__device__ __forceinline__ int part_of(int a, int b, int c) {
+  if (a < (1 << 24)) return (int)(((unsigned)a * (unsigned)b) / (unsigned)c);
+  return (int)((long long)a * b / c);
 }
 
 // Every thread of the CTA: sums the requests' costs, a run of requests a thread, in one scan, and
 // the thread whose requests hold x0 finds the unit.  A few dependent steps after one round of
-// loads: it stands before the first tile of every call.  `warp_sum`: a long long per warp.
-__device__ __forceinline__ void stream_run(const Params &p, long long *warp_sum, StreamRun *out) {
+// loads, in as little code as can be: it stands before the first tile of every call.
+__device__ __forceinline__ void stream_run(const Params &p, int *warp_sum, StreamRun *out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (p.n + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(b0 + each, p.n);
   unsigned int *err = blockIdx.x == 0 ? p.err : nullptr;
-  long long mine = 0;
-  bool back = false;
+  long long sum = 0, per_head = 0;
+  bool refuse = false;
   Request r = {0, 0, 0, 0, false};
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     r = request_of(p.lens, b, err);
-    mine += request_cost(p, r) * p.Hk;
-    back |= r.back;
+    per_head = request_cost(p, r);
+    sum += per_head * p.Hk;
+    refuse |= r.back;
   }
-  long long inc = mine;
+  if (sum > kMostOfThread) {
+    refuse = true;
+    sum = 0;
+    if (err && atomicCAS(err, 0u, (unsigned)kDevErrLength) == 0u) err[1] = (unsigned)b0;
+  }
+  const int mine = (int)sum;
+  int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, inc, d);
+    const int u = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += u;
   }
   if (lane == 31) warp_sum[warp] = inc;
-  const bool none = __syncthreads_or(back);
-  long long start = inc - mine, total = 0;
+  const bool none = __syncthreads_or(refuse);
+  int start = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) start += warp_sum[w];
-    total += warp_sum[w];
+    const int x = warp_sum[w];
+    if (w < warp) start += x;
+    total += x;
   }
   if (none) total = 0;
-  const long long most = (total + kLeastRun - 1) / kLeastRun;
-  const int parts = (int)max(1ll, min((long long)gridDim.x, most)), c = blockIdx.x;
-  const bool works = c < parts && total > 0;
-  const long long x0 = works ? mul_div(total, c, parts) : 0, x1 = works ? mul_div(total, c + 1, parts) : 0;
+  const int parts = max(1, min((int)gridDim.x, (total + kLeastRun - 1) / kLeastRun)), c = blockIdx.x;
+  int x0 = 0, x1 = 0;
+  if (c < parts) {
+    x0 = part_of(total, c, parts);
+    x1 = part_of(total, c + 1, parts);
+  }
   if (tid == 0) {
     out->total = total;
     out->parts = parts;
@@ -278,16 +298,18 @@ __device__ __forceinline__ void stream_run(const Params &p, long long *warp_sum,
   }
   if (x0 < x1 && start <= x0 && x0 < start + mine) {
     int b = b0;
-    long long per_head = 0;
-    for (;; ++b) {
-      if (each > 1) r = request_of(p.lens, b, nullptr);
-      per_head = request_cost(p, r);
-      if (x0 < start + per_head * p.Hk) break;
-      start += per_head * p.Hk;
-    }
-    const int h = (int)mul_div(x0 - start, 1, per_head);
-    start += h * per_head;
+    if (each > 1)
+#pragma unroll 1
+      for (;; ++b) {
+        r = request_of(p.lens, b, nullptr);
+        per_head = request_cost(p, r);
+        if (x0 < start + (int)per_head * p.Hk) break;
+        start += (int)per_head * p.Hk;
+      }
+    const int h = (unsigned)(x0 - start) / (unsigned)per_head;
+    start += h * (int)per_head;
     int t = 0;
+#pragma unroll 1
     for (int u; start + (u = unit_cost(p, r, t)) <= x0; ++t) start += u;
     out->b = b;
     out->h = h;
@@ -311,7 +333,9 @@ struct StreamWalk {
       const int nt = min(tq, r.req.q - r.t * tq), pos0 = r.req.kv - r.req.q + r.t * tq;
       const TileRange u = unit_tiles(pos0, nt, r.req.kv, 128, p.causal, p.window);
       const int tiles = u.e - u.a;
-      const int from = (int)max(0ll, r.x0 - r.u0), to = (int)min((long long)tiles, r.x1 - r.u0);
+      // a tile belongs to the run that holds its start (runs are longer than a tile)
+      const int cost = nt > p.tq1 ? kTileCost2 : kTileCost1;
+      const int from = r.x0 > r.u0 ? (r.x0 - r.u0 + cost - 1) / cost : 0, to = min(tiles, (r.x1 - r.u0 + cost - 1) / cost);
       found = from < to || (tiles == 0 && from == 0);
       if (found) {
         it.b = r.b;
@@ -327,9 +351,9 @@ struct StreamWalk {
         it.slot = whole ? -1 : 2 * (int)blockIdx.x + (from == 0 ? 1 : 0);
         if (!whole && from == 0) {
           // the CTA that holds the unit's last tile: the last c with total * c / parts <= its place
-          const long long end = r.u0 + tiles;
+          const int end = r.u0 + (tiles - 1) * cost + 1;  // one past that tile's start
           const int last = r.total < (1 << 24) ? (int)(((unsigned)end * (unsigned)r.parts - 1u) / (unsigned)r.total)
-                                               : (int)((end * r.parts - 1) / r.total);
+                                               : (int)(((long long)end * r.parts - 1) / r.total);
           SeqsMerge m;
           m.h = r.h;
           m.nt = nt;
@@ -343,7 +367,7 @@ struct StreamWalk {
           merge_told = true;
         }
       }
-      r.u0 += tiles + kUnitCost;
+      r.u0 += tiles * cost + (nt > p.tq1 ? kUnitCost2 : kUnitCost1);
       if (++r.t * tq >= r.req.q) {
         r.t = 0;
         if (++r.h == p.Hk) {
@@ -366,10 +390,20 @@ struct StreamWalk {
   }
 };
 
-template <typename E, int D>
+// The rest of a wait that did not succeed at once.  Out of line and of few arguments (parity, role,
+// barrier and tag in one word): the kernel has dozens of waits.
+template <typename C>
+__device__ __noinline__ bool wait_more(const Params &p, uint32_t base, uint32_t what) {
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(__cvta_shared_to_generic(base + C::offAbort));
+  const uint32_t i = (what >> 16) & 0xffu;
+  return wait_phase_slow(base + (uint32_t)C::offBar + 8 * i, what >> 31, abort_flag, p.timeout_ns, p.err,
+                         (what >> 24) & 0x7fu, wtag((int)i, (int)(what & 0xffffu)));
+}
+
+template <typename E, int D, bool GROUPED, bool STREAM>
 __global__ void __launch_bounds__(kThreads, 1)
     seqs_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  using C = Cfg<E, D>;
+  using C = Cfg<E, D, GROUPED>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -380,7 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return base + (uint32_t)(C::offBar + 8 * i); };
   auto wait = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
-    return wait_phase(bar(i), parity, abort_flag, p.timeout_ns, p.err, code, wtag(i, tag));
+    if (mbar_test(bar(i), parity)) return true;
+    return wait_more<C>(p, base, parity << 31 | code << 24 | (unsigned)i << 16 | ((unsigned)tag & 0xffffu));
   };
 
   if (threadIdx.x == 0) {
@@ -404,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the work list, and whatever the caller's earlier kernels wrote
   pdl_trigger();
   StreamRun *run_of_cta = reinterpret_cast<StreamRun *>(gbase + C::offStat + 128);
-  if (p.stream) stream_run(p, reinterpret_cast<long long *>(gbase + C::offStat), run_of_cta);
+  if constexpr (STREAM) stream_run(p, reinterpret_cast<int *>(gbase + C::offStat), run_of_cta);
 
   // A wait of a whole warp of which one lane polls: 32 polling lanes take the time of 32 tests.
   auto wait_warp = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
@@ -415,9 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A wait that may last as long as a piece of work, by a warp whose polling would take issue
   // slots from the softmax warps: it sleeps between looks.  (One thread.)
   auto wait_long = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
+#pragma unroll 1
     for (int look = 0; look < 20000; ++look) {
       if (mbar_test(bar(i), parity)) return true;
-      __nanosleep(100);
+      if (look > 16) __nanosleep(100);
     }
     return wait(i, parity, code, tag);
   };
@@ -480,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < boxes) {
             const uint32_t dst = base + C::offKV + st * C::kTile;
             const CUtensorMap *tm = w ? &maps.v : &maps.k;
-            if (p.grouped) {
+            if constexpr (GROUPED) {
               tma_load_5d(dst + pg * p.box_rows * 128 * C::PN, tm, bar(C::KVFull + st), 0, 0, 0, page * p.page_groups, it.h);
             } else if (boxes == 1) {
               tma_load_5d(dst, tm, bar(C::KVFull + st), 0, row, 0, it.h, page);
@@ -511,20 +547,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutProducer, ok, it); ++k) {
       const int tiles = tiles_of(it);
       if (tiles == 0) continue;
-      if (loads > 0 && lane == 0) ok = wait_long(C::QEmpty, (loads - 1) & 1u, kDevErrTimeoutProducer, (int)k);  // the last piece's S MMAs
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      if (!ok) break;
       const int nq = it.nt > p.tq1 ? 2 : 1;
       if (lane == 0) {
-        for (int t = 0; t < nq; ++t) {
+        for (int t = 0; t < nq && ok; ++t) {
+          const uint32_t before = t ? loads1 : loads;
+          // the last S MMA on the tile's earlier contents
+          if (before > 0) ok = wait_long(C::QEmpty + t, (before - 1) & 1u, kDevErrTimeoutProducer, (int)k);
+          if (!ok) break;
           mbar_expect_tx(bar(C::QFull + t), q_bytes);
           for (int pn = 0; pn < C::PN; ++pn)
             tma_load_3d(base + C::offQ + t * C::kTile + pn * kPanel, &maps.q, bar(C::QFull + t), pn * 64, it.h * p.group,
                         it.qrow0 + t * p.tq1);
+          if (t) ++loads1; else ++loads;
         }
       }
-      ++loads;
-      loads1 += nq - 1;
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (!ok) break;
       n += 2 * tiles;
       const int valid = it.kv - (it.key0 + (tiles - 1) * 128);  // rows of the last tile that are the request's
       if (valid < 128) {
@@ -540,16 +578,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         uint8_t *tile = gbase + C::offKV + st * C::kTile;
         for (int x = valid * 8 + lane; x < 128 * 8; x += 32) {  // 16-byte words of a panel: 64 a group of 8 keys
-          uint8_t *at = tile + (x >> 6) * p.group_step + (x & 63) * 16;
+          uint8_t *at = tile + (x >> 6) * C::kGroupStep + (x & 63) * 16;
 #pragma unroll
-          for (int pn = 0; pn < C::PN; ++pn) *reinterpret_cast<uint4 *>(at + pn * p.panel_step) = make_uint4(0u, 0u, 0u, 0u);
+          for (int pn = 0; pn < C::PN; ++pn) *reinterpret_cast<uint4 *>(at + pn * C::kPanelStep) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::VFix));
       }
     }
-    if (!ok) {
+    if (!ok && lane == 0) {
       if (loads > 0)
         wait_phase(bar(C::QFull), (loads - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain, wtag(C::QFull, 0));
       if (loads1 > 0)
@@ -562,8 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // for it: descriptors are sums of constants and a stage's offset (the address field of a
     // descriptor does not carry), ring positions are stepped, not divided.
     const uint32_t q_lo = ((base + C::offQ) >> 4) | (1u << 16), k_lo = ((base + C::offKV) >> 4) | (1u << 16);
-    const uint32_t panel = (uint32_t)p.panel_step >> 4, group = (uint32_t)p.group_step >> 4;
-    const uint32_t v_lo = ((base + C::offKV) >> 4) | (panel << 16);
+    const uint32_t v_lo = ((base + C::offKV) >> 4) | ((uint32_t)(C::kPanelStep >> 4) << 16);
     int kst = 0;                      // ring stage of the next K tile, and its phase
     uint32_t kph = 0;
     uint32_t loads = 0, loads1 = 0;   // Q tiles 0 and 1 used
@@ -571,24 +608,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t fixes = 0;
     bool ok = true;
     SeqsItem it;
+    auto mma_s = [&](int g, int qt, int st) {
+      mma_scores<C>(tmem + g * 128, q_lo + (uint32_t)(qt * (C::kTile >> 4)), k_lo + (uint32_t)(st * (C::kTile >> 4)),
+                    bar(C::SFull + g));
+    };
+    auto mma_pv = [&](int g, bool first, int st) {
+      mma_output<C>(tmem + 256 + g * 128, tmem + g * 128, v_lo + (uint32_t)(st * (C::kTile >> 4)), !first);
+    };
+    auto next = [](int &st, uint32_t &ph) {
+      if (++st == C::NS) {
+        st = 0;
+        ph ^= 1u;
+      }
+    };
     for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutMma, ok, it); ++k) {
       if (lane == 0 && tiles_of(it) > 0) {
         const int tiles = tiles_of(it);
         const bool dual = it.nt > p.tq1;
         const bool ragged = it.kv - (it.key0 + (tiles - 1) * 128) < 128;  // rows of the last tile are not the request's
-        auto next = [](int &st, uint32_t &ph) {
-          if (++st == C::NS) {
-            st = 0;
-            ph ^= 1u;
-          }
-        };
-        auto mma_s = [&](int g, int qt, int st) {
-          mma_scores<C>(tmem + g * 128, q_lo + (uint32_t)(qt * (C::kTile >> 4)), k_lo + (uint32_t)(st * (C::kTile >> 4)),
-                        panel, group, bar(C::SFull + g));
-        };
-        auto mma_pv = [&](int g, bool first, int st) {
-          mma_output<C>(tmem + 256 + g * 128, tmem + g * 128, v_lo + (uint32_t)(st * (C::kTile >> 4)), group, !first);
-        };
         // V of the piece's tile j has landed; the rows past the request's end in its last one are zero
         auto v_ready = [&](int j, int st, uint32_t ph) -> bool {
           if (!wait(C::KVFull + st, ph, kDevErrTimeoutMma, j)) return false;
@@ -605,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             mma_s(0, 0, kst);
+            if (j == tiles - 1) mma_commit(bar(C::QEmpty));
             if (j > 0) {
               ok = wait(C::PReady + 1, steps1++ & 1u, kDevErrTimeoutMma, j);
               if (!ok) break;
@@ -618,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_s(1, 1, kst);
             mma_commit(bar(C::KVEmpty + kst));
-            if (j == tiles - 1) mma_commit(bar(C::QEmpty));
+            if (j == tiles - 1) mma_commit(bar(C::QEmpty + 1));
             next(kst, kph);
             vst = kst;
             vph = kph;
@@ -675,17 +713,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ work
     if (lane == 0) {
-      const unsigned n_items = p.stream ? 0u : p.counters[1];
+      unsigned n_items = 0;
       StreamWalk walk;
-      walk.merge_told = false;
-      if (p.stream) walk.r = *run_of_cta;
+      if constexpr (STREAM) {
+        walk.merge_told = false;
+        walk.r = *run_of_cta;
+      } else {
+        n_items = p.counters[1];
+      }
       bool more = true;
       for (uint32_t k = 0; more; ++k) {
         // a piece is claimed when the producer is nearly through with the one before, not earlier:
         // claimed ahead, pieces would wait behind a long one while other CTAs run dry
         if (k > 0 && !wait_long(C::Want, (k - 1) & 1u, kDevErrTimeoutProducer, (int)k)) break;
         SeqsItem it;
-        if (p.stream) {
+        if constexpr (STREAM) {
           more = walk.next(p, it);
         } else {
           const unsigned e = atomicAdd(&p.counters[0], 1u);
@@ -701,133 +743,155 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax groups
+    // The tile loop needs most of the registers, so what only a piece's start and end use is taken
+    // from the item ring again (its slot is given back at the end) or computed again.
     const int g = (warp - 4) >> 2;  // group
     const int wq = warp & 3;        // TMEM lane quarter of this warp
-    const int r = wq * 32 + lane;   // row of the tile
-    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + (uint32_t)(g * 128);
-    const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(g * 128);
-    float2 *stat = reinterpret_cast<float2 *>(gbase + C::offStat);
-    const int tok = r / p.group, hd = r - tok * p.group;              // this row's token and head
-    const int tok0 = (wq * 32) / p.group, tok1 = (wq * 32 + 31) / p.group;  // tokens of the warp's rows
-    const bool row_used = tok < p.tq1;
+    const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(g * 128), tO = tS + 256u;
     uint32_t steps = 0, pieces0 = 0, pieces1 = 0, singles = 0;  // phases: S steps, O-done of both groups, Stat / EpiDone
     bool ok = true;
-    SeqsItem it;
-    for (uint32_t k = 0; next_item(k, kDevErrTimeoutSoftmax, ok, it); ++k) {
-      const int tiles = tiles_of(it);
+    for (uint32_t k = 0;; ++k) {
+      const int slot = (int)(k & 1u);
+      volatile const SeqsItem &it = item_ring[slot];
+      if (lane == 0) ok = wait_long(C::ItemFull + slot, (k >> 1) & 1u, kDevErrTimeoutSoftmax, (int)k);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+      if (!ok || it.b < 0) break;
+      const int key0 = it.key0, key1 = it.key1;
+      const int tiles = key1 > key0 ? (key1 - key0 + 127) >> 7 : 0;
       const bool dual = it.nt > p.tq1;
       const int nsub = dual ? 2 * tiles : tiles;
       const int mine = (nsub - g + 1) >> 1;  // steps of this group
-      const int first_tok = dual ? g * p.tq1 : 0;
-      const int left = min(p.tq1, it.nt - first_tok);  // tokens of this group's row tile
-      const bool active = tok0 < left;                 // some row of this warp is a token's
-      const bool row_ok = row_used && tok < left;
-      const int pos = it.pos0 + first_tok + tok;
-      int lo = 0, hi = 0;
-      if (row_ok) seen_keys(pos, it.kv, p.causal, p.window, lo, hi);
-      // what every (used) row of the warp sees, for the tiles that need no mask
-      int max_lo, min_hi, unused;
-      seen_keys(it.pos0 + first_tok + min(tok1, left - 1), it.kv, p.causal, p.window, max_lo, unused);
-      seen_keys(it.pos0 + first_tok + tok0, it.kv, p.causal, p.window, unused, min_hi);
-      // a row that is no token's holds whatever its memory held: its max never asks for a rescale,
-      // which the whole warp would take part in
-      float run = row_ok ? -INFINITY : INFINITY;
-      float l[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < mine; ++i) {
-        ok = ok && wait(C::SFull + g, (steps + (uint32_t)i) & 1u, kDevErrTimeoutSoftmax, i);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (active) {
-          const int kb = it.key0 + (dual ? i : 2 * i + g) * 128;
-          if (kb < max_lo || kb + 128 > min_hi) mask_rows(tS, kb, lo, hi, max_lo, min_hi);
-          softmax_online_tile<E, D>(tS, tO, p.alpha, i > 0, run, l);
-          tmem_st_wait();
+      float run, l[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        const int first_tok = dual ? g * p.tq1 : 0;
+        const int left = min(p.tq1, it.nt - first_tok);  // tokens of this group's row tile
+        const int tok0 = wq * 32 / p.group, tok1 = (wq * 32 + 31) / p.group;  // tokens of the warp's rows
+        const int tok = (wq * 32 + opaque_laneid()) / p.group;
+        const bool row_ok = tok < left;
+        const int pos = it.pos0 + first_tok, kv = it.kv;
+        int lo = 0, hi = 0;
+        if (row_ok) seen_keys(pos + tok, kv, p.causal, p.window, lo, hi);
+        // what every (used) row of the warp sees, for the tiles that need no mask
+        int max_lo, min_hi, unused;
+        seen_keys(pos + min(tok1, left - 1), kv, p.causal, p.window, max_lo, unused);
+        seen_keys(pos + tok0, kv, p.causal, p.window, unused, min_hi);
+        // a row that is no token's holds whatever its memory held: its max never asks for a rescale,
+        // which the whole warp would take part in
+        run = row_ok ? -INFINITY : INFINITY;
+        if (tok0 >= left) min_hi = INT_MIN;  // no row of this warp is a token's
+        int kb = key0 + (dual ? 0 : g * 128);
+        const int kstep = dual ? 128 : 256;
+        for (int i = 0; i < mine; ++i, kb += kstep) {
+          ok = wait(C::SFull + g, (steps + (uint32_t)i) & 1u, kDevErrTimeoutSoftmax, i);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (min_hi != INT_MIN) {
+            if (kb < max_lo || kb + 128 > min_hi) mask_rows(tS, kb, lo, hi, max_lo, min_hi);
+            softmax_online_tile<E, D, 1>(tS, tO, p.alpha, i > 0, run, l);
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          mbar_arrive(bar(C::PReady + g));
         }
-        tc_fence_before();
-        mbar_arrive(bar(C::PReady + g));
       }
       steps += (uint32_t)mine;
-      float lsum = (l[0] + l[1]) + (l[2] + l[3]);
-      // what the sums carry: 2^(bias - run) (see p_bias)
+      float lsum = (l[0] + l[1]) + (l[2] + l[3]);  // carries 2^(bias - run) (see p_bias)
+      float2 *stat = reinterpret_cast<float2 *>(gbase + C::offStat) + wq * 32 + lane;
       if (!dual && g == 1) {
         // the other group joins the two results: it needs this group's max and sums, and O1 until
         // it says that it has read it
-        stat[r] = make_float2(run, lsum);
+        *stat = make_float2(run, lsum);
         mbar_arrive(bar(C::Stat));
         ok = ok && wait(C::EpiDone, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        pieces0 += nsub > 0;
-        pieces1 += nsub > 1;
-        ++singles;
-        continue;
+      } else {
+        float c0 = 1.f, c1 = 0.f;
+        if (mine > 0) ok = ok && wait(C::ODone + g, (g ? pieces1 : pieces0) & 1u, kDevErrTimeoutSoftmax, (int)k);
+        if (!dual) {
+          // (group 1's arrival also says that it has seen O1 of its earlier pieces done, so that the
+          // phase waited for next is the one after those)
+          ok = ok && wait(C::Stat, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
+          if (nsub > 1) ok = ok && wait(C::ODone + 1, pieces1 & 1u, kDevErrTimeoutSoftmax, (int)k);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (!dual) {
+          const float2 o = *stat;
+          const float m = fmaxf(run, o.x);
+          c0 = run == -INFINITY ? 0.f : ex2(run - m);
+          c1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
+          lsum = lsum * c0 + o.y * c1;
+          run = m;
+        }
+        const int first_tok = dual ? g * p.tq1 : 0;
+        const int left = min(p.tq1, it.nt - first_tok);
+        const int r = wq * 32 + opaque_laneid(), tok = r / p.group, hd = r - tok * p.group;
+        const bool row_ok = tok < left;
+        if (wq * 32 / p.group < left) {
+          const int part = it.slot;
+          const bool whole = part < 0;
+          const float inv = !whole ? 1.f : (lsum == 0.f ? 0.f : 1.0f / lsum);  // no key seen: zeros, lse = -inf
+          const float s0 = c0 * inv, s1 = c1 * inv;
+          const int64_t qrow = (int64_t)it.qrow0 + first_tok + tok;
+          const int head = it.h * p.group + hd;
+          const int64_t slot_row = (int64_t)part * p.slot_rows + (first_tok + tok) * p.group + hd;
+          const bool f32 = !whole || p.out_f32;
+          uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) + (head * p.osH + qrow * p.osS) * (p.out_f32 ? 4 : 2)
+                               : reinterpret_cast<uint8_t *>(p.part_o + slot_row * D);
+          uint8_t *row[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned long long d = __shfl_sync(0xffffffffu, row_ok ? reinterpret_cast<unsigned long long>(dst) : 0ull,
+                                                     (lane & ~3) + i);
+            row[i] = d ? reinterpret_cast<uint8_t *>(d) + (lane & 3) * 16 : nullptr;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float x[32];
+            if (tiles == 0) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = 0.f;
+            } else {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * s0;
+              if (!dual) {
+                // (a group that saw no key of its own: its O is not a number's to scale)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = c0 == 0.f ? 0.f : x[e];
+                if (nsub > 1) {
+                  tmem_ld32(tO + 128 + c * 32, o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) x[e] = c1 == 0.f ? x[e] : fmaf(__uint_as_float(o[e]), s1, x[e]);
+                }
+              }
+            }
+            if (!f32) store_rows16<E>(row, c * 64, x, lane);
+            else if (row_ok) store_row32(dst + c * 128, x);
+          }
+          if (row_ok) {
+            // acc = sum 2^(z - run + bias): the bias leaves o as it is and comes off the log
+            const float mx = run == -INFINITY ? run : run - p_bias<E>();
+            if (!whole) p.part_ml[slot_row] = make_float2(mx, lsum);
+            else if (p.lse)
+              p.lse[head * p.T + qrow] = lsum == 0.f ? -INFINITY : 0.69314718055994531f * (mx + log2f(lsum));
+          }
+        }
+        if (!dual) {
+          tc_fence_before();
+          mbar_arrive(bar(C::EpiDone));
+        }
       }
-      float c0 = 1.f, c1 = 0.f;
-      if (mine > 0) ok = ok && wait(C::ODone + g, (g ? pieces1 : pieces0) & 1u, kDevErrTimeoutSoftmax, (int)k);
-      if (!dual) {
-        // (group 1's arrival also says that it has seen O1 of its earlier pieces done, so that the
-        // phase waited for next is the one after those)
-        ok = ok && wait(C::Stat, singles & 1u, kDevErrTimeoutSoftmax, (int)k);
-        if (nsub > 1) ok = ok && wait(C::ODone + 1, pieces1 & 1u, kDevErrTimeoutSoftmax, (int)k);
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
       pieces0 += nsub > 0;
       pieces1 += nsub > 1;
-      if (!dual) {
-        const float2 o = stat[r];
-        const float m = fmaxf(run, o.x);
-        c0 = run == -INFINITY ? 0.f : ex2(run - m);
-        c1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
-        lsum = lsum * c0 + o.y * c1;
-        run = m;
-        ++singles;
-      }
-      if (active) {
-        const bool whole = it.slot < 0;
-        const float inv = !whole ? 1.f : (lsum == 0.f ? 0.f : 1.0f / lsum);  // no key seen: zeros, lse = -inf
-        const float s0 = c0 * inv, s1 = c1 * inv;
-        const int64_t qrow = (int64_t)it.qrow0 + first_tok + tok;
-        const int head = it.h * p.group + hd;
-        const int64_t slot_row = (int64_t)it.slot * p.slot_rows + (first_tok + tok) * p.group + hd;
-        const bool f32 = !whole || p.out_f32;
-        uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) + (head * p.osH + qrow * p.osS) * (p.out_f32 ? 4 : 2)
-                             : reinterpret_cast<uint8_t *>(p.part_o + slot_row * D);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float x[32];
-          if (mine > 0) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = c0 == 0.f ? 0.f : __uint_as_float(o[e]) * s0;
-            if (!dual && nsub > 1) {
-              tmem_ld32(tO + 128 + c * 32, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = c1 == 0.f ? x[e] : fmaf(__uint_as_float(o[e]), s1, x[e]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = 0.f;
-          }
-          if (!f32) store_rows16<E>(dst + c * 64, row_ok, x, lane);
-          else if (row_ok) store_row32(dst + c * 128, x);
-        }
-        if (row_ok) {
-          // acc = sum 2^(z - run + bias): the bias leaves o as it is and comes off the log
-          const float mx = run == -INFINITY ? run : run - p_bias<E>();
-          if (!whole) p.part_ml[slot_row] = make_float2(mx, lsum);
-          else if (p.lse)
-            p.lse[head * p.T + qrow] = lsum == 0.f ? -INFINITY : 0.69314718055994531f * (mx + log2f(lsum));
-        }
-      }
-      if (!dual) {
-        tc_fence_before();
-        mbar_arrive(bar(C::EpiDone));
-      }
+      singles += dual ? 0 : 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::ItemEmpty + slot));
     }
   }
 
@@ -904,19 +968,26 @@ bool rows16(const View &x, int64_t es) {
   return x.sD == 1 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && ok(x.sS, x.S) && ok(x.sH, x.H) && ok(x.sB, x.B);
 }
 
-template <typename E, int D>
+template <typename E, int D, bool GROUPED, bool STREAM>
 cudaError_t launch_typed(const Maps &maps, const Params &p, cudaStream_t st) {
+  constexpr int smem = Cfg<E, D, GROUPED>::kSmem;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(seqs_tc_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<E, D>::kSmem);
+    e = cudaFuncSetAttribute(seqs_tc_kernel<E, D, GROUPED, STREAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_pdl(seqs_tc_kernel<E, D>, dim3((unsigned)current_device_sm_count()), dim3(kThreads), Cfg<E, D>::kSmem, st,
-                    maps, p);
+  return launch_pdl(seqs_tc_kernel<E, D, GROUPED, STREAM>, dim3((unsigned)current_device_sm_count()), dim3(kThreads), smem,
+                    st, maps, p);
+}
+template <typename E, int D>
+cudaError_t launch_dim(const Maps &maps, const Params &p, bool grouped, bool stream, cudaStream_t st) {
+  if (grouped)
+    return stream ? launch_typed<E, D, true, true>(maps, p, st) : launch_typed<E, D, true, false>(maps, p, st);
+  return stream ? launch_typed<E, D, false, true>(maps, p, st) : launch_typed<E, D, false, false>(maps, p, st);
 }
 
 }  // namespace
@@ -954,12 +1025,10 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.tq1 = g.tq / 2;
   p.box_rows = a.paged && a.k.S < 128 ? (int)a.k.S : 128;
   const int64_t groups = p.box_rows < 128 ? page_groups(a.k) : 0;
-  p.grouped = groups > 0 && groups == page_groups(a.v);
+  const bool grouped = groups > 0 && groups == page_groups(a.v);
   p.page_groups = (int)groups;
-  p.panel_step = p.grouped ? 1024 : kPanel;
-  p.group_step = p.grouped ? 1024 * (int)(a.k.D / 64) : 1024;
   if (!encode_q(&maps.q, a.q, p.group, p.tq1) ||
-      !(p.grouped ? encode_pages(&maps.k, a.k) && encode_pages(&maps.v, a.v)
+      !(grouped ? encode_pages(&maps.k, a.k) && encode_pages(&maps.v, a.v)
                   : encode_kv(&maps.k, a.k, p.box_rows) && encode_kv(&maps.v, a.v, p.box_rows)))
     return cudaErrorNotSupported;
   p.causal = a.causal;
@@ -976,7 +1045,6 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.lens = seqs_lens(a);
   p.n = (int)a.n;
   p.Hk = (int)a.k.H;
-  p.stream = g.stream;
   p.part_o = reinterpret_cast<float *>(ws + s.part_o);
   p.part_ml = reinterpret_cast<float2 *>(ws + s.part_ml);
   p.slot_rows = g.slot_rows;
@@ -989,8 +1057,10 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.err = a.err;
   p.timeout_ns = a.timeout_ns;
   if (a.q.dtype == FM_BF16)
-    return a.q.D == 128 ? launch_typed<__nv_bfloat16, 128>(maps, p, st) : launch_typed<__nv_bfloat16, 64>(maps, p, st);
-  return a.q.D == 128 ? launch_typed<__half, 128>(maps, p, st) : launch_typed<__half, 64>(maps, p, st);
+    return a.q.D == 128 ? launch_dim<__nv_bfloat16, 128>(maps, p, grouped, g.stream, st)
+                        : launch_dim<__nv_bfloat16, 64>(maps, p, grouped, g.stream, st);
+  return a.q.D == 128 ? launch_dim<__half, 128>(maps, p, grouped, g.stream, st)
+                      : launch_dim<__half, 64>(maps, p, grouped, g.stream, st);
 }
 
 }  // namespace fm

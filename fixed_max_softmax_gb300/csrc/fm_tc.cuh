@@ -343,6 +343,15 @@ __host__ __device__ constexpr float p_bias() {
   return std::is_same<T, __half>::value ? 7.0f : 0.0f;
 }
 
+// The lane index, read where it is used: arithmetic on it cannot be hoisted out of an enclosing
+// loop (a persistent kernel's start and end of an item, whose lane-dependent values would
+// otherwise stay live across every key tile).
+__device__ __forceinline__ int opaque_laneid() {
+  int l;
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(l));
+  return l;
+}
+
 // p = 2^(alpha*s - bias) for 32 scores of one full chunk, two at a time with fp32x2 FMA and
 // adds; the row sum goes to two pair accumulators, P (T: bf16 or fp16) to 16 packed words
 // pk[OFF..OFF+16).
@@ -440,8 +449,8 @@ __device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (
 // of its rows needs it and the other rows use a scale of 1.  Columns to leave out (past the
 // chunk's end, key sinks) hold -inf (mask_tile): they drop out of the max and give p = 0;
 // while every key so far was left out, run stays -inf and the shift used is 0.  HD: the columns
-// of O.
-template <typename T = __nv_bfloat16, int HD = 128>
+// of O; UNROLL_O: blocks of 32 of them in the rescale's unrolled body.
+template <typename T = __nv_bfloat16, int HD = 128, int UNROLL_O = 4>
 __device__ __forceinline__ void softmax_online_tile(uint32_t tS, uint32_t tO, float alpha, bool have_o, float &run,
                                                     float (&l)[4]) {
   float mx;
@@ -472,7 +481,7 @@ __device__ __forceinline__ void softmax_online_tile(uint32_t tS, uint32_t tO, fl
   }
   softmax_fixed_tile<false, T>(tS, alpha, run == -INFINITY ? 0.f : -(run - p_bias<T>()), l);
   if (any && have_o) {
-#pragma unroll
+#pragma unroll UNROLL_O
     for (int c = 0; c < HD / 32; ++c) {
       uint32_t o[32];
       tmem_ld32(tO + c * 32, o);
