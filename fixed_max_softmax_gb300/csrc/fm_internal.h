@@ -225,6 +225,7 @@ struct PagedExtendArgs {
   int32_t *free_out, *cu_q;
   int64_t *slots;
   int32_t *positions, *status;
+  int slots_apart = 0;  // the tokens' slots are written by a kernel of their own
 };
 cudaError_t launch_paged_extend(const PagedExtendArgs &a, cudaStream_t st);
 cudaError_t launch_paged_write(const View &k, const View &v, const int64_t *slots, const View &kc, const View &vc,

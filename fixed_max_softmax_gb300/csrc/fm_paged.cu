@@ -7,13 +7,13 @@
 //                     same order, page e of the call being free[count + G - 1 - e]
 //   token t of request i at position p = base_i + t - cu_i:  slot = table[i][p / page_size] *
 //                     page_size + p mod page_size
-// One cluster of CTAs does it in one launch: every CTA takes the prefix sums of all requests for
-// itself (12 bytes a request, read through L2), so that the CTAs meet only once, between the last
-// read of the old state and the first write of the new one, which is what allows kv_len,
-// free_count and the rows of reused requests to be updated in place.  A token's page is taken
-// from the free list by its rank, not from the table that another CTA is writing.  Bound by the
-// latency of a few dependent loads up to some thousand tokens, then by the 12 bytes a token that
-// it writes.
+// One cluster of CTAs moves the pages: every CTA takes the prefix sums of all requests for itself
+// (12 bytes a request, read through L2), so that the CTAs meet only once, between the last read of
+// the old state and the first write of the new one, which is what allows kv_len, free_count and the
+// rows of reused requests to be updated in place.  Up to 4,096 tokens the same CTA writes their
+// slots, a token's page taken from the free list by its rank; beyond that a second kernel over the
+// whole GPU does, from the finished table (336,704 tokens of 96 requests: 29.8 us by the cluster
+// alone).  Bound by the latency of a few dependent loads, then by the 12 bytes a token.
 //
 // fm_paged_write: a copy of rows to their slots, bound by HBM (each row read and written once).
 #include <cuda_bf16.h>
@@ -57,6 +57,56 @@ __device__ __forceinline__ Sums shfl_up(const Sums &a, int d) {
 }
 
 __device__ __forceinline__ int pages_of(int x, int ps) { return (int)(((unsigned)x + (unsigned)ps - 1u) / (unsigned)ps); }
+
+// Slots and positions of the T tokens (-1 from there to max_tokens), four to a thread: one search,
+// and most often one page.  request_of(token), start(request), base(request): a request's first
+// token and what it held before, page(request, j): its j-th page.
+template <typename R, typename S, typename B, typename P>
+__device__ __forceinline__ void put_tokens(const PagedExtendArgs &a, int T, int first, int step, R request_of, S start, B base,
+                                           P page) {
+  const long long cap = a.max_tokens;
+  const int ps = (int)a.page_size;
+  for (long long q = first; q * 4 < cap; q += step) {
+    const long long t0 = q * 4;
+    long long slot[4];
+    int pos[4];
+    int i = t0 < T ? request_of((int)t0) : 0;
+    int last_i = -1, end = 0, shift = 0, last_page = -1, pg = 0;  // shift: position of the request's token 0 of this call
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const long long t = t0 + u;
+      slot[u] = -1;
+      pos[u] = -1;
+      if (t < T) {
+        if (last_i < 0 || t >= end) {
+          while (t >= start(i + 1)) ++i;
+          end = start(i + 1);
+          shift = base(i) - start(i);
+          last_page = -1;
+          last_i = i;
+        }
+        const int p = (int)t + shift;
+        const int j = p / ps;
+        if (j != last_page) {
+          pg = page(i, j);
+          last_page = j;
+        }
+        pos[u] = p;
+        slot[u] = (long long)pg * ps + (p - j * ps);
+      }
+    }
+    if (t0 + 4 <= cap && ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0) {
+      *reinterpret_cast<longlong2 *>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2 *>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int u = 0; u < 4 && t0 + u < cap; ++u) {
+        a.slots[t0 + u] = slot[u];
+        a.positions[t0 + u] = pos[u];
+      }
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kExtThreads) paged_extend_kernel(const PagedExtendArgs a) {
   pdl_wait();
@@ -165,44 +215,25 @@ __global__ void __launch_bounds__(kExtThreads) paged_extend_kernel(const PagedEx
     *a.free_out = top - fresh;
     *a.status = status;
   }
-  // four tokens a thread: one search, and most often one page
-  const long long cap = a.max_tokens;
-  for (long long q = g0; q * 4 < cap; q += gstep) {
-    const long long t0 = q * 4;
-    long long slot[4];
-    int pos[4];
-    int i = t0 < T ? owner(tok_pre, n, (int)t0) : n;
-    int last_page = -1, page = 0, last_i = -1;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const long long t = t0 + u;
-      slot[u] = -1;
-      pos[u] = -1;
-      if (t < T) {
-        while (t >= tok_pre[i + 1]) ++i;
-        const int p = base[i] + (int)t - tok_pre[i];
-        const int j = p / ps;
-        if (j != last_page || i != last_i) {
-          const int have = pages_of(base[i], ps);
-          page = j < have ? a.table[i * a.table_stride + j] : a.free_pages[top - 1 - (take_pre[i] + j - have)];
-          last_page = j;
-          last_i = i;
-        }
-        pos[u] = p;
-        slot[u] = (long long)page * ps + (p - j * ps);
-      }
-    }
-    if (t0 + 4 <= cap && ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0) {
-      *reinterpret_cast<longlong2 *>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
-      *reinterpret_cast<longlong2 *>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
-      *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-      for (int u = 0; u < 4 && t0 + u < cap; ++u) {
-        a.slots[t0 + u] = slot[u];
-        a.positions[t0 + u] = pos[u];
-      }
-    }
-  }
+  if (a.slots_apart) return;
+  put_tokens(a, T, g0, gstep, [&](int x) { return owner(tok_pre, n, x); }, [&](int i) { return tok_pre[i]; },
+             [&](int i) { return base[i]; },
+             [&](int i, int j) {
+               const int have = pages_of(base[i], ps);
+               return j < have ? a.table[i * a.table_stride + j] : a.free_pages[top - 1 - (take_pre[i] + j - have)];
+             });
+}
+
+// Slots and positions of many tokens, after the kernel above: its cu_q and lengths say which request
+// and position a token is, its table the page.
+__global__ void __launch_bounds__(256) paged_slots_kernel(const PagedExtendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = (int)a.n;
+  const int32_t *cu = a.cu_q;
+  put_tokens(a, cu[n], blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, [&](int x) { return owner(cu, n, x); },
+             [&](int i) { return cu[i]; }, [&](int i) { return a.kv_out[i] - (cu[i + 1] - cu[i]); },
+             [&](int i, int j) { return a.table[i * a.table_stride + j]; });
 }
 
 // ---------------------------------------------------------------- cache writes
@@ -271,7 +302,8 @@ bool rows16(const View &x, int64_t es) {
 
 }  // namespace
 
-cudaError_t launch_paged_extend(const PagedExtendArgs &a, cudaStream_t st) {
+cudaError_t launch_paged_extend(const PagedExtendArgs &args, cudaStream_t st) {
+  PagedExtendArgs a = args;
   const size_t smem = (size_t)(4 * (a.n + 1)) * 4;
   static bool attr_set[64] = {};  // once per device, so never while a stream is captured after a first call
   int dev = 0;
@@ -282,8 +314,10 @@ cudaError_t launch_paged_extend(const PagedExtendArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  // one CTA for up to 4,096 tokens (one pass of its threads); beyond that a cluster of 8
-  const unsigned ctas = a.max_tokens > 4096 ? 8 : 1;
+  // one CTA for up to 4,096 tokens (one pass of its threads); beyond that a cluster of 8 for the
+  // pages and a kernel of its own for the tokens
+  a.slots_apart = a.max_tokens > 4096 ? 1 : 0;
+  const unsigned ctas = a.slots_apart ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kExtThreads);
@@ -298,7 +332,10 @@ cudaError_t launch_paged_extend(const PagedExtendArgs &a, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, paged_extend_kernel, a);
+  e = cudaLaunchKernelEx(&cfg, paged_extend_kernel, a);
+  if (e != cudaSuccess || !a.slots_apart) return e;
+  const int64_t want = (a.max_tokens + 1023) / 1024, cap = (int64_t)current_device_sm_count() * 8;
+  return launch_pdl(paged_slots_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, a);
 }
 
 cudaError_t launch_paged_write(const View &k, const View &v, const int64_t *slots, const View &kc, const View &vc,

@@ -270,7 +270,7 @@ SeqsGeom seqs_geom_simt(int64_t T, int group) {
   g.slot_rows = (int)(g.tq < T ? g.tq : T) * group;
   g.ctas = 2 * current_device_sm_count();
   g.n_slots = 4 * g.ctas;
-  g.min_tiles = 2;
+  g.min_tiles = 1;
   g.stream = 0;
   return g;
 }
