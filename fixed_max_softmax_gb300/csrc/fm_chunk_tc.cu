@@ -345,6 +345,106 @@ __device__ __noinline__ void mask_tile(uint32_t tS, int nvalid, int g0, const in
   tmem_st_wait();
 }
 
+// Fixed-m softmax of one 128x128 S tile for this thread's row; P overwrites S.  The four
+// 32-column TMEM loads are double-buffered: chunk c+1 is in flight while chunk c is
+// exponentiated.  Key columns to leave out hold -inf (mask_tile) and give p = 0.  P leaves in
+// 16-column stores, one per chunk, or with WIDE (the fixed-m tile loop, which has the
+// registers) in one 32-column store per 64 keys: fewer TMEM stores, measured faster there.
+template <bool WIDE>
+__device__ __forceinline__ void softmax_fixed_tile(uint32_t tS, float alpha, float nbias, float (&l)[4]) {
+  constexpr int NPK = WIDE ? 32 : 16;
+  uint32_t sa[32], sb[32];
+  uint32_t pk[NPK];
+  tmem_ld32_async(tS, sa);
+  tmem_ld_wait(sa);
+  const uint64_t a2 = f2_pack(__float_as_uint(alpha), __float_as_uint(alpha));
+  const uint64_t nb2 = f2_pack(__float_as_uint(nbias), __float_as_uint(nbias));
+  uint64_t acc0 = 0, acc1 = 0;  // +0.0f pairs
+  // P columns [16c, 16c+16) of chunk c lie in S columns already read
+  tmem_ld32_async(tS + 32, sb);
+  exp_chunk_full<__nv_bfloat16, 0>(sa, a2, nb2, acc0, acc1, pk);
+  if constexpr (!WIDE) tmem_st16(tS + 0, pk);
+  tmem_ld_wait(sb);
+  tmem_ld32_async(tS + 64, sa);
+  if constexpr (WIDE) {
+    exp_chunk_full<__nv_bfloat16, 16>(sb, a2, nb2, acc0, acc1, pk);
+    tmem_st32(tS + 0, pk);
+  } else {
+    exp_chunk_full<__nv_bfloat16, 0>(sb, a2, nb2, acc0, acc1, pk);
+    tmem_st16(tS + 16, pk);
+  }
+  tmem_ld_wait(sa);
+  tmem_ld32_async(tS + 96, sb);
+  exp_chunk_full<__nv_bfloat16, 0>(sa, a2, nb2, acc0, acc1, pk);
+  if constexpr (!WIDE) tmem_st16(tS + 32, pk);
+  tmem_ld_wait(sb);
+  if constexpr (WIDE) {
+    exp_chunk_full<__nv_bfloat16, 16>(sb, a2, nb2, acc0, acc1, pk);
+    tmem_st32(tS + 32, pk);
+  } else {
+    exp_chunk_full<__nv_bfloat16, 0>(sb, a2, nb2, acc0, acc1, pk);
+    tmem_st16(tS + 48, pk);
+  }
+  float x0, x1, y0, y1;
+  f2_unpack(acc0, x0, x1);
+  f2_unpack(acc1, y0, y1);
+  l[0] += x0;
+  l[1] += x1;
+  l[2] += y0;
+  l[3] += y1;
+}
+
+// Online softmax of one S tile for this thread's row, in two passes over TMEM: the first
+// takes the row max of the 128 scores (two column halves, 64 registers), the second
+// exponentiates exactly like the fixed-m tile (double-buffered 32-column loads) with the
+// running max as the shift.  The tile max updates the running max `run` (base-2 units)
+// lazily: only when it grows by more than 2^8, or on the first tile.  The row sum is
+// rescaled before the new terms are added, and O in TMEM after P is out.  The rescale
+// decision is per row but tcgen05.ld/st are warp-collective, so the warp rescales when any
+// of its rows needs it and the other rows use a scale of 1.  Columns to leave out (past the
+// chunk's end, key sinks) hold -inf (mask_tile): they drop out of the max and give p = 0;
+// while every key so far was left out, run stays -inf and the shift used is 0.
+__device__ __forceinline__ void softmax_online_tile(uint32_t tS, uint32_t tO, float alpha, bool have_o, float &run,
+                                                    float (&l)[4]) {
+  float mx;
+  {
+    uint32_t sa[32], sb[32];
+    tmem_ld32_async(tS, sa);
+    tmem_ld32_async(tS + 32, sb);
+    tmem_ld_wait(sa);
+    tmem_reg_tie(sb);
+    mx = max64(sa, sb, -INFINITY);
+    tmem_ld32_async(tS + 64, sa);
+    tmem_ld32_async(tS + 96, sb);
+    tmem_ld_wait(sa);
+    tmem_reg_tie(sb);
+    mx = max64(sa, sb, mx);
+  }
+  const float zmax = mx * alpha;
+  const bool need = run == -INFINITY || zmax > run + kLazyRescale;
+  const bool any = __any_sync(0xffffffffu, need);
+  float sc = 1.0f;
+  if (any) {
+    const float nr = need ? fmaxf(run, zmax) : run;
+    // O holds earlier tiles only when j > 0, and nothing but zeros while run is -inf
+    if (have_o && need) sc = run == -INFINITY ? 0.f : ex2(run - nr);
+    run = nr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[i] *= sc;
+  }
+  softmax_fixed_tile<false>(tS, alpha, run == -INFINITY ? 0.f : -run, l);
+  if (any && have_o) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tmem_ld32(tO + c * 32, o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sc);
+      tmem_st32(tO + c * 32, o);
+    }
+  }
+}
+
 // One CTA per work item (grid (pairs, H, B)): the schedule every launch takes unless the
 // persistent one is asked for.
 __global__ void __launch_bounds__(kThreads, 1)

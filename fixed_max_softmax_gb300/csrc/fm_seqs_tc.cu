@@ -68,6 +68,9 @@ struct Cfg {
   static constexpr uint32_t idescQK = idesc_f16(128, 128, false, bf16);  // K [keys, D]: K-major
   static constexpr uint32_t idescPV = idesc_f16(128, D, true, bf16);     // V [keys, D]: MN-major
 };
+// How a call's work is dealt out: even runs cut by the kernel (requests of few queries), the work list,
+// and the work list of long prompts.
+enum : int { kStream, kList, kLong };
 constexpr int kItemReaders = 11;  // arrivals that free an item slot: warps 0, 1, 2 and the 8 softmax warps
 
 struct Maps {
@@ -120,6 +123,68 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
 // The code that runs once a piece (masks, epilogue) is kept in short loops: straight-line code that
 // is not in the instruction cache takes longer to fetch than to run (512-token causal prompts:
 // 227 -> 183 us).
+
+// Online softmax of one S tile for this thread's row, as softmax_online_tile, but exponentiating in
+// a loop over the two halves of the columns (LOOPS = 1) for the same reason: 229 -> 211 us for 32
+// prompts of 1,024, a serving step 245 -> 205 us; a run of long tiles without masks between them
+// does better unrolled (LOOPS = 2: 16k dense-shaped 6.0 -> 5.75 ms).
+template <typename E, int D, int LOOPS>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float alpha, bool have_o, float &run, float (&l)[4]) {
+  uint32_t sa[32], sb[32], pk[16];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int h = 0; h < 128; h += 64) {
+    tmem_ld32_async(tS + h, sa);
+    tmem_ld32_async(tS + h + 32, sb);
+    tmem_ld_wait(sa);
+    tmem_reg_tie(sb);
+    mx = max64(sa, sb, mx);
+  }
+  const float zmax = mx * alpha;
+  const bool need = run == -INFINITY || zmax > run + kLazyRescale;
+  const bool any = __any_sync(0xffffffffu, need);
+  float sc = 1.0f;
+  if (any) {
+    const float nr = need ? fmaxf(run, zmax) : run;
+    // O holds earlier tiles only with have_o, and nothing but zeros while run is -inf
+    if (have_o && need) sc = run == -INFINITY ? 0.f : ex2(run - nr);
+    run = nr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[i] *= sc;
+  }
+  const float nbias = run == -INFINITY ? 0.f : -(run - p_bias<E>());
+  const uint64_t a2 = f2_pack(__float_as_uint(alpha), __float_as_uint(alpha));
+  const uint64_t nb2 = f2_pack(__float_as_uint(nbias), __float_as_uint(nbias));
+  uint64_t acc0 = 0, acc1 = 0;
+  tmem_ld32_async(tS, sa);
+#pragma unroll LOOPS
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld_wait(sa);
+    tmem_ld32_async(tS + 64 * h + 32, sb);
+    exp_chunk_full<E, 0>(sa, a2, nb2, acc0, acc1, pk);
+    tmem_st16(tS + 32 * h, pk);  // P columns lie in S columns already read
+    tmem_ld_wait(sb);
+    if (h == 0) tmem_ld32_async(tS + 64, sa);
+    exp_chunk_full<E, 0>(sb, a2, nb2, acc0, acc1, pk);
+    tmem_st16(tS + 32 * h + 16, pk);
+  }
+  float x0, x1, y0, y1;
+  f2_unpack(acc0, x0, x1);
+  f2_unpack(acc1, y0, y1);
+  l[0] += x0;
+  l[1] += x1;
+  l[2] += y0;
+  l[3] += y1;
+  if (any && have_o) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      tmem_ld32(tO + c, sa);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) sa[e] = __float_as_uint(__uint_as_float(sa[e]) * sc);
+      tmem_st32(tO + c, sa);
+    }
+  }
+}
 
 // Bits [0, n) set, for n of any sign.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
@@ -400,7 +465,7 @@ __device__ __noinline__ bool wait_more(const Params &p, uint32_t base, uint32_t 
                          (what >> 24) & 0x7fu, wtag((int)i, (int)(what & 0xffffu)));
 }
 
-template <typename E, int D, bool GROUPED, bool STREAM>
+template <typename E, int D, bool GROUPED, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     seqs_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using C = Cfg<E, D, GROUPED>;
@@ -439,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the work list, and whatever the caller's earlier kernels wrote
   pdl_trigger();
   StreamRun *run_of_cta = reinterpret_cast<StreamRun *>(gbase + C::offStat + 128);
-  if constexpr (STREAM) stream_run(p, reinterpret_cast<int *>(gbase + C::offStat), run_of_cta);
+  if constexpr (MODE == kStream) stream_run(p, reinterpret_cast<int *>(gbase + C::offStat), run_of_cta);
 
   // A wait of a whole warp of which one lane polls: 32 polling lanes take the time of 32 tests.
   auto wait_warp = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {
@@ -715,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       unsigned n_items = 0;
       StreamWalk walk;
-      if constexpr (STREAM) {
+      if constexpr (MODE == kStream) {
         walk.merge_told = false;
         walk.r = *run_of_cta;
       } else {
@@ -727,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // claimed ahead, pieces would wait behind a long one while other CTAs run dry
         if (k > 0 && !wait_long(C::Want, (k - 1) & 1u, kDevErrTimeoutProducer, (int)k)) break;
         SeqsItem it;
-        if constexpr (STREAM) {
+        if constexpr (MODE == kStream) {
           more = walk.next(p, it);
         } else {
           const unsigned e = atomicAdd(&p.counters[0], 1u);
@@ -789,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (min_hi != INT_MIN) {
             if (kb < max_lo || kb + 128 > min_hi) mask_rows(tS, kb, lo, hi, max_lo, min_hi);
-            softmax_online_tile<E, D, 1>(tS, tO, p.alpha, i > 0, run, l);
+            softmax_tile<E, D, MODE == kLong ? 2 : 1>(tS, tO, p.alpha, i > 0, run, l);
             tmem_st_wait();
           }
           tc_fence_before();
@@ -968,7 +1033,7 @@ bool rows16(const View &x, int64_t es) {
   return x.sD == 1 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && ok(x.sS, x.S) && ok(x.sH, x.H) && ok(x.sB, x.B);
 }
 
-template <typename E, int D, bool GROUPED, bool STREAM>
+template <typename E, int D, bool GROUPED, int MODE>
 cudaError_t launch_typed(const Maps &maps, const Params &p, cudaStream_t st) {
   constexpr int smem = Cfg<E, D, GROUPED>::kSmem;
   static bool attr_set[64] = {};
@@ -976,18 +1041,21 @@ cudaError_t launch_typed(const Maps &maps, const Params &p, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(seqs_tc_kernel<E, D, GROUPED, STREAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(seqs_tc_kernel<E, D, GROUPED, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_pdl(seqs_tc_kernel<E, D, GROUPED, STREAM>, dim3((unsigned)current_device_sm_count()), dim3(kThreads), smem,
+  return launch_pdl(seqs_tc_kernel<E, D, GROUPED, MODE>, dim3((unsigned)current_device_sm_count()), dim3(kThreads), smem,
                     st, maps, p);
 }
 template <typename E, int D>
-cudaError_t launch_dim(const Maps &maps, const Params &p, bool grouped, bool stream, cudaStream_t st) {
-  if (grouped)
-    return stream ? launch_typed<E, D, true, true>(maps, p, st) : launch_typed<E, D, true, false>(maps, p, st);
-  return stream ? launch_typed<E, D, false, true>(maps, p, st) : launch_typed<E, D, false, false>(maps, p, st);
+cudaError_t launch_dim(const Maps &maps, const Params &p, bool grouped, int mode, cudaStream_t st) {
+  if (grouped) {
+    if (mode == kStream) return launch_typed<E, D, true, kStream>(maps, p, st);
+    return launch_typed<E, D, true, kList>(maps, p, st);
+  }
+  if (mode == kStream) return launch_typed<E, D, false, kStream>(maps, p, st);
+  return mode == kList ? launch_typed<E, D, false, kList>(maps, p, st) : launch_typed<E, D, false, kLong>(maps, p, st);
 }
 
 }  // namespace
@@ -1056,11 +1124,13 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.T = a.q.S;
   p.err = a.err;
   p.timeout_ns = a.timeout_ns;
+  // packed prompts of more than 8,192 queries each on average: 64 and more key tiles a piece
+  const int mode = g.stream ? kStream : (!a.paged && a.q.S > 8192 * a.n ? kLong : kList);
   if (a.q.dtype == FM_BF16)
-    return a.q.D == 128 ? launch_dim<__nv_bfloat16, 128>(maps, p, grouped, g.stream, st)
-                        : launch_dim<__nv_bfloat16, 64>(maps, p, grouped, g.stream, st);
-  return a.q.D == 128 ? launch_dim<__half, 128>(maps, p, grouped, g.stream, st)
-                      : launch_dim<__half, 64>(maps, p, grouped, g.stream, st);
+    return a.q.D == 128 ? launch_dim<__nv_bfloat16, 128>(maps, p, grouped, mode, st)
+                        : launch_dim<__nv_bfloat16, 64>(maps, p, grouped, mode, st);
+  return a.q.D == 128 ? launch_dim<__half, 128>(maps, p, grouped, mode, st)
+                      : launch_dim<__half, 64>(maps, p, grouped, mode, st);
 }
 
 }  // namespace fm
