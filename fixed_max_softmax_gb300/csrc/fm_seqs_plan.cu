@@ -5,9 +5,9 @@
 // to cut, and writes one entry per piece of work; the attention kernel's CTAs take entries in
 // order from a counter.  Order: request, key head, range of keys, and the unit of queries
 // running fastest (longest first), so that the CTAs at work at one moment mostly read the same
-// key tiles, from L2.  A unit is cut into equal ranges of keys when it holds more than 1 / 3 of
-// an even share of the work, so that no CTA is left with a long piece at the end; a cut unit's
-// pieces leave unnormalised sums (o, max, sum) that seqs_merge_kernel joins in key order, so the
+// key tiles, from L2.  A unit is cut into equal ranges of keys when it holds more than 2 / 3 of
+// an even share of the work, and long pieces then go first, so that no CTA is left with one at the
+// end; a cut unit's pieces leave unnormalised sums (o, max, sum) that seqs_merge_kernel joins in key order, so the
 // result does not depend on which CTA did what.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
     }
     return;
   }
-  // 2. tiles a piece: a third of an even share, doubled until the partial results fit their space
-  long long cut = max((long long)a.g.min_tiles, (work + 3 * a.g.ctas - 1) / (3 * a.g.ctas));
+  // 2. tiles a piece: two thirds of an even share, doubled until the partial results fit their space
+  long long cut = max((long long)a.g.min_tiles, (2 * work + 3 * a.g.ctas - 1) / (3 * a.g.ctas));
   long long slots, entries;
   for (;; cut *= 2) {
     long long s_carry = 0, e_carry = 0;
@@ -136,72 +136,96 @@ __global__ void __launch_bounds__(kPlanThreads) seqs_plan_kernel(const PlanArgs 
   if (tid == 0) pre[n] = (int)entries;
   __syncthreads();
   // 3. the entries, pieces without keys left out (a unit without any key keeps one).  Where no unit
-  // is cut every entry stays, and none has to be counted.
+  // is cut every entry stays, in order.  Otherwise the pieces go by length, a quarter of the longest
+  // at a time, each quarter in order: long pieces taken last would leave the other CTAs idle.
   const bool all = slots == 0;
   const int n_entries = (int)entries;
-  int n_items = 0, n_merges = 0, n_groups = 0;
+  auto entry = [&](int e, SeqsItem &it, SeqsMerge &mg) -> int {  // quarter of a piece, -1: no keys of it
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= e) lo = mid; else hi = mid;
+    }
+    const int4 r0 = a.req[2 * lo], r1 = a.req[2 * lo + 1];
+    const int nt = r1.x, pieces = r1.z, per = r1.y;
+    int x = e - pre[lo];
+    const int t = nt - 1 - x % nt;
+    x /= nt;
+    const int s = x % pieces, h = x / pieces;
+    it.b = lo;
+    it.h = h;
+    it.nt = min(tq, r0.y - t * tq);
+    it.qrow0 = r0.x + t * tq;
+    it.pos0 = r0.z - r0.y + t * tq;
+    it.kv = r0.z;
+    it.krow0 = r0.w;
+    const TileRange u = unit_tiles(it.pos0, it.nt, it.kv, bk, a.causal, a.window);
+    const int tiles = u.e - u.a;
+    const int mine = max(1, (tiles + per - 1) / per);  // pieces of this unit
+    it.key0 = (u.a + s * per) * bk;
+    it.key1 = tiles > 0 ? min((u.a + min((s + 1) * per, tiles)) * bk, u.hi) : it.key0;
+    const int slot0 = pre[n + 1 + lo] + h * pieces * nt + t;
+    it.slot = mine > 1 ? slot0 + s * nt : -1;
+    it.pad[0] = it.pad[1] = 0;
+    mg.h = h;
+    mg.nt = s == 0 && mine > 1 ? it.nt : 0;  // tokens of a unit to merge, told by its first piece
+    mg.qrow0 = it.qrow0;
+    mg.slot0 = slot0;
+    mg.slot1 = slot0 + nt;
+    mg.stride = nt;
+    mg.nseg = mine;
+    if (s >= mine) return -1;
+    const long long len = min(per, tiles - s * per);
+    return 3 - (int)min(3ll, 4 * len / (cut + 1));
+  };
+  SeqsItem it;
+  SeqsMerge mg;
+  if (all) {
+    for (int e = tid; e < n_entries; e += kPlanThreads) {
+      entry(e, it, mg);
+      a.items[e] = it;
+    }
+    if (tid == 0) {
+      a.counters[0] = a.counters[2] = a.counters[3] = 0;
+      a.counters[1] = (unsigned)n_entries;
+    }
+    return;
+  }
+  // counts of the four quarters, 16 bits each in a scan over 1,024 entries
+  int at[4] = {0, 0, 0, 0}, n_merges = 0, n_groups = 0;
   for (int c0 = 0; c0 < n_entries; c0 += kPlanThreads) {
-    const int e = c0 + tid;
-    bool keep = false, cuts = false;
-    SeqsItem it;
-    SeqsMerge mg;
-    if (e < n_entries) {
-      int lo = 0, hi = n;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= e) lo = mid; else hi = mid;
-      }
-      const int4 r0 = a.req[2 * lo], r1 = a.req[2 * lo + 1];
-      const int nt = r1.x, pieces = r1.z, per = r1.y;
-      int x = e - pre[lo];
-      const int t = nt - 1 - x % nt;
-      x /= nt;
-      const int s = x % pieces, h = x / pieces;
-      it.b = lo;
-      it.h = h;
-      it.nt = min(tq, r0.y - t * tq);
-      it.qrow0 = r0.x + t * tq;
-      it.pos0 = r0.z - r0.y + t * tq;
-      it.kv = r0.z;
-      it.krow0 = r0.w;
-      const TileRange u = unit_tiles(it.pos0, it.nt, it.kv, bk, a.causal, a.window);
-      const int tiles = u.e - u.a;
-      const int mine = max(1, (tiles + per - 1) / per);  // pieces of this unit
-      keep = s < mine;
-      it.key0 = (u.a + s * per) * bk;
-      it.key1 = tiles > 0 ? min((u.a + min((s + 1) * per, tiles)) * bk, u.hi) : it.key0;
-      const int slot0 = pre[n + 1 + lo] + h * pieces * nt + t;
-      it.slot = mine > 1 ? slot0 + s * nt : -1;
-      it.pad[0] = it.pad[1] = 0;
-      cuts = s == 0 && mine > 1;
-      mg.h = h;
-      mg.nt = it.nt;
-      mg.qrow0 = it.qrow0;
-      mg.slot0 = slot0;
-      mg.slot1 = slot0 + nt;
-      mg.stride = nt;
-      mg.nseg = mine;
-    }
-    if (all) {
-      if (e < n_entries) a.items[e] = it;
-      continue;
-    }
-    // one scan of three counts, each below 2^21 in 1,024 entries: entries kept, units cut, and the
-    // cut units' groups of kMergeRows rows
-    const int groups = cuts ? (mg.nt * a.g.group + kMergeRows - 1) / kMergeRows : 0;
+    const int e = c0 + tid, c = e < n_entries ? entry(e, it, mg) : -1;
     long long sum;
-    const long long at = block_scan((keep ? 1ll : 0ll) | (cuts ? 1ll << 21 : 0ll) | ((long long)groups << 42), warp_sum, sum);
-    const int mask = (1 << 21) - 1;
-    if (keep) a.items[n_items + (int)(at & mask)] = it;
-    mg.group0 = n_groups + (int)(at >> 42);
-    if (cuts) a.merges[n_merges + (int)((at >> 21) & mask)] = mg;
-    n_items += (int)(sum & mask);
-    n_merges += (int)((sum >> 21) & mask);
-    n_groups += (int)(sum >> 42);
+    block_scan(c < 0 ? 0ll : 1ll << (16 * c), warp_sum, sum);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) at[i + 1] += (int)((sum >> (16 * i)) & 0xffff);
+    at[0] += (int)((sum >> 48) & 0xffff);
+  }
+  // at[0] has counted the last quarter: the starts follow
+  const int n_items = at[0] + at[1] + at[2] + at[3];
+  at[2] += at[1];
+  at[3] += at[2];
+  at[0] = 0;
+  for (int c0 = 0; c0 < n_entries; c0 += kPlanThreads) {
+    const int e = c0 + tid, c = e < n_entries ? entry(e, it, mg) : -1;
+    long long sum;
+    const long long before = block_scan(c < 0 ? 0ll : 1ll << (16 * c), warp_sum, sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c == i) a.items[at[i] + (int)((before >> (16 * i)) & 0xffff)] = it;
+      at[i] += (int)((sum >> (16 * i)) & 0xffff);
+    }
+    // units cut, and their groups of kMergeRows rows
+    const int groups = c >= 0 && mg.nt > 0 ? (mg.nt * a.g.group + kMergeRows - 1) / kMergeRows : 0;
+    const long long mb = block_scan(groups > 0 ? (1ll << 32) | groups : 0ll, warp_sum, sum);
+    mg.group0 = n_groups + (int)(mb & 0xffffffffll);
+    if (groups > 0) a.merges[n_merges + (int)(mb >> 32)] = mg;
+    n_merges += (int)(sum >> 32);
+    n_groups += (int)(sum & 0xffffffffll);
   }
   if (tid == 0) {
     a.counters[0] = 0;
-    a.counters[1] = (unsigned)(all ? n_entries : n_items);
+    a.counters[1] = (unsigned)n_items;
     a.counters[2] = (unsigned)n_merges;
     a.counters[3] = (unsigned)n_groups;
   }
