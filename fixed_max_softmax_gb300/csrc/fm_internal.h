@@ -207,6 +207,11 @@ struct SeqsSpace {
 SeqsGeom seqs_geom_simt(int64_t T, int group);
 SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group);
 SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_t D);
+// The shared memory that every variant may use; once per device, at its first call: a later call that
+// needs another variant may be inside a stream capture.
+cudaError_t seqs_plan_prepare();
+cudaError_t seqs_simt_prepare();
+cudaError_t seqs_tc_prepare();
 // Work list of the call into its workspace; then one of the attention kernels; then the merge.
 cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 cudaError_t launch_seqs_simt(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);

@@ -51,6 +51,20 @@ size_t space_bytes(int64_t n, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
   return simt > tc ? simt : tc;
 }
 
+// Every attention kernel's attributes, at the first call on the current device.
+cudaError_t prepare() {
+  constexpr int kDevices = 64;
+  static bool ready[kDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < kDevices && ready[dev])) return e;
+  if ((e = seqs_plan_prepare()) != cudaSuccess || (e = seqs_simt_prepare()) != cudaSuccess ||
+      (e = seqs_tc_prepare()) != cudaSuccess)
+    return e;
+  if (dev >= 0 && dev < kDevices) ready[dev] = true;
+  return cudaSuccess;
+}
+
 // The call behind fm_attn_varlen and fm_attn_paged.
 int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
               const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace, size_t workspace_bytes,
@@ -116,6 +130,8 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   a.timeout_ns = wait_timeout_ns();
   if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = prepare();
+  if (e != cudaSuccess) return cuda_fail(e, "preparing the attention kernels");
   // the work list, the attention, the merge of what was cut
   auto run = [&](const SeqsGeom &g, cudaError_t (*attend)(const SeqsArgs &, const SeqsGeom &, const SeqsSpace &, cudaStream_t)) {
     const SeqsSpace s = seqs_space(g, a.n, a.q.S, a.k.H, a.q.D);
@@ -124,7 +140,7 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
     if (e == cudaSuccess) e = launch_seqs_merge(a, g, s, st);
     return e;
   };
-  cudaError_t e = cudaErrorNotSupported;
+  e = cudaErrorNotSupported;
   if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group), launch_seqs_tc);
   // fp32, and layouts that the tensor-core kernel or the tensor-map encoder does not take (a work
   // list made for it then goes unused)

@@ -7,8 +7,8 @@
 // running fastest (longest first), so that the CTAs at work at one moment mostly read the same
 // key tiles, from L2.  A unit is cut into equal ranges of keys when it holds more than 2 / 3 of
 // an even share of the work, and long pieces then go first, so that no CTA is left with one at the
-// end; a cut unit's pieces leave unnormalised sums (o, max, sum) that seqs_merge_kernel joins in key order, so the
-// result does not depend on which CTA did what.
+// end; a cut unit's pieces leave unnormalised sums (o, max, sum) that seqs_merge_kernel joins in key
+// order, so the result does not depend on which CTA did what.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -364,6 +364,10 @@ SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_
   return s;
 }
 
+cudaError_t seqs_plan_prepare() {
+  return cudaFuncSetAttribute(seqs_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kMaxSeqs + 2) * 4);
+}
+
 cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st) {
   uint8_t *ws = static_cast<uint8_t *>(a.ws);
   PlanArgs p;
@@ -379,15 +383,6 @@ cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpa
   p.merges = reinterpret_cast<SeqsMerge *>(ws + s.merges);
   p.err = a.err;
   const size_t smem = (size_t)(2 * a.n + 2) * 4;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(seqs_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kMaxSeqs + 2) * 4);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
-  }
   return launch_pdl(seqs_plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, p);
 }
 
@@ -404,7 +399,9 @@ cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSp
   m.T = a.q.S;
   m.lse = a.lse;
   m.o = a.o;
-  const dim3 grid = g.stream ? dim3((unsigned)g.ctas, g.slot_rows > 4 * kMergeRows ? 4 : 1) : dim3((unsigned)(4 * g.ctas));
+  // without a list of cut units, one CTA for each that may be, more where requests have many rows
+  const int64_t per = (a.q.S + a.n - 1) / a.n;
+  const dim3 grid = g.stream ? dim3((unsigned)g.ctas, (unsigned)(per < 8 ? per : 8)) : dim3((unsigned)(8 * g.ctas));
   const dim3 threads(32 * kMergeRows);
   if (a.o.D == 128) {
     if (a.o.dtype == FM_F32) return launch_pdl(seqs_merge_kernel<float, 128>, grid, threads, 0, st, m);

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kT, 2) seqs_simt_kernel(const SimtArgs a, cons
     if (idx >= n_items) return;
     const SeqsItem it = a.items[idx];
     const int rows = it.nt * a.group;
+    const int seen0 = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;  // earlier keys no token of the unit sees
     const E *qp = reinterpret_cast<const E *>(a.q.ptr) + (int64_t)it.h * a.group * a.q.sH + (int64_t)it.qrow0 * a.q.sS;
     for (int i = tid; i < kR * (D / 4); i += kT) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kT, 2) seqs_simt_kernel(const SimtArgs a, cons
       for (int i = tid; i < kK * (D / 4); i += kT) {
         const int j = i / (D / 4), d = (i % (D / 4)) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + j < it.key1) {
+        if (j0 + j >= seen0 && j0 + j < it.key1) {
           const E *p = key_row<E>(a, a.k, it, j0 + j);
           if (p) x = load4(p + d * a.k.sD, a.k.sD, vec);
         }
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kT, 2) seqs_simt_kernel(const SimtArgs a, cons
       for (int i = tid; i < kK * (D / 4); i += kT) {
         const int j = i / (D / 4), d = (i % (D / 4)) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + j < it.key1) {
+        if (j0 + j >= seen0 && j0 + j < it.key1) {
           const E *p = key_row<E>(a, a.v, it, j0 + j);
           if (p) x = load4(p + d * a.v.sD, a.v.sD, vec);
         }
@@ -233,19 +234,20 @@ __global__ void __launch_bounds__(kT, 2) seqs_simt_kernel(const SimtArgs a, cons
   }
 }
 
+template <int D>
+constexpr int smem_bytes = (kR * (D + 4) + kK * (D + 4) + kR * (kK + 4)) * 4;
+
 template <typename E, typename O, int D>
 cudaError_t launch_typed(const SimtArgs &p, bool vec, cudaStream_t st) {
-  constexpr int smem = (kR * (D + 4) + kK * (D + 4) + kR * (kK + 4)) * 4;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  return launch_pdl(seqs_simt_kernel<E, O, D>, dim3((unsigned)current_device_sm_count() * 2), dim3(kT), smem_bytes<D>, st, p,
+                    vec);
+}
+template <typename E, typename O>
+cudaError_t allow_smem() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(seqs_simt_kernel<E, O, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<128>);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(seqs_simt_kernel<E, O, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
-  }
-  return launch_pdl(seqs_simt_kernel<E, O, D>, dim3((unsigned)current_device_sm_count() * 2), dim3(kT), smem, st, p, vec);
+  return cudaFuncSetAttribute(seqs_simt_kernel<E, O, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<64>);
 }
 
 template <typename E>
@@ -261,6 +263,13 @@ bool quads(const View &x, int64_t es) {
 }
 
 }  // namespace
+
+cudaError_t seqs_simt_prepare() {
+  for (cudaError_t e : {allow_smem<float, float>(), allow_smem<__nv_bfloat16, float>(), allow_smem<__nv_bfloat16, __nv_bfloat16>(),
+                        allow_smem<__half, float>(), allow_smem<__half, __half>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
 
 SeqsGeom seqs_geom_simt(int64_t T, int group) {
   SeqsGeom g;

@@ -15,7 +15,7 @@
 // groups of 8 keys are evenly spaced whatever the page size, which a matrix descriptor needs: one
 // box a page and panel was bound by the number of boxes (16-key pages: 1.73 us a tile of K and V,
 // 32-key pages 1.40, the rate of HBM).  Pages past the request's end are asked for at a page that
-// does not exist, which TMA fills with zeros.
+// does not exist, which TMA fills with zeros, and so are pages before the unit's window.
 // Work.  A CTA a SM takes pieces from the list in order (a counter), or, where requests have few
 // queries, an even run of all units' key tiles.  A piece is a unit of queries
 // -- two row tiles, or one when its tokens fit one (decoding, the rest of a chunk) -- against a
@@ -26,7 +26,7 @@
 // MMA order for step s of a piece (group s mod 2):  S(s), P V(s - 1): one group's softmax runs
 // under the other's two MMAs.
 // 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM), 2 Q loads and the zeroing of V rows past the
-// request's end (they meet p = 0, but may hold NaN), 3 fetches work, 4-7 and 8-11 softmax.
+// request's end or before the window (they meet p = 0, but may hold NaN), 3 fetches work, 4-7 and 8-11 softmax.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
 // Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
 #include <cudaTypedefs.h>
@@ -538,6 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it.b >= 0;
   };
   auto tiles_of = [](const SeqsItem &it) { return it.key1 > it.key0 ? (it.key1 - it.key0 + 127) >> 7 : 0; };
+  // keys before this one are seen by no token of the piece
+  auto first_seen = [&](const SeqsItem &it) { return p.window > 0 ? max(0, it.pos0 - p.window + 1) : 0; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ K/V producer
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     SeqsItem it;
     for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutProducer, ok, it); ++k) {
-      const int tiles = tiles_of(it);
+      const int tiles = tiles_of(it), lo = first_seen(it);
       // coordinates of this lane's box: row and page (packed: row of the tensor, batch 0)
       auto coords = [&](int kb, int &row, int &page) {
         if (!p.paged) {
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int key = kb + pg * p.box_rows;
         row = p.ps > 128 ? key % p.ps : 0;
-        page = p.num_pages;  // past the end: zeros
-        if (lane < boxes && key < it.kv) {
+        page = p.num_pages;  // past the end, before the window: zeros
+        if (lane < boxes && key < it.kv && key + p.box_rows > lo) {
           const int at = key / p.ps;
           page = p.table[it.b * p.table_stride + at];
           if (page < 0 || page >= p.num_pages) {
@@ -629,20 +631,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       if (!ok) break;
       n += 2 * tiles;
-      const int valid = it.kv - (it.key0 + (tiles - 1) * 128);  // rows of the last tile that are the request's
-      if (valid < 128) {
+      // rows of a tile's V that are to be zero: before the window in the first, past the end in the last
+      auto zero_rows = [&](uint32_t v, int from, int to) {
         // the MMA warp says when that tile's V has landed (its stage may be rounds ahead of this warp)
-        const uint32_t v = n - 1;
         const int st = (int)(v % C::NS);
         if (lane == 0)
           ok = wait_long(C::VNeed, fixes & 1u, kDevErrTimeoutProducer, (int)k) &&
                wait(C::KVFull + st, (v / C::NS) & 1u, kDevErrTimeoutProducer, (int)k);
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        if (!ok) break;
+        if (!ok) return;
         ++fixes;
         __syncwarp();
         uint8_t *tile = gbase + C::offKV + st * C::kTile;
-        for (int x = valid * 8 + lane; x < 128 * 8; x += 32) {  // 16-byte words of a panel: 64 a group of 8 keys
+        for (int x = from * 8 + lane; x < to * 8; x += 32) {  // 16-byte words of a panel: 64 a group of 8 keys
           uint8_t *at = tile + (x >> 6) * C::kGroupStep + (x & 63) * 16;
 #pragma unroll
           for (int pn = 0; pn < C::PN; ++pn) *reinterpret_cast<uint4 *>(at + pn * C::kPanelStep) = make_uint4(0u, 0u, 0u, 0u);
@@ -650,7 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::VFix));
-      }
+      };
+      const int before = first_seen(it) - it.key0, valid = it.kv - (it.key0 + (tiles - 1) * 128);
+      if (before > 0) zero_rows(n - 2 * tiles + 1, 0, min(before, 128));
+      if (ok && valid < 128) zero_rows(n - 1, max(valid, 0), 128);
+      if (!ok) break;
     }
     if (!ok && lane == 0) {
       if (loads > 0)
@@ -690,13 +695,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && tiles_of(it) > 0) {
         const int tiles = tiles_of(it);
         const bool dual = it.nt > p.tq1;
-        const bool ragged = it.kv - (it.key0 + (tiles - 1) * 128) < 128;  // rows of the last tile are not the request's
-        // V of the piece's tile j has landed; the rows past the request's end in its last one are zero
+        // tiles with V rows that are to be zero first: the first, where keys before the window share it,
+        // and the last, past the request's end (the same tile twice, if it is both)
+        const bool head = first_seen(it) > it.key0, tail = it.kv - (it.key0 + (tiles - 1) * 128) < 128;
+        // V of the piece's tile j has landed, and those rows are zero
         auto v_ready = [&](int j, int st, uint32_t ph) -> bool {
           if (!wait(C::KVFull + st, ph, kDevErrTimeoutMma, j)) return false;
-          if (!ragged || j < tiles - 1) return true;
-          mbar_arrive(bar(C::VNeed));
-          return wait(C::VFix, fixes++ & 1u, kDevErrTimeoutMma, j);
+          for (int f = (head && j == 0) + (tail && j == tiles - 1); f > 0; --f) {
+            mbar_arrive(bar(C::VNeed));
+            if (!wait(C::VFix, fixes++ & 1u, kDevErrTimeoutMma, j)) return false;
+          }
+          return true;
         };
         ok = wait(C::QFull, loads++ & 1u, kDevErrTimeoutMma, (int)k);
         int vst = 0;
@@ -1035,18 +1044,20 @@ bool rows16(const View &x, int64_t es) {
 
 template <typename E, int D, bool GROUPED, int MODE>
 cudaError_t launch_typed(const Maps &maps, const Params &p, cudaStream_t st) {
-  constexpr int smem = Cfg<E, D, GROUPED>::kSmem;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(seqs_tc_kernel<E, D, GROUPED, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return launch_pdl(seqs_tc_kernel<E, D, GROUPED, MODE>, dim3((unsigned)current_device_sm_count()), dim3(kThreads),
+                    Cfg<E, D, GROUPED>::kSmem, st, maps, p);
+}
+template <typename E, int D, bool GROUPED, int MODE>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(seqs_tc_kernel<E, D, GROUPED, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<E, D, GROUPED>::kSmem);
+}
+template <typename E, int D>
+cudaError_t allow_smem_dim() {
+  for (cudaError_t e : {allow_smem<E, D, true, kStream>(), allow_smem<E, D, true, kList>(), allow_smem<E, D, false, kStream>(),
+                        allow_smem<E, D, false, kList>(), allow_smem<E, D, false, kLong>()})
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
-  }
-  return launch_pdl(seqs_tc_kernel<E, D, GROUPED, MODE>, dim3((unsigned)current_device_sm_count()), dim3(kThreads), smem,
-                    st, maps, p);
+  return cudaSuccess;
 }
 template <typename E, int D>
 cudaError_t launch_dim(const Maps &maps, const Params &p, bool grouped, int mode, cudaStream_t st) {
@@ -1059,6 +1070,13 @@ cudaError_t launch_dim(const Maps &maps, const Params &p, bool grouped, int mode
 }
 
 }  // namespace
+
+cudaError_t seqs_tc_prepare() {
+  for (cudaError_t e : {allow_smem_dim<__nv_bfloat16, 128>(), allow_smem_dim<__nv_bfloat16, 64>(),
+                        allow_smem_dim<__half, 128>(), allow_smem_dim<__half, 64>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
 
 // The tensor-core kernel takes 16-bit types whose rows a tensor map describes, and pages that
 // divide its key tiles or are made of them.

@@ -453,9 +453,11 @@ FM_API int fm_bounds_noalloc(const fm_tensor *q, const fm_tensor *k_full, const 
  *     no key gets o = 0 and lse = -inf.
  *   - FM_F32, FM_BF16 or FM_F16, one type for q, k, v; sums, the row max and the normalise are fp32;
  *     for 16-bit inputs the weights p are rounded to that type before they meet v.
- *   - Keys and values past a request's end (the rest of its last page, its neighbours' rows) may
- *     hold anything, NaN too: they change nothing.  A value row that some query of the request
- *     sees must be finite: a NaN or infinity there may reach that request's other rows.
+ *   - Keys and values that no query of the request sees (past its end in its last page, its
+ *     neighbours' rows, before every query's window) may hold anything, NaN too: they change
+ *     nothing, and table entries of pages before the window are not read.  A value row that some
+ *     query of the request sees must be finite: a NaN or infinity there may reach that request's
+ *     other rows.
  *   - All lengths are read on the device: nothing waits for them, calls can be captured into a
  *     graph and replayed with other lengths (the first call on a device comes before any
  *     capture).  Lengths that do not fit the tensors are clamped, cu_q that runs backwards computes

@@ -238,6 +238,47 @@ def test_paged_window(dev, window, lens):
     check_paged(q, ks, vs, lens, o, lse, window=window)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ps", [8, 16, 64, 128])
+@pytest.mark.parametrize("window,lens", [(50, [(1, 700), (1, 30), (1, 300)]), (130, [(60, 900), (1, 1), (5, 640)])])
+def test_keys_before_the_window_may_hold_anything(dev, dtype, ps, window, lens):
+    """Rows that every query's window has passed hold NaN, and the table entries of whole such pages
+    point outside the cache: as after a server has taken those pages back."""
+    g = torch.Generator(device=dev).manual_seed(20)
+    ks, vs, kc, vc, table = paged_case(g, lens, 2, 128, ps, dtype, True)
+    for i, (a, b) in enumerate(lens):
+        first = max(0, b - a - window + 1)  # the oldest key that the first query sees
+        for j in range(first // ps + 1):
+            rows = min(ps, first - j * ps)
+            if rows > 0:
+                kc[table[i, j], :, :rows] = float("nan")
+                vc[table[i, j], :, :rows] = float("nan")
+            if rows == ps:
+                table[i, j] = -1
+    q = rand(g, sum(a for a, _ in lens), 8, 128, dtype=dtype)
+    o, lse = run_paged(q, kc, vc, table, lens, dev, window=window)
+    fm.fm_sync_status()
+    check_paged(q, ks, vs, lens, o, lse, window=window)
+
+
+def test_offsets_past_32_bits(dev):
+    """A cache of more than 2^31 elements, with the request on its last pages: written and read."""
+    g = torch.Generator(device=dev).manual_seed(21)
+    Hk, D, ps, pages = 8, 128, 16, 135000
+    kc, vc = (torch.empty(pages, ps, Hk, D, dtype=BF16, device=dev).transpose(1, 2) for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    lens = [(1, 200), (3, 100)]
+    table = torch.tensor([[pages - 1 - 2 * j for j in range(13)], [pages - 2 - 2 * j for j in range(13)]], dtype=torch.int32)
+    ks, vs = ([rand(g, s, Hk, D, dtype=BF16) for _, s in lens] for _ in range(2))
+    slots = [int(table[i, p // ps]) * ps + p % ps for i, (_, s) in enumerate(lens) for p in range(s)]
+    fm.fm_paged_write(torch.cat(ks), torch.cat(vs), ints(slots, dev, torch.int64), kc, vc)
+    q = rand(g, 4, 16, D, dtype=BF16)
+    o, lse = run_paged(q, kc, vc, table.to(dev), lens, dev)
+    fm.fm_sync_status()
+    check_paged(q, ks, vs, lens, o, lse)
+    assert torch.equal(kc[table[0, 0], :, 3], ks[0][3])
+
+
 def test_paged_not_causal_and_shared_pages(dev):
     """Two requests whose tables name the same pages, and every query seeing every key."""
     g = torch.Generator(device=dev).manual_seed(10)
@@ -316,6 +357,46 @@ def test_captured_and_replayed_with_other_lengths(dev):
         graph.replay()
         fm.fm_sync_status()
         check_paged(q, [k[:n] for k, n in zip(ks, now)], [v[:n] for v, n in zip(vs, now)], [(1, n) for n in now], o, lse)
+
+
+def test_a_captured_call_may_be_the_first_of_its_kind(tmp_path):
+    """After one call on the device, calls that take other kernels (types, page sizes, prompts instead
+    of single tokens) can be captured though none of them has run: in a process of its own."""
+    import subprocess
+    import sys
+
+    code = """
+import torch, fixed_max_softmax_gb300 as fm
+dev = torch.device("cuda:0")
+def call(dtype, T, n, D, ps, out):
+    q = torch.ones(T, 4, D, dtype=dtype, device=dev)
+    kc = torch.ones(200 // ps + 2, 2, ps, D, dtype=dtype, device=dev)
+    cu = torch.tensor([0] + [T // n * (i + 1) for i in range(n)], dtype=torch.int32, device=dev)
+    kv = torch.full((n,), 190, dtype=torch.int32, device=dev)
+    table = torch.arange(200 // ps + 1, dtype=torch.int32, device=dev).repeat(n, 1)
+    ws = torch.empty(fm.fm_attn_seqs_workspace_size(n, T, 4, 2, D), dtype=torch.uint8, device=dev)
+    o = torch.zeros_like(q)
+    out.append((q, kc, cu, kv, table, ws, o))
+    return lambda: fm.fm_attn_paged(q, kc, kc, cu, kv, table, fm.seqs_opts(), o, None, ws)
+bufs = []
+call(torch.float32, 2, 2, 64, 16, bufs)()
+todo = [call(d, T, n, D, ps, bufs) for d in (torch.bfloat16, torch.float16, torch.float32) for D in (64, 128)
+        for T, n in ((2, 2), (160, 1)) for ps in (16, 128, 5)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for f in todo:
+        f()
+for b in bufs[1:]:
+    assert not b[-1].any()
+g.replay()
+fm.fm_sync_status()
+for b in bufs:  # equal weights and values of one: two sums of at most 190 equal fp32 terms, in different orders
+    assert ((b[-1].float() - 1).abs() <= 2 * 198 * 2.0 ** -24).all(), b[0].dtype
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
