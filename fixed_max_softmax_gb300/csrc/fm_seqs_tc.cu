@@ -25,8 +25,8 @@
 //                   at the end: a decoding request's tiles go through both groups at once
 // MMA order for step s of a piece (group s mod 2):  S(s), P V(s - 1): one group's softmax runs
 // under the other's two MMAs.
-// 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM), 2 Q loads and the zeroing of V rows past the
-// request's end or before the window (they meet p = 0, but may hold NaN), 3 fetches work, 4-7 and 8-11 softmax.
+// 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM), 2 zeroes V rows past the request's end or before
+// the window (they meet p = 0, but may hold NaN), 3 fetches work and loads its Q, 4-7 and 8-11 softmax.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
 // Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
 #include <cudaTypedefs.h>
@@ -278,7 +278,7 @@ __device__ __forceinline__ void mma_output(uint32_t tO, uint32_t tP, uint32_t b,
 // piece that continues a unit (slot 2c) and one that begins a unit and does not end it (2c + 1).
 // The line's measure, in about 0.35 us: a key tile of a unit of one row tile (streamed from HBM) and
 // of two (bound by the tensor core and the exponentials), and a unit's start and end.
-constexpr int kTileCost1 = 4, kTileCost2 = 5, kUnitCost1 = 5, kUnitCost2 = 10;
+constexpr int kTileCost1 = 4, kTileCost2 = 5, kUnitCost1 = 12, kUnitCost2 = 20;
 constexpr int kLeastRun = 12;  // shorter runs would cost more to merge than they save (none is shorter than a tile)
 
 // This CTA's part [x0, x1) of the line, and the unit that x0 falls in: (b, h, t), starting at u0.
@@ -606,37 +606,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                    wtag(C::KVFull, 0));
     }
   } else if (warp == 2) {
-    // ------------------------------------------------------------ Q loads, V rows past the end
-    const uint32_t q_bytes = (uint32_t)(C::PN * p.group * p.tq1 * 128);
-    uint32_t n = 0, loads = 0, loads1 = 0, fixes = 0;
+    // ------------------------------------------------------------ V rows that are to be zero
+    uint32_t n = 0, fixes = 0;
     bool ok = true;
     SeqsItem it;
     for (uint32_t k = 0; ok && next_item(k, kDevErrTimeoutProducer, ok, it); ++k) {
       const int tiles = tiles_of(it);
       if (tiles == 0) continue;
-      const int nq = it.nt > p.tq1 ? 2 : 1;
-      if (lane == 0) {
-        for (int t = 0; t < nq && ok; ++t) {
-          const uint32_t before = t ? loads1 : loads;
-          // the last S MMA on the tile's earlier contents
-          if (before > 0) ok = wait_long(C::QEmpty + t, (before - 1) & 1u, kDevErrTimeoutProducer, (int)k);
-          if (!ok) break;
-          mbar_expect_tx(bar(C::QFull + t), q_bytes);
-          for (int pn = 0; pn < C::PN; ++pn)
-            tma_load_3d(base + C::offQ + t * C::kTile + pn * kPanel, &maps.q, bar(C::QFull + t), pn * 64, it.h * p.group,
-                        it.qrow0 + t * p.tq1);
-          if (t) ++loads1; else ++loads;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      if (!ok) break;
       n += 2 * tiles;
       // rows of a tile's V that are to be zero: before the window in the first, past the end in the last
       auto zero_rows = [&](uint32_t v, int from, int to) {
         // the MMA warp says when that tile's V has landed (its stage may be rounds ahead of this warp)
         const int st = (int)(v % C::NS);
+        // (every decoding request has one to wait for, and time to poll)
         if (lane == 0)
-          ok = wait_long(C::VNeed, fixes & 1u, kDevErrTimeoutProducer, (int)k) &&
+          ok = (MODE == kStream ? wait(C::VNeed, fixes & 1u, kDevErrTimeoutProducer, (int)k)
+                                : wait_long(C::VNeed, fixes & 1u, kDevErrTimeoutProducer, (int)k)) &&
                wait(C::KVFull + st, (v / C::NS) & 1u, kDevErrTimeoutProducer, (int)k);
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         if (!ok) return;
@@ -657,13 +642,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && valid < 128) zero_rows(n - 1, max(valid, 0), 128);
       if (!ok) break;
     }
-    if (!ok && lane == 0) {
-      if (loads > 0)
-        wait_phase(bar(C::QFull), (loads - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain, wtag(C::QFull, 0));
-      if (loads1 > 0)
-        wait_phase(bar(C::QFull + 1), (loads1 - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain,
-                   wtag(C::QFull + 1, 0));
-    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // One thread, and as few instructions as can be between a group's arrival and the MMA that waits
@@ -673,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t v_lo = ((base + C::offKV) >> 4) | ((uint32_t)(C::kPanelStep >> 4) << 16);
     int kst = 0;                      // ring stage of the next K tile, and its phase
     uint32_t kph = 0;
-    uint32_t loads = 0, loads1 = 0;   // Q tiles 0 and 1 used
+    uint32_t loads0 = 0, loads1 = 0;  // uses of Q slots 0 and 1
+    int qs = 0;                       // Q slot of the next piece of one row tile
     uint32_t steps0 = 0, steps1 = 0;  // softmax steps of each group so far
     uint32_t fixes = 0;
     bool ok = true;
@@ -707,10 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        ok = wait(C::QFull, loads++ & 1u, kDevErrTimeoutMma, (int)k);
         int vst = 0;
         uint32_t vph = 0;
         if (dual) {
+          ok = wait(C::QFull, loads0++ & 1u, kDevErrTimeoutMma, (int)k);
           for (int j = 0; j < tiles && ok; ++j) {
             ok = wait(C::KVFull + kst, kph, kDevErrTimeoutMma, j);
             if (!ok) break;
@@ -761,13 +740,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j + 2 >= tiles) mma_commit(bar(C::ODone + g));
             return true;
           };
+          ok = wait(C::QFull + qs, (qs ? loads1++ : loads0++) & 1u, kDevErrTimeoutMma, (int)k);
           for (int j = 0; j < tiles && ok; ++j) {
             ok = wait(C::KVFull + kst, kph, kDevErrTimeoutMma, j);
             if (!ok) break;
             tc_fence_after();
-            mma_s(j & 1, 0, kst);
+            mma_s(j & 1, qs, kst);
             mma_commit(bar(C::KVEmpty + kst));
-            if (j == tiles - 1) mma_commit(bar(C::QEmpty));
+            if (j == tiles - 1) mma_commit(bar(C::QEmpty + qs));
             if (j > 0) ok = pv(j - 1);
             next(kst, kph);
             vst = kst;
@@ -775,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             next(kst, kph);
           }
           if (ok) ok = pv(tiles - 1);
+          qs ^= 1;
         }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -785,8 +766,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_phase(bar(C::Drain), 0, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain, wtag(C::Drain, 0));
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------ work
+    // ------------------------------------------------------------ work, and its Q tiles
+    // A piece of two row tiles has them in Q slots 0 and 1; pieces of one take the slots in turn, so
+    // that the next one's Q lands while this one is at work.
     if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)(C::PN * p.group * p.tq1 * 128);
       unsigned n_items = 0;
       StreamWalk walk;
       if constexpr (MODE == kStream) {
@@ -795,11 +779,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         n_items = p.counters[1];
       }
-      bool more = true;
+      uint32_t loads0 = 0, loads1 = 0;
+      int qs = 0;
+      bool more = true, ok = true;
       for (uint32_t k = 0; more; ++k) {
         // a piece is claimed when the producer is nearly through with the one before, not earlier:
         // claimed ahead, pieces would wait behind a long one while other CTAs run dry
-        if (k > 0 && !wait_long(C::Want, (k - 1) & 1u, kDevErrTimeoutProducer, (int)k)) break;
+        if (k > 0) ok = wait_long(C::Want, (k - 1) & 1u, kDevErrTimeoutProducer, (int)k);
+        if (!ok) break;
         SeqsItem it;
         if constexpr (MODE == kStream) {
           more = walk.next(p, it);
@@ -810,9 +797,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!more) it.b = -1;
         const int slot = (int)(k & 1u);
-        if (!wait_long(C::ItemEmpty + slot, ((k >> 1) & 1u) ^ 1u, kDevErrTimeoutProducer, (int)k)) break;
+        ok = wait_long(C::ItemEmpty + slot, ((k >> 1) & 1u) ^ 1u, kDevErrTimeoutProducer, (int)k);
+        if (!ok) break;
         item_ring[slot] = it;
         mbar_arrive(bar(C::ItemFull + slot));
+        if (!more || tiles_of(it) == 0) continue;
+        const bool dual = it.nt > p.tq1;
+        for (int t = 0; t < (dual ? 2 : 1) && ok; ++t) {
+          const int qt = dual ? t : qs;
+          const uint32_t before = qt ? loads1 : loads0;
+          // the last S MMA on the slot's earlier contents
+          if (before > 0) ok = wait_long(C::QEmpty + qt, (before - 1) & 1u, kDevErrTimeoutProducer, (int)k);
+          if (!ok) break;
+          mbar_expect_tx(bar(C::QFull + qt), q_bytes);
+          for (int pn = 0; pn < C::PN; ++pn)
+            tma_load_3d(base + C::offQ + qt * C::kTile + pn * kPanel, &maps.q, bar(C::QFull + qt), pn * 64, it.h * p.group,
+                        it.qrow0 + t * p.tq1);
+          if (qt) ++loads1; else ++loads0;
+        }
+        if (!ok) break;
+        if (!dual) qs ^= 1;
+      }
+      if (!ok) {
+        // every copy already issued lands before the CTA can exit
+        if (loads0 > 0)
+          wait_phase(bar(C::QFull), (loads0 - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain, wtag(C::QFull, 0));
+        if (loads1 > 0)
+          wait_phase(bar(C::QFull + 1), (loads1 - 1) & 1u, nullptr, p.timeout_ns, p.err, kDevErrTimeoutDrain,
+                     wtag(C::QFull + 1, 0));
       }
     }
   } else {
