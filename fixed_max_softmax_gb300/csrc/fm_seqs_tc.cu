@@ -78,6 +78,8 @@ struct Maps {
 };
 struct Params {
   int group, tq1;  // heads of a key head, tokens of a row tile
+  uint32_t inv_group;  // ceil(2^16 / group): row * inv_group >> 16 is row / group for the rows of a tile
+  int wide;            // o's rows are 32-byte aligned
   int causal, window;
   float alpha;
   int paged, ps, box_rows, num_pages;
@@ -206,42 +208,37 @@ __device__ __noinline__ void mask_rows(uint32_t tS, int kb, int lo, int hi, int 
   tmem_st_wait();
 }
 
-// 32 columns of each of a warp's rows to memory as 16-bit elements, lane r holding row r.  The 64
-// bytes of a row go out as one piece, four lanes a row, after a 4 x 4 exchange of 16-byte words
-// within each four lanes; lane by lane, a store would touch 32 lines of memory instead of 8, and
-// the store unit takes a line a cycle.  row[i]: this lane's 16 bytes of the i-th of its four lanes'
-// rows, nullptr where that row is not written.
-template <typename E>
-__device__ __forceinline__ void store_rows16(uint8_t *const (&row)[4], int offset, const float (&x)[32], int lane) {
-  uint4 w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = make_uint4(pack_half<E>(x[8 * i], x[8 * i + 1]), pack_half<E>(x[8 * i + 2], x[8 * i + 3]),
-                      pack_half<E>(x[8 * i + 4], x[8 * i + 5]), pack_half<E>(x[8 * i + 6], x[8 * i + 7]));
-  auto exchange = [&](uint4 &a, uint4 &b, int d) {  // a 2 x 2 transpose between lanes d apart
-    const bool up = (lane & d) != 0;
-    uint4 t = up ? a : b;
-    t.x = __shfl_xor_sync(0xffffffffu, t.x, d);
-    t.y = __shfl_xor_sync(0xffffffffu, t.y, d);
-    t.z = __shfl_xor_sync(0xffffffffu, t.z, d);
-    t.w = __shfl_xor_sync(0xffffffffu, t.w, d);
-    if (up) a = t; else b = t;
-  };
-  exchange(w[0], w[1], 1);
-  exchange(w[2], w[3], 1);
-  exchange(w[0], w[2], 2);
-  exchange(w[1], w[3], 2);
-  // w[i] is now word lane % 4 of row (lane & ~3) + i
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (row[i]) *reinterpret_cast<uint4 *>(row[i] + offset) = w[i];
+// 32 bytes of a row in one store (wide: 32-byte aligned) or two.
+__device__ __forceinline__ void store32(uint8_t *dst, const uint32_t (&w)[8], bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  else {
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
-__device__ __forceinline__ void store_row32(uint8_t *dst, const float (&x)[32]) {
-  uint4 *p = reinterpret_cast<uint4 *>(dst);
+// 32 columns of this lane's row to memory, as 16-bit elements or fp32.  Whole 32-byte sectors, lane by
+// lane: few instructions, and the stores drain while the next piece starts.
+template <typename E>
+__device__ __forceinline__ void store_row(uint8_t *dst, const float (&x)[32], bool f32, bool wide) {
+  uint32_t w[8];
+  if (f32) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    p[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
-                      __float_as_uint(x[4 * i + 3]));
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(x[8 * i + e]);
+      store32(dst + 32 * i, w, wide);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = pack_half<E>(x[16 * i + 2 * e], x[16 * i + 2 * e + 1]);
+      store32(dst + 32 * i, w, wide);
+    }
+  }
 }
 
 // A descriptor's upper half: stride of 8 rows in 16-byte units, version, 128-byte swizzle.
@@ -834,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = (warp - 4) >> 2;  // group
     const int wq = warp & 3;        // TMEM lane quarter of this warp
     const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(g * 128), tO = tS + 256u;
+    auto token = [&](int row) -> int { return (int)((uint32_t)row * p.inv_group >> 16); };  // of a row of the tile
     uint32_t steps = 0, pieces0 = 0, pieces1 = 0, singles = 0;  // phases: S steps, O-done of both groups, Stat / EpiDone
     bool ok = true;
     for (uint32_t k = 0;; ++k) {
@@ -852,8 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const int first_tok = dual ? g * p.tq1 : 0;
         const int left = min(p.tq1, it.nt - first_tok);  // tokens of this group's row tile
-        const int tok0 = wq * 32 / p.group, tok1 = (wq * 32 + 31) / p.group;  // tokens of the warp's rows
-        const int tok = (wq * 32 + opaque_laneid()) / p.group;
+        const int tok0 = token(wq * 32), tok1 = token(wq * 32 + 31);  // tokens of the warp's rows
+        const int tok = token(wq * 32 + opaque_laneid());
         const bool row_ok = tok < left;
         const int pos = it.pos0 + first_tok, kv = it.kv;
         int lo = 0, hi = 0;
@@ -915,9 +913,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int first_tok = dual ? g * p.tq1 : 0;
         const int left = min(p.tq1, it.nt - first_tok);
-        const int r = wq * 32 + opaque_laneid(), tok = r / p.group, hd = r - tok * p.group;
+        const int r = wq * 32 + opaque_laneid(), tok = token(r), hd = r - tok * p.group;
         const bool row_ok = tok < left;
-        if (wq * 32 / p.group < left) {
+        if (token(wq * 32) < left) {
           const int part = it.slot;
           const bool whole = part < 0;
           const float inv = !whole ? 1.f : (lsum == 0.f ? 0.f : 1.0f / lsum);  // no key seen: zeros, lse = -inf
@@ -925,16 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t qrow = (int64_t)it.qrow0 + first_tok + tok;
           const int head = it.h * p.group + hd;
           const int64_t slot_row = (int64_t)part * p.slot_rows + (first_tok + tok) * p.group + hd;
-          const bool f32 = !whole || p.out_f32;
+          const bool f32 = !whole || p.out_f32, wide = !whole || p.wide;  // (partial results are aligned)
           uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) + (head * p.osH + qrow * p.osS) * (p.out_f32 ? 4 : 2)
                                : reinterpret_cast<uint8_t *>(p.part_o + slot_row * D);
-          uint8_t *row[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const unsigned long long d = __shfl_sync(0xffffffffu, row_ok ? reinterpret_cast<unsigned long long>(dst) : 0ull,
-                                                     (lane & ~3) + i);
-            row[i] = d ? reinterpret_cast<uint8_t *>(d) + (lane & 3) * 16 : nullptr;
-          }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float x[32];
@@ -957,8 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            if (!f32) store_rows16<E>(row, c * 64, x, lane);
-            else if (row_ok) store_row32(dst + c * 128, x);
+            if (row_ok) store_row<E>(dst + c * (f32 ? 128 : 64), x, f32, wide);
           }
           if (row_ok) {
             // acc = sum 2^(z - run + bias): the bias leaves o as it is and comes off the log
@@ -1049,9 +1039,9 @@ int64_t page_groups(const View &t) {
   return (t.B + 1) * g < ((int64_t)1 << 31) ? g : 0;
 }
 
-bool rows16(const View &x, int64_t es) {
-  auto ok = [&](int64_t s, int64_t n) { return n <= 1 || (s > 0 && (s * es) % 16 == 0 && s * es < ((int64_t)1 << 40)); };
-  return x.sD == 1 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && ok(x.sS, x.S) && ok(x.sH, x.H) && ok(x.sB, x.B);
+bool rows_aligned(const View &x, int64_t es, int64_t to) {
+  auto ok = [&](int64_t s, int64_t n) { return n <= 1 || (s > 0 && (s * es) % to == 0 && s * es < ((int64_t)1 << 40)); };
+  return x.sD == 1 && reinterpret_cast<uintptr_t>(x.ptr) % to == 0 && ok(x.sS, x.S) && ok(x.sH, x.H) && ok(x.sB, x.B);
 }
 
 template <typename E, int D, bool GROUPED, int MODE>
@@ -1097,7 +1087,8 @@ bool seqs_tc_supported(const SeqsArgs &a) {
   if (a.k.S < 1 || a.k.B < 1) return false;
   const int64_t ps = a.k.S;
   if (a.paged && !(ps == 8 || ps == 16 || ps == 32 || ps == 64 || ps % 128 == 0)) return false;
-  return rows16(a.q, 2) && rows16(a.k, 2) && rows16(a.v, 2) && rows16(a.o, a.o.dtype == FM_F32 ? 4 : 2);
+  return rows_aligned(a.q, 2, 16) && rows_aligned(a.k, 2, 16) && rows_aligned(a.v, 2, 16) &&
+         rows_aligned(a.o, a.o.dtype == FM_F32 ? 4 : 2, 16);
 }
 
 SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
@@ -1121,6 +1112,8 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   Params p;
   p.group = g.group;
   p.tq1 = g.tq / 2;
+  p.inv_group = (65536u + (uint32_t)g.group - 1u) / (uint32_t)g.group;
+  p.wide = rows_aligned(a.o, a.o.dtype == FM_F32 ? 4 : 2, 32);
   p.box_rows = a.paged && a.k.S < 128 ? (int)a.k.S : 128;
   const int64_t groups = p.box_rows < 128 ? page_groups(a.k) : 0;
   const bool grouped = groups > 0 && groups == page_groups(a.v);
