@@ -927,28 +927,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) + (head * p.osH + qrow * p.osS) * (p.out_f32 ? 4 : 2)
                                : reinterpret_cast<uint8_t *>(p.part_o + slot_row * D);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
             float x[32];
-            if (tiles == 0) {
+            if (tiles > 0) {
+              tmem_ld32(tO + c, o);
+            } else {  // no key: O is an earlier piece's
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = 0.f;
-            } else {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * s0;
-              if (!dual) {
-                // (a group that saw no key of its own: its O is not a number's to scale)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = c0 == 0.f ? 0.f : x[e];
-                if (nsub > 1) {
-                  tmem_ld32(tO + 128 + c * 32, o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) x[e] = c1 == 0.f ? x[e] : fmaf(__uint_as_float(o[e]), s1, x[e]);
-                }
-              }
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
             }
-            if (row_ok) store_row<E>(dst + c * (f32 ? 128 : 64), x, f32, wide);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * s0;
+            if (!dual && nsub > 1) {
+              tmem_ld32(tO + 128 + c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), s1, x[e]);
+            }
+            if (row_ok) store_row<E>(dst + c * (f32 ? 4 : 2), x, f32, wide);
           }
           if (row_ok) {
             // acc = sum 2^(z - run + bias): the bias leaves o as it is and comes off the log
