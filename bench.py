@@ -37,27 +37,28 @@ FALLBACK_PEAKS = {"bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0, "hbm_g
 # grows with the head count).
 # Valid only for the kernel code it was measured on (comments aside): the bench reports null
 # otherwise.
-CHUNK_TRAFFIC = {"code_sha256_16": "de3b182134dfb248", "bytes_per_launch": 5 * (620.001e6 + 846.480e6) / 2}
+CHUNK_TRAFFIC = {"code_sha256_16": "3c2f19cba7f34b12", "bytes_per_launch": 5 * (623.434e6 + 844.840e6) / 2}
 
 
-def kernel_code_hash(path: str) -> str:
-    """sha256[:16] of a CUDA source with its // comments and blank lines removed, so that a
+def kernel_code_hash(*paths: str) -> str:
+    """sha256[:16] of CUDA sources with their // comments and blank lines removed, so that a
     comment edit keeps a recorded measurement while any change to the code drops it."""
     import hashlib
     import re
 
     lines = []
-    for ln in open(path, encoding="utf-8").read().splitlines():
-        ln = re.sub(r"//.*$", "", ln).rstrip()
-        if ln:
-            lines.append(ln)
+    for path in paths:
+        for ln in open(path, encoding="utf-8").read().splitlines():
+            ln = re.sub(r"//.*$", "", ln).rstrip()
+            if ln:
+                lines.append(ln)
     return hashlib.sha256("\n".join(lines).encode()).hexdigest()[:16]
 
 
 def chunk_traffic():
-    src = os.path.join(ROOT, "fixed_max_softmax_gb300", "csrc", "fm_chunk_tc.cu")
+    csrc = os.path.join(ROOT, "fixed_max_softmax_gb300", "csrc")
     try:
-        h = kernel_code_hash(src)
+        h = kernel_code_hash(os.path.join(csrc, "fm_chunk_tc.cu"), os.path.join(csrc, "fm_tc.cuh"))
     except OSError:
         return None
     return CHUNK_TRAFFIC["bytes_per_launch"] if h == CHUNK_TRAFFIC["code_sha256_16"] else None
