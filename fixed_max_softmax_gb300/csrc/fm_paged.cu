@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 #include <limits.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "fm_internal.h"
@@ -305,7 +306,7 @@ bool rows16(const View &x, int64_t es) {
 cudaError_t launch_paged_extend(const PagedExtendArgs &args, cudaStream_t st) {
   PagedExtendArgs a = args;
   const size_t smem = (size_t)(4 * (a.n + 1)) * 4;
-  static bool attr_set[64] = {};  // once per device, so never while a stream is captured after a first call
+  static std::atomic<bool> attr_set[64] = {};  // once per device, so never while a stream is captured after a first call
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

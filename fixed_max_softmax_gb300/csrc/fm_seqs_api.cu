@@ -4,6 +4,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "fm_internal.h"
 
 using namespace fm;
@@ -54,7 +56,7 @@ size_t space_bytes(int64_t n, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
 // Every attention kernel's attributes, at the first call on the current device.
 cudaError_t prepare() {
   constexpr int kDevices = 64;
-  static bool ready[kDevices] = {};
+  static std::atomic<bool> ready[kDevices] = {};  // set by whichever thread is first, or by several
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev >= 0 && dev < kDevices && ready[dev])) return e;

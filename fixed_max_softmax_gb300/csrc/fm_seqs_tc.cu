@@ -284,10 +284,9 @@ struct StreamRun {
   int parts, b, h, t;
   Request req;
 };
-// The line is measured in 32 bits: a thread's requests may hold 2^31 / kThreads of it (5.5 million
-// key tiles, more than the GPU's memory), and a call that has more is refused as lengths that do
-// not fit.
-constexpr int kMostOfThread = 0x7fffffff / kThreads;
+// The line is measured in 32 bits, sums stopping at kMostLine: a call of so much (5e8 key tiles of a
+// key head, a minute's work and more) is refused as lengths that do not fit.
+constexpr int kMostLine = 0x7fff0000;
 
 __device__ __forceinline__ int unit_cost(const Params &p, const Request &r, int t) {
   const int tq = 2 * p.tq1;
@@ -324,28 +323,29 @@ __device__ __forceinline__ void stream_run(const Params &p, int *warp_sum, Strea
     sum += per_head * p.Hk;
     refuse |= r.back;
   }
-  if (sum > kMostOfThread) {
-    refuse = true;
-    sum = 0;
-    if (err && atomicCAS(err, 0u, (unsigned)kDevErrLength) == 0u) err[1] = (unsigned)b0;
-  }
-  const int mine = (int)sum;
+  auto plus = [](int x, int y) { return (int)min((unsigned)x + (unsigned)y, (unsigned)kMostLine); };
+  const int mine = (int)min(sum, (long long)kMostLine);
   int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += u;
+    if (lane >= d) inc = plus(inc, u);
   }
   if (lane == 31) warp_sum[warp] = inc;
+  // no unit begins in this CTA's run until the walk says so: a wait that gives up before that leaves
+  // no stale entry for the merge
+  if (tid == 0) p.merges[blockIdx.x].nseg = 0;
   const bool none = __syncthreads_or(refuse);
   int start = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     const int x = warp_sum[w];
-    if (w < warp) start += x;
-    total += x;
+    if (w < warp) start = plus(start, x);
+    total = plus(total, x);
   }
-  if (none) total = 0;
+  if (total == kMostLine && err && tid == 0 && atomicCAS(err, 0u, (unsigned)kDevErrLength) == 0u)
+    err[1] = err[2] = err[3] = err[4] = 0u;
+  if (none || total == kMostLine) total = 0;
   const int parts = max(1, min((int)gridDim.x, (total + kLeastRun - 1) / kLeastRun)), c = blockIdx.x;
   int x0 = 0, x1 = 0;
   if (c < parts) {
@@ -385,9 +385,9 @@ __device__ __forceinline__ void stream_run(const Params &p, int *warp_sum, Strea
 // One thread: the run's pieces in order.
 struct StreamWalk {
   StreamRun r;
-  bool merge_told;
 
-  // The next piece; false when the run is at its end (the CTA's merge entry is then written).
+  // The next piece; false when the run is at its end.  Writes the CTA's merge entry, if a unit begins
+  // in its run and does not end there.
   __device__ __forceinline__ bool next(const Params &p, SeqsItem &it) {
     const int tq = 2 * p.tq1;
     bool found = false;
@@ -426,7 +426,6 @@ struct StreamWalk {
           m.stride = 2;
           m.group0 = 0;
           p.merges[blockIdx.x] = m;
-          merge_told = true;
         }
       }
       r.u0 += tiles * cost + (nt > p.tq1 ? kUnitCost2 : kUnitCost1);
@@ -443,10 +442,6 @@ struct StreamWalk {
           } while (r.req.q == 0);
         }
       }
-    }
-    if (!found && !merge_told) {
-      p.merges[blockIdx.x].nseg = 0;
-      merge_told = true;
     }
     return found;
   }
@@ -771,7 +766,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned n_items = 0;
       StreamWalk walk;
       if constexpr (MODE == kStream) {
-        walk.merge_told = false;
         walk.r = *run_of_cta;
       } else {
         n_items = p.counters[1];

@@ -462,7 +462,8 @@ FM_API int fm_bounds_noalloc(const fm_tensor *q, const fm_tensor *k_full, const 
  *     graph and replayed with other lengths (the first call on a device comes before any
  *     capture).  Lengths that do not fit the tensors are clamped, cu_q that runs backwards computes
  *     nothing, a table entry outside [0, num_pages) reads as zeros, and the next fm_sync_status
- *     returns FM_ERR_INDEX.
+ *     returns FM_ERR_INDEX; it does so too after a decoding call of more than about 4e8 tiles
+ *     (128 keys of one key head each), which computes nothing.
  *   - The workspace is scratch: its contents need no preparation and mean nothing afterwards.  Calls
  *     that may run at the same time need one each. */
 #define FM_MAX_GROUP 64
@@ -532,7 +533,8 @@ typedef struct {
  *             table and list stay, cu_q is all 0 and slots and positions all -1, so that the
  *             cache write and the attention that follow do nothing.
  * Pages given back are put on the list's end in request and table order; new pages are taken from
- * its end.  Errors: FM_ERR_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+ * its end.  A page belongs to one row here: a page that several tables share would be given back by
+ * each of their rows, so such tables are kept by the caller.  Errors: FM_ERR_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
 FM_API int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const uint8_t *release,
                            int64_t max_tokens, int32_t *cu_q, int64_t *slots, int32_t *positions, int32_t *status,
                            fm_stream_t stream);

@@ -291,6 +291,35 @@ def test_paged_not_causal_and_shared_pages(dev):
     check_paged(q, [ks[0], ks[0][:280]], [vs[0], vs[0][:280]], lens, o, lse, causal=False)
 
 
+def test_a_request_of_millions_of_keys(dev):
+    """One request whose table names the same page again and again: the softmax weights of a page,
+    its lse plus the log of the repeats.  64 heads x 22,800 tiles, more than any cache here holds."""
+    g = torch.Generator(device=dev).manual_seed(40)
+    reps, Hk, D, ps = 22800, 64, 64, 128
+    k, v = rand(g, ps, Hk, D, dtype=BF16), rand(g, ps, Hk, D, dtype=BF16)
+    q = rand(g, 1, Hk, D, dtype=BF16)
+    table = torch.zeros(1, reps, dtype=torch.int32, device=dev)
+    o, lse = run_paged(q, k.transpose(0, 1)[None], v.transpose(0, 1)[None], table, [(1, reps * ps)], dev)
+    fm.fm_sync_status()
+    ro, rl, ra, big = attend(q, k, v, True, 0, D ** -0.5)
+    # fp32 sums: the weights of a tile are summed first, then the tiles (reps terms); O takes the products
+    # of 16 keys at a time, 8 a tile
+    assert_close(o, lse, ro, rl + math.log(reps), ra, big, BF16, BF16, D, 8 * reps)
+
+
+def test_more_tiles_than_a_decoding_call_takes(dev):
+    """8,192 requests x 64 heads x 1,025 tiles (a shared page): refused on the device, nothing computed."""
+    n, Hk, D, ps = 8192, 64, 64, 128
+    kc = torch.zeros(1, Hk, ps, D, dtype=BF16, device=dev)
+    q = torch.zeros(n, Hk, D, dtype=BF16, device=dev)
+    table = torch.zeros(n, 1025, dtype=torch.int32, device=dev)
+    o, lse = run_paged(q, kc, kc, table, [(1, 1025 * ps)] * n, dev)
+    with pytest.raises(fm.FMError, match="lengths") as e:
+        fm.fm_sync_status()
+    assert e.value.code == fm.FM_ERR_INDEX
+    assert (o == 7.0).all() and (lse == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_many_requests(dev, dtype):
     g = torch.Generator(device=dev).manual_seed(11)
