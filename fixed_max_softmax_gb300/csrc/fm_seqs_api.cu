@@ -46,11 +46,26 @@ int check_group(int64_t Hq, int64_t Hk) {
   return FM_OK;
 }
 
+// Rows of a unit of the CUDA-core kernels: 8 or 16 where most requests' rows of a key head fit them.
+int simt_rows(int64_t T, int64_t n, int group) {
+  for (int rows = 8; rows <= 16; rows *= 2)
+    if (group <= rows && T * group <= rows * n) return rows;
+  return 64;
+}
+
 size_t space_bytes(int64_t n, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
   const int group = (int)(Hq / Hk);
-  const size_t simt = seqs_space(seqs_geom_simt(T, group), n, T, Hk, D).total;
+  size_t most = seqs_space(seqs_geom_simt(T, group, 64), n, T, Hk, D).total;
   const size_t tc = seqs_space(seqs_geom_tc(T, n, group), n, T, Hk, D).total;
-  return simt > tc ? simt : tc;
+  if (tc > most) most = tc;
+  for (int rows = 8; rows <= 16; rows *= 2) {
+    if (group > rows) continue;
+    // of as many tokens as a call with so few rows a request may have, so that no smaller call needs more
+    const int64_t t = T * group <= rows * n ? T : rows * n / group;
+    const size_t few = seqs_space(seqs_geom_simt(t, group, rows), n, t, Hk, D).total;
+    if (few > most) most = few;
+  }
+  return most;
 }
 
 // Every attention kernel's attributes, at the first call on the current device.
@@ -146,7 +161,8 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group), launch_seqs_tc);
   // fp32, and layouts that the tensor-core kernel or the tensor-map encoder does not take (a work
   // list made for it then goes unused)
-  if (e == cudaErrorNotSupported) e = run(seqs_geom_simt(a.q.S, group), launch_seqs_simt);
+  if (e == cudaErrorNotSupported)
+    e = run(seqs_geom_simt(a.q.S, group, simt_rows(a.q.S, a.n, group)), launch_seqs_simt);
   if (e != cudaSuccess) return cuda_fail(e, paged ? "fm_attn_paged launch" : "fm_attn_varlen launch");
   return FM_OK;
 }
