@@ -243,9 +243,11 @@ __global__ void __launch_bounds__(kT, 2) seqs_simt_kernel(const SimtArgs a, cons
 // rows are summed over those lanes by 7 exchanges that leave each lane one row's score, and for O a
 // lane holds 4 columns of all rows.  The warps' sums are joined at the end of a piece, in order.
 // Bound by the latency of its loads and by issue (about 100 instructions a key and 8 rows); fp32, 64
-// requests of up to 8,192 keys, 8 key heads, D = 128: 379 us with 8 rows (3.9 TB/s), 822 with 16,
-// 1,911 by the kernel above.  16 value rows in flight: 397 -> 379 us; more CTAs with fewer
-// registers, or 4 keys at a time, are slower (544, 437).
+// requests of up to 8,192 keys, 8 key heads, D = 128: 379 us with 8 rows (3.9 TB/s), 756 with 16,
+// 1,911 by the kernel above; bf16 on pages of 24 keys 473.  16 value rows in flight: 397 -> 379 us;
+// values asked for ahead: 819 -> 756 (16 rows), 578 -> 473 (bf16), and nothing for 8 rows of fp32;
+// keys asked for ahead too, more CTAs with fewer registers, or 4 keys at a time are slower (469,
+// 544, 437).
 constexpr int kWarps = 8, kBlock = 32;  // warps of a CTA, keys of a warp's step
 
 template <int D, int R>
@@ -325,6 +327,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) seqs_few_kernel(const SimtArgs
     for (int j0 = it.key0 + warp * kBlock; j0 < it.key1; j0 += kWarps * kBlock) {
       int page_next, row_next;
       place(j0 + kWarps * kBlock, page_next, row_next);
+      // the values on their way to L2 while the scores are computed (where fewer of their loads fit the
+      // registers, or bring half the bytes)
+      if constexpr (R == 16 || sizeof(E) == 2) {
+        if (vec && page >= 0) {
+          const E *vr = reinterpret_cast<const E *>(a.v.ptr) + it.h * a.v.sH + page * a.v.sB + row * a.v.sS;
+#pragma unroll
+          for (int d = 0; d < D; d += 128 / (int)sizeof(E)) asm volatile("prefetch.global.L2 [%0];" ::"l"(vr + d));
+        }
+      }
       // 1. scores of 32 keys
       float mx[RB];
 #pragma unroll
