@@ -82,6 +82,17 @@ def test_workspace_size(lib):
             fm.fm_attn_seqs_workspace_size(*bad)
 
 
+def test_workspace_size_never_shrinks(lib):
+    """Also where a larger call goes to another kernel or another tile of rows."""
+    for Hq, Hk in ((1, 1), (5, 1), (10, 2), (16, 1), (64, 1)):
+        sizes = [[fm.fm_attn_seqs_workspace_size(n, T, Hq, Hk, 64) for T in (1, 2, 7, 8, 9, 33, 500, 9000)]
+                 for n in (1, 2, 3, 30, 31, 500, 8192)]
+        for row in sizes:
+            assert row == sorted(row)
+        for column in zip(*sizes):
+            assert list(column) == sorted(column)
+
+
 def state(**kw):
     d = dict(n_seqs=4, page_size=16, num_pages=32, block_table=FAKE, table_stride=8, table_width=8, free_pages=FAKE,
              free_count=FAKE, free_count_out=FAKE, kv_len=FAKE, kv_len_out=FAKE)
