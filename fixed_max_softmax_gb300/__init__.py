@@ -518,12 +518,13 @@ def _ints(t, dtype, numel, name, device):
 
 
 def _table(t, n, device):
-    if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+    (rows, width), (stride, step) = (t.shape, t.stride()) if t.dim() == 2 else ((-2, 0), (0, 0))
+    if rows < n or t.dtype != torch.int32 or (width > 1 and step != 1):
         raise FMError(FM_ERR_ARG, f"block_table must be a 2-D int32 tensor of at least {n} rows with adjacent "
                                   f"entries, got {tuple(t.shape)} {t.dtype}")
     if t.get_device() != device:
         _not_here(t, "block_table", device)
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    return t.data_ptr(), stride, width
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone: a tenth of the time

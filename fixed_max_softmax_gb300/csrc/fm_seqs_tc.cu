@@ -29,7 +29,7 @@
 // the window (they meet p = 0, but may hold NaN), 3 fetches work and loads its Q, 4-7 and 8-11 softmax.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
 // Measured (us a call, plan and merge with it): decode batch of 64 over 8k keys (40 / 8 heads) 132, 83 %
-// of the copy rate; 24 prompts of up to 4,096 667, one of 33,001 7,850 (1,410 TFLOP/s, 74 % of the
+// of the copy rate; 24 prompts of up to 4,096 669, one of 33,001 7,930 (1,400 TFLOP/s, 73 % of the
 // measured burst rate).  Decoding is bound by HBM; prompts by the cycle of a group's softmax and its MMAs
 // (1.66 us a tile pair, of which 1.33 are MMAs), and by about 5 us of a unit's start and end.
 // (Figures of one kernel against another below are of calls made alone, L2 flushed before each.)
