@@ -53,6 +53,10 @@ int simt_rows(int64_t T, int64_t n, int group) {
   return 64;
 }
 
+// The workspace is given at any 16-byte boundary and used from the next of kSpaceAlign: partial results are
+// stored 32 bytes at a time, rows of theirs in whole 128-byte lines.
+constexpr size_t kSpaceAlign = 128;
+
 size_t space_bytes(int64_t n, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
   const int group = (int)(Hq / Hk);
   size_t most = seqs_space(seqs_geom_simt(T, group, 64), n, T, Hk, D).total;
@@ -65,7 +69,7 @@ size_t space_bytes(int64_t n, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
     const size_t few = seqs_space(seqs_geom_simt(t, group, rows), n, t, Hk, D).total;
     if (few > most) most = few;
   }
-  return most;
+  return most + kSpaceAlign - 16;
 }
 
 // Every attention kernel's attributes, at the first call on the current device.
@@ -142,7 +146,7 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   const size_t need = space_bytes(a.n, a.q.S, a.q.H, a.k.H, a.q.D);
   if (workspace_bytes < need) return fail(FM_ERR_ARG, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
   if (!workspace || misaligned(workspace, 16)) return fail(FM_ERR_ARG, "workspace must be given, 16-byte aligned");
-  a.ws = workspace;
+  a.ws = reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(workspace) + kSpaceAlign - 1) & ~(uintptr_t)(kSpaceAlign - 1));
   a.err = dev_error_ptr();
   a.timeout_ns = wait_timeout_ns();
   if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");

@@ -84,3 +84,25 @@ def test_extend_and_write_stay_inside(dev, n, cap, ps):  # noqa: F811
         fm.fm_sync_status()
         assert all(b.intact() for b in every) and kc.intact() and vc.intact(), step
         assert (status.t.item() == 0) == (new < 10 ** 6)
+
+
+@pytest.mark.parametrize("shift", [16, 32, 48, 112])
+@pytest.mark.parametrize("dtype,D,ps", [(BF16, 128, 16), (F16, 64, 128), (F32, 64, 16), (BF16, 128, 5)])
+@pytest.mark.parametrize("lens", [LONG, [(1, 9000)], [(400, 5000)]])
+def test_workspace_at_any_16_byte_boundary(dev, shift, dtype, D, ps, lens):  # noqa: F811
+    """Units cut along their keys, so that partial results are stored: in a workspace of exactly the stated size
+    that begins 16, 32, 48 or 112 bytes past a 128-byte line, as one cut from a pool may."""
+    g = torch.Generator(device=dev).manual_seed(32)
+    ks, vs, kc, vc, table = paged_case(g, lens, 2, D, ps, dtype, True)
+    T = sum(a for a, _ in lens)
+    q = rand(g, T, 10, D, dtype=dtype)
+    o, lse = torch.full_like(q, 7.0), torch.full((10, T), 7.0, device=dev)
+    nbytes = fm.fm_attn_seqs_workspace_size(len(lens), T, 10, 2, D)
+    whole = Space(nbytes + shift, dev)
+    ws = whole.t[shift:]
+    assert ws.data_ptr() % 128 == shift and ws.numel() == nbytes
+    fm.fm_attn_paged(q, kc, vc, ints(starts([a for a, _ in lens]), dev), ints([b for _, b in lens], dev), table, fm.seqs_opts(),
+                     o, lse, ws)
+    fm.fm_sync_status()
+    assert whole.intact() and bool((whole.t[:shift] == 0xA5).all())
+    check_paged(q, ks, vs, lens, o, lse)
