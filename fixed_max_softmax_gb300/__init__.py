@@ -552,6 +552,8 @@ def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream, device):
         lse = lse.data_ptr()
     ws = nbytes = 0
     if workspace is not None:
+        if not workspace.is_contiguous():  # its elements' bytes would not be a range that the kernels may write
+            raise FMError(FM_ERR_ARG, f"workspace must be contiguous, got shape {tuple(workspace.shape)}, strides {workspace.stride()}")
         if workspace.get_device() != device:
             _not_here(workspace, "workspace", device)
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -198,3 +198,19 @@ def test_binding_checks_integer_tensors():
         fm._table(torch.zeros(3, 4, dtype=torch.int32).t(), 3, 0)
     with pytest.raises(fm.FMError, match="block_table"):
         fm._table(torch.zeros(2, 4, dtype=torch.int32), 3, 0)
+
+
+@pytest.mark.parametrize("ws", [torch.empty(1, dtype=torch.uint8).expand(1 << 30), torch.empty(1 << 16, dtype=torch.uint8)[::2],
+                                torch.empty(64, 128).t()], ids=["expanded", "every other byte", "transposed"])
+@pytest.mark.parametrize("paged", [False, True])
+def test_binding_refuses_a_workspace_that_is_no_range_of_bytes(lib, monkeypatch, ws, paged):
+    """One byte expanded to a gigabyte passes for a workspace by its number of elements."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # (where get_device() says that host tensors are)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q, cache = torch.zeros(4, 2, 128), torch.zeros(3, 2, 16, 128)
+    with pytest.raises(fm.FMError, match="contiguous") as e:
+        if paged:
+            fm.fm_attn_paged(q, cache, cache, i(2), i(1), i(1, 4), fm.seqs_opts(), q, None, ws, stream=0)
+        else:
+            fm.fm_attn_varlen(q, q, q, i(2), i(2), fm.seqs_opts(), q, None, ws, stream=0)
+    assert e.value.code == fm.FM_ERR_ARG
