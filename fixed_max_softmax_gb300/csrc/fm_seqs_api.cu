@@ -111,9 +111,10 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   a.window = opts ? opts->window : 0;
   if (a.window > 0 && !a.causal) return fail(FM_ERR_ARG, "a window needs causal = 1");
   if (a.window >= kMaxRows) a.window = 0;  // no request has more keys
+  if (opts && isnan(opts->softmax_scale)) return fail(FM_ERR_ARG, "softmax_scale must be finite");
   const double scale = (opts && opts->softmax_scale > 0.f) ? (double)opts->softmax_scale : 1.0 / sqrt((double)a.q.D);
-  if (!isfinite(scale)) return fail(FM_ERR_ARG, "softmax_scale must be finite");
   a.alpha = (float)(scale * 1.4426950408889634);
+  if (!isfinite(a.alpha)) return fail(FM_ERR_ARG, "softmax_scale must be finite, in base 2 (times log2 e) too");
   if (!seqs) return fail(FM_ERR_ARG, "seqs is NULL");
   a.paged = paged;
   a.n = seqs->n_seqs;

@@ -214,3 +214,19 @@ def test_binding_refuses_a_workspace_that_is_no_range_of_bytes(lib, monkeypatch,
         else:
             fm.fm_attn_varlen(q, q, q, i(2), i(2), fm.seqs_opts(), q, None, ws, stream=0)
     assert e.value.code == fm.FM_ERR_ARG
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), 3.0e38, 2.4e38])
+def test_a_softmax_scale_that_is_no_number_is_refused(lib, paged, scale):
+    """NaN does not select the default, and a scale that overflows when taken to base 2 (2.36e38 and more) is as
+    infinite as infinity."""
+    assert attn(lib, paged, opt=fm.seqs_opts(softmax_scale=scale)) == fm.FM_ERR_ARG
+    assert "softmax_scale" in fm.fm_last_error()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("-inf"), 1e-45, 1e38])
+def test_a_softmax_scale_that_is_one_gets_past_that_check(lib, paged, scale):
+    assert attn(lib, paged, opt=fm.seqs_opts(softmax_scale=scale), nbytes=1000) == fm.FM_ERR_ARG
+    assert "workspace" in fm.fm_last_error()
