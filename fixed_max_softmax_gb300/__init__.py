@@ -473,7 +473,8 @@ class HostPipeline:
 
 # ---- requests of different lengths, and a paged key/value cache ------------------------------------
 def seqs_opts(causal: bool = True, window: int = 0, softmax_scale: float = 0.0) -> fm_seqs_opts:
-    return fm_seqs_opts(float(softmax_scale), int(bool(causal)), int(window))
+    # (a C int32 would take the window's low 32 bits; no request has 2^31 keys)
+    return fm_seqs_opts(float(softmax_scale), int(bool(causal)), max(-1, min(int(window), 2 ** 31 - 1)))
 
 
 # These calls are made once a layer and step, often for a few microseconds of work, so their arguments

@@ -230,3 +230,10 @@ def test_a_softmax_scale_that_is_no_number_is_refused(lib, paged, scale):
 def test_a_softmax_scale_that_is_one_gets_past_that_check(lib, paged, scale):
     assert attn(lib, paged, opt=fm.seqs_opts(softmax_scale=scale), nbytes=1000) == fm.FM_ERR_ARG
     assert "workspace" in fm.fm_last_error()
+
+
+@pytest.mark.parametrize("window,held", [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1),
+                                         (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 63 - 1, 2 ** 31 - 1), (-1, -1), (-2 ** 32, -1)])
+def test_a_window_past_32_bits_is_not_cut_to_its_low_bits(window, held):
+    """2^32 + 5 is no window of 5 keys, -2^32 not none."""
+    assert fm.seqs_opts(window=window).window == held
