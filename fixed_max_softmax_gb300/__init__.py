@@ -640,7 +640,8 @@ class PagedKVCache:
     kv_len; write(k, v) puts their rows into the pages; attention(q) attends over them.  Everything
     stays on the device: nothing here waits for the GPU, and status (0: the last extend fitted) is read
     when the caller chooses.  Several layers share one bookkeeping by sharing it: PagedKVCache(...,
-    shared=first) keeps pages of its own and uses the first layer's tables."""
+    shared=first) keeps pages of its own (heads, head dimension and type as it likes) and uses the first
+    layer's tables, so that its num_pages, page_size and limits have to be the first one's."""
 
     def __init__(self, num_pages, page_size, kv_heads, head_dim, max_seqs, max_pages_per_seq, max_tokens,
                  dtype=torch.bfloat16, device="cuda", shared: "PagedKVCache | None" = None):
@@ -651,6 +652,12 @@ class PagedKVCache:
         if shared is not None:
             if (shared.page_size, shared.free_pages.numel()) != (self.page_size, num_pages):
                 raise FMError(FM_ERR_SHAPE, "layers that share tables need the same pages")
+            has = (shared.kv_len.numel(), shared.block_table.shape[1], shared.slots.numel())
+            if has != (max_seqs, max_pages_per_seq, max_tokens):
+                raise FMError(FM_ERR_SHAPE, "layers that share tables have the first one's max_seqs, max_pages_per_seq and "
+                                            f"max_tokens {has}, not {(max_seqs, max_pages_per_seq, max_tokens)}")
+            if shared.kv_len.device != pages.device:
+                raise FMError(FM_ERR_ARG, f"layers that share tables are on one device: {shared.kv_len.device}, not {pages.device}")
             for name in ("block_table", "free_pages", "free_count", "kv_len", "cu_q", "slots", "positions", "status"):
                 setattr(self, name, getattr(shared, name))
         else:

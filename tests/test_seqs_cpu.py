@@ -237,3 +237,19 @@ def test_a_softmax_scale_that_is_one_gets_past_that_check(lib, paged, scale):
 def test_a_window_past_32_bits_is_not_cut_to_its_low_bits(window, held):
     """2^32 + 5 is no window of 5 keys, -2^32 not none."""
     assert fm.seqs_opts(window=window).window == held
+
+
+def test_layers_that_share_tables_share_their_limits():
+    """A second layer asked for more rows, wider tables or more tokens does not get the first one's without a word."""
+    make = lambda *limits, device="cpu", **kw: fm.PagedKVCache(6, 4, 2, 64, *limits, device=device, **kw)  # noqa: E731
+    first = make(3, 5, 7)
+    second = fm.PagedKVCache(6, 4, 1, 128, 3, 5, 7, dtype=torch.float32, device="cpu", shared=first)
+    assert second.kv_len is first.kv_len and second.slots is first.slots and second.k.shape == (6, 1, 4, 128)
+    for limits in ((4, 5, 7), (3, 6, 7), (3, 5, 8), (2, 5, 7)):
+        with pytest.raises(fm.FMError, match="max_seqs") as e:
+            make(*limits, shared=first)
+        assert e.value.code == fm.FM_ERR_SHAPE
+    with pytest.raises(fm.FMError, match="one device"):
+        make(3, 5, 7, device="meta", shared=first)
+    with pytest.raises(fm.FMError, match="same pages"):
+        fm.PagedKVCache(6, 8, 2, 64, 3, 5, 7, device="cpu", shared=first)
