@@ -1,6 +1,7 @@
 """The variants of the serving attention that only some sizes and layouts reach, each against the plain 64-bit
 computation: long packed prompts at D = 64, pages whose pitch no grouped tensor map describes, windows at D = 64 and
-in fp16, work lists of more than one pass of the planning CTA with cut units among them, batches of mostly idle rows."""
+in fp16, work lists of more than one pass of the planning CTA with cut units among them, batches of mostly idle rows;
+the largest number of requests, and calls of nothing."""
 import pytest
 import torch
 
@@ -145,3 +146,72 @@ def test_decoding_rows_in_long_buffers(dev, dtype, D):  # noqa: F811
     check_paged(q[:24], ks, vs, lens, o[:24], lse[:, :24])
     assert (o[24:] == 7.0).all() and (lse[:, 24:] == 7.0).all()
     assert starts([a for a, _ in lens])[-1] == 24
+
+
+@pytest.mark.parametrize("dtype,G,tokens", [(BF16, 4, 1), (F16, 16, 9), (F32, 4, 1), (F32, 16, 1), (F32, 16, 5)])
+def test_the_largest_number_of_requests(dev, dtype, G, tokens):  # noqa: F811
+    """FM_MAX_SEQS requests: even runs and a work list on the tensor cores, units of 8, 16 and 64 rows on the CUDA cores;
+    a sample of the requests, those in the last pass of the planning CTA among them."""
+    g = torch.Generator(device=dev).manual_seed(58)
+    n, D = fm.FM_MAX_SEQS, 64
+    lens = [(tokens, tokens + (i * 7) % 40) for i in range(n)]
+    lens[5000] = (tokens, 3000)
+    cq, ck = starts([a for a, _ in lens]), starts([b for _, b in lens])
+    q, k, v = (rand(g, t, h, D, dtype=dtype) for t, h in ((cq[-1], G), (ck[-1], 1), (ck[-1], 1)))
+    o, lse = run_varlen(q, k, v, lens, dev=dev)
+    for i in (0, 1, 383, 384, 1023, 1024, 4999, 5000, 5001, 7167, 7168, n - 2, n - 1):
+        a, b = slice(cq[i], cq[i + 1]), slice(ck[i], ck[i + 1])
+        r = attend(q[a], k[b], v[b], True, 0, D ** -0.5)
+        assert_close(o[a], lse[:, a], *r, dtype, dtype, D, lens[i][1])
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("n,cap", [(8192, 9000), (8192, 3000)])
+def test_extend_of_the_largest_number_of_requests(dev, n, cap):  # noqa: F811
+    """One token each in place (as many as the slots hold), by one CTA and by the two kernels."""
+    t32 = dict(dtype=torch.int32, device=dev)
+    new = torch.zeros(n, **t32)
+    new[:min(n, cap)] = 1
+    kv = (torch.arange(n, device=dev) % 4).int()  # pages of 4: none, or one that the token still fits
+    held = int((kv > 0).sum())
+    pages = n + 3
+    table = torch.full((n, 2), -1, **t32)
+    table[kv > 0, 0] = torch.arange(held, **t32)
+    free = torch.full((pages,), -1, **t32)
+    free[:pages - held] = torch.arange(held, pages, **t32)
+    count, cu, status = torch.tensor([pages - held], **t32), torch.zeros(n + 1, **t32), torch.full((1,), 9, **t32)
+    slots, pos = torch.full((cap,), 9, dtype=torch.int64, device=dev), torch.full((cap,), 9, **t32)
+    fresh = ((kv == 0) & (new == 1)).cpu()
+    page = table[:, 0].cpu().long()
+    page[fresh] = free.cpu().long()[pages - held - 1 - torch.arange(int(fresh.sum()))]
+    want = (page * 4 + kv.cpu().long())[:min(n, cap)]
+    want_pos, want_kv = kv.cpu()[:min(n, cap)], kv + new
+    fm.fm_paged_extend(new, None, kv, kv, table, free, count, count, 4, cu, slots, pos, status)
+    fm.fm_sync_status()
+    assert status.item() == 0 and torch.equal(kv, want_kv) and count.item() == pages - held - int(fresh.sum())
+    assert torch.equal(slots[:len(want)].cpu(), want) and torch.equal(pos[:len(want)].cpu(), want_pos)
+    assert (slots[len(want):] == -1).all() and (pos[len(want):] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_pages_no_keys_no_queries(dev, dtype):  # noqa: F811
+    """Caches of no page, tables of no column, keys of no row: every query sees nothing.  And calls of no query."""
+    q = torch.ones(5, 4, 64, dtype=dtype, device=dev)
+    none = torch.empty(0, 2, 16, 64, dtype=dtype, device=dev)
+    lens = [(2, 0), (0, 0), (3, 0)]
+    for pages in (none, torch.full((3, 2, 16, 64), float("nan"), dtype=dtype, device=dev)):
+        o, lse = run_paged(q, pages, pages, torch.empty(3, 0, dtype=torch.int32, device=dev), lens, dev)
+        fm.fm_sync_status()
+        assert (o == 0).all() and torch.isneginf(lse).all()
+    rows = torch.empty(0, 2, 64, dtype=dtype, device=dev)
+    o, lse = run_varlen(q, rows, rows, lens, dev=dev)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = run_varlen(q[:0], rows, rows, [(0, 0)] * 3, dev=dev)
+    assert o.numel() == lse.numel() == 0
+    c = fm.PagedKVCache(3, 16, 2, 64, 2, 1, 4, dtype=dtype, device=dev)
+    c.extend(torch.zeros(2, dtype=torch.int32, device=dev))
+    c.write(rows, rows)
+    assert c.attention(q[:0]).shape == (0, 4, 64)
+    assert not c.attention(q).any()  # five rows behind the last token
+    fm.fm_sync_status()
+    assert c.status.tolist() == [0]
