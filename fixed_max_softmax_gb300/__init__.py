@@ -15,10 +15,10 @@ Functions with the ABI's names (same arguments, torch tensors in place of pointe
 ``fm_attn_seqs_workspace_size``, ``fm_attn_varlen``, ``fm_attn_paged``, ``fm_paged_extend``,
 ``fm_paged_write``.
 
-``attention_varlen()`` is the one-call form of packed prompts, ``PagedKVCache`` owns a paged
-cache with its bookkeeping (extend, write, attention).  ``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
+``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
 (bounds, one ``fm_attn_chunk`` per KV chunk, finalize); ``attention()`` is the
-one-call form.
+one-call form.  ``attention_varlen()`` is the one-call form of packed prompts, ``PagedKVCache``
+owns a paged cache with its bookkeeping (extend, write, attention).
 
 There is no CPU path: if the library is not built, ``load()`` raises.
 """
@@ -682,7 +682,8 @@ class PagedKVCache:
 
     def attention(self, q, out=None, lse=None, causal=True, window=0, softmax_scale=0.0, stream=None):
         """q [T, Hq, D], the new tokens' queries in the order of the last extend; returns o [T, Hq, D]
-        (rows behind the last token are left as they were in `out`, zero without one)."""
+        (rows behind the last token are left as they were in `out`, zero without one).  A step that is
+        not captured is quicker with `out`: nothing has to be filled with zeros."""
         T, Hq, D = q.shape
         with _on_stream(stream):
             if out is None:

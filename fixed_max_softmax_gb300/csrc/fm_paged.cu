@@ -10,13 +10,14 @@
 // One cluster of CTAs moves the pages: every CTA takes the prefix sums of all requests for itself
 // (12 bytes a request, read through L2), so that the CTAs meet only once, between the last read of
 // the old state and the first write of the new one, which is what allows kv_len, free_count and the
-// rows of reused requests to be updated in place.  Up to 4,096 tokens the same CTA writes their
-// slots, a token's page taken from the free list by its rank; beyond that a second kernel over the
-// whole GPU does, from the finished table (336,704 tokens of 96 requests: 29.8 us by the cluster
-// alone, 11.3 by the two).  Bound by the latency of a few dependent loads, then by the 12 bytes a token.
+// rows of reused requests to be updated in place.  Where the slots have room for up to 4,096 tokens the
+// same CTA fills them, a token's page taken from the free list by its rank; where for more, a second
+// kernel over the whole GPU does, from the finished table (336,704 tokens of 96 requests: 29.8 us by the
+// cluster alone, 11.1 by the two).  The room decides, not the tokens, whose number is on the device: all of it is
+// filled, with -1 behind the last token.  Bound by the latency of a few dependent loads, then by 12 bytes a slot.
 //
 // fm_paged_write: a copy of rows to their slots, bound by HBM (each row read and written once): 53,013
-// tokens of 8 heads, D = 128, in 71.5 us, 90 % of the copy rate.
+// tokens of 8 heads, D = 128, in 72.5 us, 89 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>

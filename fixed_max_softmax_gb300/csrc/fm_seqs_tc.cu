@@ -2,8 +2,8 @@
 // packed prompts, chunks over a paged cache, and decoding, for bf16 and fp16, D = 64 or 128.
 //
 //   S = Q K^T   tcgen05.mma, Q and K from swizzled shared memory (TMA), fp32 in tensor memory
-//   P           online softmax of the rows (running max, rescaled lazily), rounded to 16 bits
-//               over S in tensor memory; sums in fp32 registers
+//   P           online softmax of the rows (running max, rescaled lazily), rounded to the inputs' type
+//               over S in tensor memory; sums in fp32 registers, of the weights before they are rounded
 //   O += P V    tcgen05.mma, P from tensor memory, V from shared memory
 //
 // Rows.  A tile's 128 rows are floor(128 / G) tokens x the G query heads of one key head, token by
@@ -28,12 +28,18 @@
 // 12 warps: 0 K/V producer, 1 MMA issuer (and TMEM), 2 zeroes V rows past the request's end or before
 // the window (they meet p = 0, but may hold NaN), 3 fetches work and loads its Q, 4-7 and 8-11 softmax.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).
-// Measured (us a call, plan and merge with it): decode batch of 64 over 8k keys (40 / 8 heads) 132, 83 %
-// of the copy rate; 24 prompts of up to 4,096 669, one of 33,001 7,930 (1,400 TFLOP/s, 73 % of the
+// Measured (us a call, plan and merge with it): decode batch of 64 over 8k keys (40 / 8 heads) 130, 84 %
+// of the copy rate; 24 prompts of up to 4,096 676, one of 33,001 7,957 (1,400 TFLOP/s, 73 % of the
 // measured burst rate).  Decoding is bound by HBM; prompts by the cycle of a group's softmax and its MMAs
 // (1.66 us a tile pair, of which 1.33 are MMAs), and by about 5 us of a unit's start and end.
 // (Figures of one kernel against another below are of calls made alone, L2 flushed before each.)
 // Every wait is bounded; on expiry the kernel records it and returns, as the chunk kernel does.
+//
+// P has 16 bits because the operands of a tcgen05.mma of 16-bit kind share one type, and V has the
+// inputs'; as tf32, V would have to be converted and the MMA would run at half the rate.  Each weight is off
+// by at most half a step (2^-8 relative in bf16, 2^-11 in fp16), o by no more than that of sum p |v|: over whole
+// outputs 0.0020 to 0.0023 (2-norm, bf16) and 0.0003 (fp16) from 64 bits, where rounding o alone leaves
+// 0.0016 to 0.0017 and 0.0002.
 #include <cudaTypedefs.h>
 #include <limits.h>
 #include <string.h>
@@ -135,8 +141,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
 // a loop over the two halves of the columns (LOOPS = 1) for the same reason: 203 -> 185 us for 32
 // prompts of 1,024 (16 / 4 heads, D = 128), 727 -> 674 us for 24 of up to 4,096 (40 / 8 heads), and no
 // loss at 33k (7.82 and 7.78 ms).  At D = 64 a tile has half the MMA time to hide it, and long
-// prompts do better unrolled (LOOPS = 2): 2.89 -> 2.51 ms at 20,000, 232 -> 219 us for 4 of up to
-// 4,096, but 162 -> 166 us for 16 of up to 2,048.
+// prompts do better unrolled (LOOPS = 2), which packed prompts of 4,096 and more on average take: one of
+// 20,000 2.89 -> 2.51 ms, of 6,000 323 -> 289 us, of 4,096 180 -> 165; 4 of 4,096 each 575 -> 524, 16 of
+// them 2,143 -> 1,948.  Below, gains end between 2,048 (4 of them 191 -> 183 us, 16 628 -> 612) and 1,024 (4 of
+// them 83 -> 84); of unequal lengths, 16 of up to 2,048 lose (162 -> 166), 4 of up to 4,096 gain (232 -> 219).
+// The bound on the mean lies where every mix that was measured gains.
 template <typename E, int D, int LOOPS>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float alpha, bool have_o, float &run, float (&l)[4]) {
   uint32_t sa[32], sb[32], pk[16];
@@ -291,8 +300,9 @@ struct StreamRun {
   int parts, b, h, t;
   Request req;
 };
-// The line is measured in 32 bits, sums stopping at kMostLine: a call of so much (5e8 key tiles of a
-// key head, a minute's work and more) is refused as lengths that do not fit.
+// The line is measured in 32 bits, sums stopping at kMostLine: a call of so much (4.3e8 key tiles of units of
+// two row tiles, 5.4e8 of one: some 5 s of the whole GPU by the measure above) is refused as lengths that do
+// not fit.
 constexpr int kMostLine = 0x7fff0000;
 
 __device__ __forceinline__ int unit_cost(const Params &p, const Request &r, int t) {
@@ -1101,6 +1111,9 @@ SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
   // few queries a request: a tile of rows holds all of most requests' queries of a key head.  Even runs
   // against the list: decode batch of 64 149 and 158 us, 4 requests of 131k 149 and 171, a step of 120
   // decoding requests and 3 chunks 203 and 208; 24 packed prompts of up to 4,096 751 and 674.
+  // The rule knows the arrays, not the lengths in them, which are on the device: the decode batch in
+  // buffers of 2,048 rows takes the list (146 -> 155 us), a prompt of 6,000 among 255 idle rows even runs
+  // (325 -> 351).
   g.stream = T * group <= 128 * n ? 1 : 0;
   return g;
 }
@@ -1147,7 +1160,7 @@ cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace
   p.T = a.q.S;
   p.err = a.err;
   p.timeout_ns = a.timeout_ns;
-  // packed prompts of 4,096 queries and more on average, D = 64 (see softmax_tile)
+  // packed prompts of 4,096 queries and more on average (of the arrays' rows), D = 64 (see softmax_tile)
   const int mode = g.stream ? kStream : (a.q.D == 64 && !a.paged && a.q.S >= 4096 * a.n ? kLong : kList);
   if (a.q.dtype == FM_BF16)
     return a.q.D == 128 ? launch_dim<__nv_bfloat16, 128>(maps, p, grouped, mode, st)

@@ -451,8 +451,16 @@ FM_API int fm_bounds_noalloc(const fm_tensor *q, const fm_tensor *k_full, const 
  *   - With q_i queries and s_i keys, query t of request i stands at position p = s_i - q_i + t.
  *     causal: it sees keys j <= p; window > 0 (needs causal): only j > p - window.  A row that sees
  *     no key gets o = 0 and lse = -inf.
- *   - FM_F32, FM_BF16 or FM_F16, one type for q, k, v; sums, the row max and the normalise are fp32;
- *     for 16-bit inputs the weights p are rounded to that type before they meet v.
+ *   - FM_F32, FM_BF16 or FM_F16, one type for q, k, v; sums, the row max and the normalise are fp32.
+ *   - 16-bit types run on the tensor cores, where the weights p are rounded to that type before they meet v,
+ *     if every tensor's innermost stride is 1, its address and other strides are multiples of 16 bytes, no
+ *     stride of more than one element is 0 (a head expanded to several) and a page has 8, 16, 32, 64 or a
+ *     multiple of 128 rows.  Other 16-bit layouts and fp32 run on the CUDA cores, several times slower; p is
+ *     fp32 there.
+ *   - How the work is cut is chosen from the arrays' sizes (T, n_seqs, heads), since the lengths are
+ *     on the device.  Rows of q that no request owns and requests without queries change no result but
+ *     cost time: little on the tensor cores, up to five times for fp32 decoding in buffers far longer than its
+ *     rows.
  *   - Keys and values that no query of the request sees (past its end in its last page, its
  *     neighbours' rows, before every query's window) may hold anything, NaN too: they change
  *     nothing, and table entries of pages before the window are not read.  A value row that some
@@ -463,7 +471,7 @@ FM_API int fm_bounds_noalloc(const fm_tensor *q, const fm_tensor *k_full, const 
  *     capture).  Lengths that do not fit the tensors are clamped, cu_q that runs backwards computes
  *     nothing, a table entry outside [0, num_pages) reads as zeros, and the next fm_sync_status
  *     returns FM_ERR_INDEX; it does so too after a decoding call of more than about 4e8 tiles
- *     (128 keys of one key head each), which computes nothing.
+ *     (128 keys of one key head each; some 5 s of work), which computes nothing.
  *   - The workspace is scratch: its contents need no preparation and mean nothing afterwards.  Calls
  *     that may run at the same time need one each. */
 #define FM_MAX_GROUP 64
@@ -492,7 +500,7 @@ FM_API int fm_attn_seqs_workspace_size(int64_t n_seqs, int64_t T, int64_t Hq, in
 /* fm_attn_varlen -- attention over packed keys: whole prompts of different lengths.
  *   q [1, Hq, T, D];  k, v [1, Hk, Tk, D];  seqs: n_seqs, cu_q, cu_k
  *   o_out [1, Hq, T, D], q's type or FM_F32;  lse f32 [Hq, T] contiguous or NULL (natural log)
- *   workspace of fm_attn_seqs_workspace_size bytes, 16-byte aligned
+ *   workspace of fm_attn_seqs_workspace_size bytes, 16-byte aligned (a part of a larger buffer will do)
  * Deterministic: the same call gives the same bits.  Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE,
  * FM_ERR_UNSUPPORTED (D not 64 or 128, too many heads to a key head, requests or rows), FM_ERR_CUDA. */
 FM_API int fm_attn_varlen(const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
@@ -518,7 +526,8 @@ typedef struct {
   int32_t *kv_len_out;       /* [n], may be kv_len */
 } fm_page_state;
 
-/* fm_paged_extend -- room for the next tokens of every request, in one launch.
+/* fm_paged_extend -- room for the next tokens of every request: one launch where max_tokens is at most
+ * 4,096, two beyond (the room decides, not the tokens; all of slots and positions is written each time).
  *   new_len   int32 [n]  tokens to come (0: none)
  *   release   uint8 [n] or NULL: 1 = the request that held row i has ended: its pages go back to
  *             the list first, and new_len[i] tokens begin a new request in that row
