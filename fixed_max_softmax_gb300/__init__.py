@@ -13,7 +13,7 @@ Functions with the ABI's names (same arguments, torch tensors in place of pointe
 ``fm_probe_wait_timeout``,
 ``fm_last_error``, ``fm_version``; and for requests of different lengths
 ``fm_attn_seqs_workspace_size``, ``fm_attn_varlen``, ``fm_attn_paged``, ``fm_paged_extend``,
-``fm_paged_write``.
+``fm_paged_write``; for trees of drafted tokens ``fm_tree_mask``, ``fm_attn_tree``.
 
 ``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
 (bounds, one ``fm_attn_chunk`` per KV chunk, finalize); ``attention()`` is the
@@ -47,12 +47,13 @@ ABI_SYMBOLS = ("fm_bounds_workspace_size", "fm_bounds", "fm_attn_chunk", "fm_fin
                "fm_last_error", "fm_version", "fm_bounds_noalloc", "fm_finalize_lse", "fm_probe_wait_timeout",
                "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
-               "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write")
+               "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree")
 FM_MAX_CHUNKS = 8
 FM_MAX_SINKS = 8
 FM_NOALLOC_SCRATCH_BYTES = 4 << 20
 FM_MAX_GROUP = 64
 FM_MAX_SEQS = 8192
+FM_MAX_NODES = 1024
 
 
 class FMError(RuntimeError):
@@ -146,6 +147,8 @@ def load(path: str | None = None):
     lib.fm_attn_paged.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.fm_paged_extend.argtypes = [P, P, P, i64, P, P, P, P, P]
     lib.fm_paged_write.argtypes = [P, P, P, P, P, P]
+    lib.fm_tree_mask.argtypes = [P, P, i64, P, i64, i64, P, P]
+    lib.fm_attn_tree.argtypes = [P, P, P, P, P, i64, i64, P, P, P, P, ctypes.c_size_t, P]
     lib.fm_sync_status.argtypes = [P]
     lib.fm_last_error.restype = ctypes.c_char_p
     lib.fm_last_error.argtypes = []
@@ -154,7 +157,7 @@ def load(path: str | None = None):
                  "fm_version", "fm_bounds_noalloc", "fm_finalize_lse", "fm_probe_wait_timeout",
                  "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                  "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
-                 "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write"):
+                 "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -543,7 +546,7 @@ def fm_attn_seqs_workspace_size(n_seqs: int, T: int, Hq: int, Hk: int, D: int) -
     return n.value
 
 
-def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream, device):
+def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream, device, mask=()):
     if lse is not None:
         heads, rows = (q.shape[1], q.shape[0]) if q.dim() == 3 else (q.shape[1], q.shape[2])
         if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != heads * rows:
@@ -558,7 +561,7 @@ def _attn_seqs(fn, q, k, v, seqs, opt, o_out, lse, workspace, stream, device):
         if workspace.get_device() != device:
             _not_here(workspace, "workspace", device)
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    rc = fn(_rows(q, "q", device), k, v, seqs, ctypes.byref(opt), _rows(o_out, "o_out", device), lse, ws, nbytes,
+    rc = fn(_rows(q, "q", device), k, v, seqs, *mask, ctypes.byref(opt), _rows(o_out, "o_out", device), lse, ws, nbytes,
             _stream_handle(stream, device))
     return rc if rc == FM_OK else _check(rc)
 
@@ -582,6 +585,40 @@ def fm_attn_paged(q, k_cache, v_cache, cu_q, kv_len, block_table, opt: fm_seqs_o
     seqs = _SEQS_BYTES(n, _ints(cu_q, i32, 1, "cu_q", dev), 0, _ints(kv_len, i32, n, "kv_len", dev), table, stride, width)
     return _attn_seqs(load().fm_attn_paged, q, _cache(k_cache, "k_cache", dev), _cache(v_cache, "v_cache", dev), seqs, opt,
                       o_out, lse, workspace, stream, dev)
+
+
+def _mask(t, rows, device):
+    """Data pointer, words and stride of a tree mask: a row for each of `rows` tokens."""
+    (have, words), (stride, step) = (t.shape, t.stride()) if t.dim() == 2 else ((-2, 0), (0, 0))
+    if have < rows or t.dtype != torch.int32 or (words > 1 and step != 1):
+        raise FMError(FM_ERR_ARG, f"mask must be a 2-D int32 tensor of at least {rows} rows with adjacent words, got "
+                                  f"{tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        _not_here(t, "mask", device)
+    return t.data_ptr(), words, stride
+
+
+def fm_tree_mask(parent, cu_q, kv_len, mask, positions=None, stream=None):
+    """mask int32 [T, words] (bit j of word j / 32) and positions int32 [T] of trees of drafted tokens: parent
+    int32 [T] counts from each request's first node, -1 a root; see include/fm.h."""
+    dev, n, i32, T = torch.cuda.current_device(), cu_q.numel() - 1, torch.int32, parent.numel()
+    seqs = _SEQS_BYTES(n, _ints(cu_q, i32, 1, "cu_q", dev), 0, _ints(kv_len, i32, n, "kv_len", dev), 0, 0, 0)
+    rc = load().fm_tree_mask(seqs, _ints(parent, i32, 0, "parent", dev), T, *_mask(mask, T, dev),
+                             None if positions is None else _ints(positions, i32, T, "positions", dev),
+                             _stream_handle(stream, dev))
+    return rc if rc == FM_OK else _check(rc)
+
+
+def fm_attn_tree(q, k_cache, v_cache, cu_q, kv_len, block_table, mask, opt: fm_seqs_opts, o_out, lse=None, workspace=None,
+                 stream=None):
+    """fm_attn_paged where of its request's new tokens each row sees those that its row of mask (int32
+    [T, words], from fm_tree_mask) names; see include/fm.h."""
+    dev, n, i32 = torch.cuda.current_device(), cu_q.numel() - 1, torch.int32
+    table, stride, width = _table(block_table, n, dev)
+    seqs = _SEQS_BYTES(n, _ints(cu_q, i32, 1, "cu_q", dev), 0, _ints(kv_len, i32, n, "kv_len", dev), table, stride, width)
+    rows = q.shape[0] if q.dim() == 3 else q.shape[2] if q.dim() == 4 else 0
+    return _attn_seqs(load().fm_attn_tree, q, _cache(k_cache, "k_cache", dev), _cache(v_cache, "v_cache", dev), seqs, opt,
+                      o_out, lse, workspace, stream, dev, _mask(mask, rows, dev))
 
 
 def fm_paged_extend(new_len, release, kv_len, kv_len_out, block_table, free_pages, free_count, free_count_out,

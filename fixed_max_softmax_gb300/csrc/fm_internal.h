@@ -24,6 +24,7 @@ enum : unsigned int {
   kDevErrPage = 8,        // a page table entry outside the cache (request, position, entry)
   kDevErrSlot = 9,        // a cache slot outside the cache (token, slot low and high word)
   kDevErrLength = 10,     // request lengths that do not fit the tensors (request, rows, keys)
+  kDevErrParent = 11,     // a node's parent is not an earlier node (request, node, parent)
 };
 
 // Debug builds (nvcc -DFM_DEBUG): FM_DCHECK(ok, err, site, index) is false when `ok` is, and then
@@ -164,6 +165,10 @@ struct SeqsArgs {
   int64_t table_stride, table_width;
   float alpha;           // softmax_scale * log2(e)
   int causal, window;
+  // trees of drafted tokens (paged, causal): what a token sees of its request's new tokens, a row of
+  // mask_words words a token
+  const uint32_t *mask = nullptr;
+  int64_t mask_words = 0, mask_stride = 0;
   float *lse;            // [Hq, T] or nullptr
   void *ws;
   unsigned int *err;
@@ -212,13 +217,27 @@ SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_
 cudaError_t seqs_plan_prepare();
 cudaError_t seqs_simt_prepare();
 cudaError_t seqs_tc_prepare();
+cudaError_t seqs_tree_simt_prepare();
+cudaError_t seqs_tree_tc_prepare();
 // Work list of the call into its workspace; then one of the attention kernels; then the merge.
 cudaError_t launch_seqs_plan(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 cudaError_t launch_seqs_simt(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 bool seqs_tc_supported(const SeqsArgs &a);
 // cudaErrorNotSupported, launching nothing, when the tensor maps cannot be encoded.
 cudaError_t launch_seqs_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+// The same two for trees of drafted tokens.
+cudaError_t launch_seqs_tree_simt(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+cudaError_t launch_seqs_tree_tc(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
 cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSpace &s, cudaStream_t st);
+
+struct TreeMaskArgs {
+  int64_t n, T, words, stride;
+  const int32_t *cu_q, *kv_len, *parent;
+  uint32_t *mask;
+  int32_t *positions;  // or nullptr
+  unsigned int *err;
+};
+cudaError_t launch_tree_mask(const TreeMaskArgs &a, cudaStream_t st);
 
 struct PagedExtendArgs {
   int64_t n, page_size, num_pages, table_stride, table_width, max_tokens;

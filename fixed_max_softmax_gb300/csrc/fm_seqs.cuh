@@ -2,6 +2,8 @@
 // tiles that a unit sees, and where a key's row lies.
 #pragma once
 
+#include <limits.h>
+
 #include "fm_internal.h"
 
 namespace fm {
@@ -78,6 +80,37 @@ inline SeqsLens seqs_lens(const SeqsArgs &a) {
 __device__ __forceinline__ void seen_keys(int p, int kv, int causal, int window, int &lo, int &hi) {
   hi = causal ? min(kv, p + 1) : kv;
   lo = window > 0 ? p - window + 1 : 0;
+}
+
+// Trees of drafted tokens.  Of its request's new tokens a row sees those whose bits are set in its mask
+// row, bit 0 being the first; earlier keys it sees all.  Causal requests (prompt chunks of more tokens
+// than a mask row has bits) get a base that no key reaches.
+struct TreeRow {
+  int base;              // the request's first new token among its keys
+  int words;             // of the mask row (0: no row)
+  const uint32_t *bits;
+};
+__device__ __forceinline__ TreeRow tree_row(const SeqsLens &s, const uint32_t *mask, int words, int64_t stride, int b, int kv,
+                                            int64_t row, bool ok) {
+  const int q0 = (int)max((int64_t)0, min((int64_t)s.cu_q[b], s.T));
+  const int q = (int)max((int64_t)q0, min((int64_t)s.cu_q[b + 1], s.T)) - q0;
+  TreeRow r;
+  r.base = q <= 32 * words ? kv - q : INT_MAX;
+  r.words = ok ? words : 0;
+  r.bits = mask + row * stride;
+  return r;
+}
+// Bits n0 .. n0 + 31 of a mask row; the keys before its bit 0 are all seen, those behind its last word not.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *bits, int words, int n0) {
+  const int w = n0 >> 5;
+  const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? bits[w] : 0u);
+  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? bits[w + 1] : 0u);
+  return __funnelshift_r(lo, hi, (uint32_t)n0 & 31u);
+}
+// Is the key at `key` seen?
+__device__ __forceinline__ bool tree_sees(const TreeRow &r, int key) {
+  const int n = key - r.base;
+  return n < 0 || ((n >> 5) < r.words && ((r.bits[n >> 5] >> (n & 31)) & 1u));
 }
 
 __device__ __forceinline__ void report_bad_page(unsigned int *err, int request, int position, int page) {

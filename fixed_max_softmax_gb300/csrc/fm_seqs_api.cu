@@ -83,14 +83,29 @@ cudaError_t prepare() {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev >= 0 && dev < kDevices && ready[dev])) return e;
   if ((e = seqs_plan_prepare()) != cudaSuccess || (e = seqs_simt_prepare()) != cudaSuccess ||
-      (e = seqs_tc_prepare()) != cudaSuccess)
+      (e = seqs_tc_prepare()) != cudaSuccess || (e = seqs_tree_simt_prepare()) != cudaSuccess ||
+      (e = seqs_tree_tc_prepare()) != cudaSuccess)
     return e;
   if (dev >= 0 && dev < kDevices) ready[dev] = true;
   return cudaSuccess;
 }
 
-// The call behind fm_attn_varlen and fm_attn_paged.
-int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
+// A mask of trees: rows of `words` words, `stride` apart.
+struct TreeMask {
+  const uint32_t *rows;
+  int64_t words, stride;
+};
+int check_mask(const TreeMask &m, int64_t rows) {
+  if (m.words < 1 || m.words > FM_MAX_NODES / 32)
+    return fail(m.words < 1 ? FM_ERR_ARG : FM_ERR_UNSUPPORTED, "mask rows of %lld words: 1 to %d", (long long)m.words,
+                FM_MAX_NODES / 32);
+  if (m.stride < m.words && rows > 1) return fail(FM_ERR_ARG, "mask rows of %lld words %lld apart", (long long)m.words, (long long)m.stride);
+  if ((rows > 0 && !m.rows) || misaligned(m.rows, 4)) return fail(FM_ERR_ARG, "mask must be given, 4-byte aligned");
+  return FM_OK;
+}
+
+// The call behind fm_attn_varlen, fm_attn_paged and fm_attn_tree (with a mask).
+int attn_seqs(const char *name, bool paged, const TreeMask *mask, const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
               const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace, size_t workspace_bytes,
               fm_stream_t stream) {
   clear_error();
@@ -113,6 +128,8 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   a.causal = opts ? opts->causal : 1;
   a.window = opts ? opts->window : 0;
   if (a.window > 0 && !a.causal) return fail(FM_ERR_ARG, "a window needs causal = 1");
+  if (mask && !a.causal) return fail(FM_ERR_ARG, "trees need causal = 1: a node sees no later one");
+  if (mask && a.window > 0) return fail(FM_ERR_UNSUPPORTED, "a window over trees is not supported");
   if (a.window >= kMaxRows) a.window = 0;  // no request has more keys
   if (opts && isnan(opts->softmax_scale)) return fail(FM_ERR_ARG, "softmax_scale must be finite");
   const double scale = (opts && opts->softmax_scale > 0.f) ? (double)opts->softmax_scale : 1.0 / sqrt((double)a.q.D);
@@ -142,6 +159,12 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
   } else if (!a.cu_k || misaligned(a.cu_k, 4)) {
     return fail(FM_ERR_ARG, "cu_k must be given, 4-byte aligned");
   }
+  if (mask) {
+    if ((rc = check_mask(*mask, a.q.S))) return rc;
+    a.mask = mask->rows;
+    a.mask_words = mask->words;
+    a.mask_stride = mask->stride;
+  }
   if (misaligned(lse, 4)) return fail(FM_ERR_ARG, "lse must be 4-byte aligned");
   a.lse = lse;
   const int group = (int)(a.q.H / a.k.H);
@@ -166,12 +189,12 @@ int attn_seqs(bool paged, const fm_tensor *q, const fm_tensor *k, const fm_tenso
     return e;
   };
   e = cudaErrorNotSupported;
-  if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group), launch_seqs_tc);
+  if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group), mask ? launch_seqs_tree_tc : launch_seqs_tc);
   // fp32, and layouts that the tensor-core kernel or the tensor-map encoder does not take (a work
   // list made for it then goes unused)
   if (e == cudaErrorNotSupported)
-    e = run(seqs_geom_simt(a.q.S, group, simt_rows(a.q.S, a.n, group)), launch_seqs_simt);
-  if (e != cudaSuccess) return cuda_fail(e, paged ? "fm_attn_paged launch" : "fm_attn_varlen launch");
+    e = run(seqs_geom_simt(a.q.S, group, simt_rows(a.q.S, a.n, group)), mask ? launch_seqs_tree_simt : launch_seqs_simt);
+  if (e != cudaSuccess) return cuda_fail(e, name);
   return FM_OK;
 }
 
@@ -193,13 +216,51 @@ int fm_attn_seqs_workspace_size(int64_t n_seqs, int64_t T, int64_t Hq, int64_t H
 int fm_attn_varlen(const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
                    const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace,
                    size_t workspace_bytes, fm_stream_t stream) {
-  return attn_seqs(false, q, k, v, seqs, opts, o_out, lse, workspace, workspace_bytes, stream);
+  return attn_seqs("fm_attn_varlen launch", false, nullptr, q, k, v, seqs, opts, o_out, lse, workspace, workspace_bytes, stream);
 }
 
 int fm_attn_paged(const fm_tensor *q, const fm_tensor *k_cache, const fm_tensor *v_cache, const fm_seqs *seqs,
                   const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace,
                   size_t workspace_bytes, fm_stream_t stream) {
-  return attn_seqs(true, q, k_cache, v_cache, seqs, opts, o_out, lse, workspace, workspace_bytes, stream);
+  return attn_seqs("fm_attn_paged launch", true, nullptr, q, k_cache, v_cache, seqs, opts, o_out, lse, workspace,
+                   workspace_bytes, stream);
+}
+
+int fm_attn_tree(const fm_tensor *q, const fm_tensor *k_cache, const fm_tensor *v_cache, const fm_seqs *seqs,
+                 const uint32_t *mask, int64_t mask_words, int64_t mask_stride, const fm_seqs_opts *opts,
+                 const fm_tensor *o_out, float *lse, void *workspace, size_t workspace_bytes, fm_stream_t stream) {
+  const TreeMask m = {mask, mask_words, mask_stride};
+  return attn_seqs("fm_attn_tree launch", true, &m, q, k_cache, v_cache, seqs, opts, o_out, lse, workspace, workspace_bytes,
+                   stream);
+}
+
+int fm_tree_mask(const fm_seqs *seqs, const int32_t *parent, int64_t T, uint32_t *mask, int64_t mask_words, int64_t mask_stride,
+                 int32_t *positions, fm_stream_t stream) {
+  clear_error();
+  if (!seqs) return fail(FM_ERR_ARG, "seqs is NULL");
+  if (seqs->n_seqs < 0 || T < 0) return fail(FM_ERR_ARG, "negative size");
+  if (seqs->n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)seqs->n_seqs, kMaxSeqs);
+  if (T > kMaxRows) return fail(FM_ERR_UNSUPPORTED, "more than 2^30 rows");
+  const int rc = check_mask({mask, mask_words, mask_stride}, T);
+  if (rc) return rc;
+  if (seqs->n_seqs == 0 || T == 0) return FM_OK;
+  if (!seqs->cu_q || !seqs->kv_len || !parent) return fail(FM_ERR_ARG, "every array of fm_tree_mask but positions must be given");
+  if (misaligned(seqs->cu_q, 4) || misaligned(seqs->kv_len, 4) || misaligned(parent, 4) || misaligned(positions, 4))
+    return fail(FM_ERR_ARG, "the arrays of fm_tree_mask must be aligned to their elements");
+  TreeMaskArgs a;
+  a.n = seqs->n_seqs;
+  a.T = T;
+  a.words = mask_words;
+  a.stride = mask_stride;
+  a.cu_q = seqs->cu_q;
+  a.kv_len = seqs->kv_len;
+  a.parent = parent;
+  a.mask = mask;
+  a.positions = positions;
+  a.err = dev_error_ptr();
+  if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
+  const cudaError_t e = launch_tree_mask(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_tree_mask launch");
 }
 
 int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const uint8_t *release, int64_t max_tokens,

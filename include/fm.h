@@ -514,6 +514,37 @@ FM_API int fm_attn_paged(const fm_tensor *q, const fm_tensor *k_cache, const fm_
                          const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace,
                          size_t workspace_bytes, fm_stream_t stream);
 
+/* ---- Trees of drafted tokens ------------------------------------------------------------------
+ * A request's new tokens may be guesses that a cheaper model has drafted: the nodes of a tree, packed
+ * like any new tokens (cu_q, their keys and values in the cache at consecutive positions).  Node 0 is
+ * the last token that is certain; a node's children are guesses at the token after it.
+ *   parent int32 [T]  the node's parent, counted from its request's first node: an earlier one, or -1
+ *   mask              rows of mask_words 32-bit words, mask_stride words apart, one a token: bit j (of
+ *                     word j / 32) of row t says that t sees node j of its request.  Bits of later
+ *                     nodes (j > t) and of nodes that the request does not have are not looked at.
+ * A request of more new tokens than a mask row has bits (a prompt chunk in the same call) is causal. */
+#define FM_MAX_NODES 1024 /* bits of a mask row, and nodes of a tree that fm_tree_verify takes */
+
+/* fm_tree_mask -- the mask of trees: every node sees itself and its ancestors.
+ *   seqs       n_seqs, cu_q and kv_len (keys with the nodes counted) are used
+ *   T          rows of parent, mask and positions; rows behind the last request are left as they are
+ *   mask       uint32 written, mask_words 1 to FM_MAX_NODES / 32; rows of causal requests are set to 0
+ *   positions  int32 [T] written, or NULL: kv_len - (new tokens) + the node's depth (of a causal
+ *              request its place), the position that a rotary embedding wants
+ * A parent that is not an earlier node is taken for -1 and reported by fm_sync_status (FM_ERR_INDEX), as
+ * cu_q that does not fit T rows is.  Errors: FM_ERR_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+FM_API int fm_tree_mask(const fm_seqs *seqs, const int32_t *parent, int64_t T, uint32_t *mask, int64_t mask_words,
+                        int64_t mask_stride, int32_t *positions, fm_stream_t stream);
+
+/* fm_attn_tree -- fm_attn_paged where each new token sees every key before its request's new tokens, and
+ * of these the ones up to itself that its mask row names: the nodes of one request, of different
+ * branches, in one call.  causal = 1, window = 0 (FM_ERR_ARG, FM_ERR_UNSUPPORTED otherwise).  A token
+ * whose row is 0 and that has no earlier key gets o = 0 and lse = -inf.  Values of nodes that no row of a
+ * mask names still have to be finite.  Workspace and errors as there. */
+FM_API int fm_attn_tree(const fm_tensor *q, const fm_tensor *k_cache, const fm_tensor *v_cache, const fm_seqs *seqs,
+                        const uint32_t *mask, int64_t mask_words, int64_t mask_stride, const fm_seqs_opts *opts,
+                        const fm_tensor *o_out, float *lse, void *workspace, size_t workspace_bytes, fm_stream_t stream);
+
 /* The state of a paged cache's bookkeeping (host struct of device arrays). */
 typedef struct {
   int64_t n_seqs, page_size, num_pages;
