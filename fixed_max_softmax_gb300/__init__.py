@@ -13,7 +13,7 @@ Functions with the ABI's names (same arguments, torch tensors in place of pointe
 ``fm_probe_wait_timeout``,
 ``fm_last_error``, ``fm_version``; and for requests of different lengths
 ``fm_attn_seqs_workspace_size``, ``fm_attn_varlen``, ``fm_attn_paged``, ``fm_paged_extend``,
-``fm_paged_write``; for trees of drafted tokens ``fm_tree_mask``, ``fm_attn_tree``.
+``fm_paged_write``; for trees of drafted tokens ``fm_tree_mask``, ``fm_attn_tree``, ``fm_tree_verify``.
 
 ``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
 (bounds, one ``fm_attn_chunk`` per KV chunk, finalize); ``attention()`` is the
@@ -47,7 +47,8 @@ ABI_SYMBOLS = ("fm_bounds_workspace_size", "fm_bounds", "fm_attn_chunk", "fm_fin
                "fm_last_error", "fm_version", "fm_bounds_noalloc", "fm_finalize_lse", "fm_probe_wait_timeout",
                "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
-               "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree")
+               "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree",
+               "fm_tree_verify")
 FM_MAX_CHUNKS = 8
 FM_MAX_SINKS = 8
 FM_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -149,6 +150,7 @@ def load(path: str | None = None):
     lib.fm_paged_write.argtypes = [P, P, P, P, P, P]
     lib.fm_tree_mask.argtypes = [P, P, i64, P, i64, i64, P, P]
     lib.fm_attn_tree.argtypes = [P, P, P, P, P, i64, i64, P, P, P, P, ctypes.c_size_t, P]
+    lib.fm_tree_verify.argtypes = [P, P, i64, P, P, P, P, P, i64, P, P, P, P]
     lib.fm_sync_status.argtypes = [P]
     lib.fm_last_error.restype = ctypes.c_char_p
     lib.fm_last_error.argtypes = []
@@ -157,7 +159,8 @@ def load(path: str | None = None):
                  "fm_version", "fm_bounds_noalloc", "fm_finalize_lse", "fm_probe_wait_timeout",
                  "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                  "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
-                 "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree"):
+                 "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree",
+                 "fm_tree_verify"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -512,7 +515,7 @@ def _not_here(t, name, device):
 
 
 def _ints(t, dtype, numel, name, device):
-    """Data pointer of a contiguous int tensor of at least numel elements."""
+    """Data pointer of a contiguous tensor of that dtype and of at least numel elements."""
     if t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
         raise FMError(FM_ERR_ARG, f"{name} must be a contiguous {dtype} tensor of at least {numel} elements, got "
                                   f"{tuple(t.shape)} {t.dtype}")
@@ -619,6 +622,32 @@ def fm_attn_tree(q, k_cache, v_cache, cu_q, kv_len, block_table, mask, opt: fm_s
     rows = q.shape[0] if q.dim() == 3 else q.shape[2] if q.dim() == 4 else 0
     return _attn_seqs(load().fm_attn_tree, q, _cache(k_cache, "k_cache", dev), _cache(v_cache, "v_cache", dev), seqs, opt,
                       o_out, lse, workspace, stream, dev, _mask(mask, rows, dev))
+
+
+def _probabilities(t, name, device):
+    """fm_tensor of a [T, V] tensor."""
+    if t.dim() != 2:
+        raise FMError(FM_ERR_SHAPE, f"{name}: expected a [T, V] tensor, got shape {tuple(t.shape)}")
+    if t.get_device() != device:
+        _not_here(t, name, device)
+    (T, V), (sT, sV) = t.shape, t.stride()
+    return _TENSOR_BYTES(t.data_ptr(), _DTYPES.get(t.dtype, -1), 0, 1, 1, T, V, 0, 0, sT, sV)
+
+
+def fm_tree_verify(target, draft, cu_q, tokens, parent, u, u_last, path, kept, next_token, stream=None):
+    """target and draft [T, V] probabilities after each node (draft None: the nodes were chosen, not drawn);
+    tokens, parent int32 [T], u float32 [T], u_last [n]; fills path int32 [n, max_path], kept and
+    next_token int32 [n]; see include/fm.h."""
+    dev, n, T, i32, f32 = torch.cuda.current_device(), cu_q.numel() - 1, target.shape[0], torch.int32, torch.float32
+    if path.dim() != 2 or path.shape[0] < n:
+        raise FMError(FM_ERR_ARG, f"path must be a contiguous int32 [{n}, max_path] tensor, got {tuple(path.shape)}")
+    rc = load().fm_tree_verify(_probabilities(target, "target", dev), None if draft is None else _probabilities(draft, "draft", dev),
+                               n, _ints(cu_q, i32, 1, "cu_q", dev), _ints(tokens, i32, T, "tokens", dev),
+                               _ints(parent, i32, T, "parent", dev), _ints(u, f32, T, "u", dev),
+                               _ints(u_last, f32, n, "u_last", dev), path.shape[1], _ints(path, i32, 0, "path", dev),
+                               _ints(kept, i32, n, "kept", dev), _ints(next_token, i32, n, "next_token", dev),
+                               _stream_handle(stream, dev))
+    return rc if rc == FM_OK else _check(rc)
 
 
 def fm_paged_extend(new_len, release, kv_len, kv_len_out, block_table, free_pages, free_count, free_count_out,

@@ -20,8 +20,9 @@ LIB = os.path.join(BUILD, "libfm.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 SOURCES = ["fm_api.cu", "fm_bounds.cu", "fm_chunk_simt.cu", "fm_chunk_tc.cu", "fm_finalize.cu",
            "fm_paged.cu", "fm_seqs_api.cu", "fm_seqs_plan.cu", "fm_seqs_simt.cu", "fm_seqs_tc.cu",
-           "fm_seqs_tree_simt.cu", "fm_seqs_tree_tc.cu", "fm_tree.cu"]
-HEADERS = ["fm_internal.h", "fm_seqs.cuh", "fm_seqs_simt.cuh", "fm_seqs_tc.cuh", "fm_tc.cuh"]
+           "fm_seqs_tree_simt.cu", "fm_seqs_tree_tc.cu", "fm_tree.cu", "fm_verify.cu"]
+HEADERS = ["fm_internal.h", "fm_seqs.cuh", "fm_seqs_simt.cuh", "fm_seqs_tc.cuh", "fm_tc.cuh",
+           "fm_tree.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 

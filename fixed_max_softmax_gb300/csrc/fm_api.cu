@@ -714,6 +714,9 @@ int fm_sync_status(fm_stream_t stream) {
     if (w[0] == kDevErrParent)
       return fail(FM_ERR_INDEX, "the parent of node %u of request %u is not an earlier node (%d); it was taken for a root", w[2],
                   w[1], (int)w[3]);
+    if (w[0] == kDevErrToken)
+      return fail(FM_ERR_INDEX, "the token of node %u of request %u is outside the vocabulary (%d); the node was not kept", w[2],
+                  w[1], (int)w[3]);
     if (w[0] == kDevErrDebugIndex)
       return fail(FM_ERR_INDEX,
                   "a debug build's index check failed and skipped the access (site %u, index %llu, block %u, "

@@ -25,6 +25,7 @@ enum : unsigned int {
   kDevErrSlot = 9,        // a cache slot outside the cache (token, slot low and high word)
   kDevErrLength = 10,     // request lengths that do not fit the tensors (request, rows, keys)
   kDevErrParent = 11,     // a node's parent is not an earlier node (request, node, parent)
+  kDevErrToken = 12,      // a node's token is outside the vocabulary (request, node, token)
 };
 
 // Debug builds (nvcc -DFM_DEBUG): FM_DCHECK(ok, err, site, index) is false when `ok` is, and then
@@ -238,6 +239,17 @@ struct TreeMaskArgs {
   unsigned int *err;
 };
 cudaError_t launch_tree_mask(const TreeMaskArgs &a, cudaStream_t st);
+
+struct TreeVerifyArgs {
+  const void *p, *q;  // the target's and the draft's rows (q or nullptr), sp and sq elements apart
+  int dtype;
+  int64_t sp, sq, T, V, n, max_path;
+  const int32_t *cu_q, *tokens, *parent;
+  const float *u, *u_last;
+  int32_t *path, *kept, *next;
+  unsigned int *err;
+};
+cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t st);
 
 struct PagedExtendArgs {
   int64_t n, page_size, num_pages, table_stride, table_width, max_tokens;

@@ -104,6 +104,20 @@ int check_mask(const TreeMask &m, int64_t rows) {
   return FM_OK;
 }
 
+// A row of probabilities a token: [1, 1, T, V], adjacent along V.
+int check_probabilities(const fm_tensor *t, const char *what) {
+  if (!t) return fail(FM_ERR_ARG, "%s: NULL tensor", what);
+  if (t->dtype == FM_F8E4M3 || t->dtype == FM_F8E5M2) return fail(FM_ERR_DTYPE, "%s: fp8 is not supported", what);
+  if (t->dtype != FM_F32 && t->dtype != FM_BF16 && t->dtype != FM_F16) return fail(FM_ERR_ARG, "%s: unknown dtype %d", what, t->dtype);
+  if (t->B != 1 || t->H != 1) return fail(FM_ERR_SHAPE, "%s: a [1, 1, T, V] tensor is wanted", what);
+  if (t->S < 0 || t->D < 1 || t->stride[2] < 0) return fail(FM_ERR_ARG, "%s: negative size or stride, or no vocabulary", what);
+  if (t->S > kMaxRows || t->D > kMaxRows) return fail(FM_ERR_UNSUPPORTED, "%s: more than 2^30 rows or tokens", what);
+  if (t->D > 1 && t->stride[3] != 1) return fail(FM_ERR_UNSUPPORTED, "%s: a row's probabilities must be adjacent", what);
+  if (t->S > 0 && !t->ptr) return fail(FM_ERR_ARG, "%s: NULL data pointer", what);
+  if (misaligned(t->ptr, t->dtype == FM_F32 ? 4 : 2)) return fail(FM_ERR_UNSUPPORTED, "%s: misaligned data", what);
+  return FM_OK;
+}
+
 // The call behind fm_attn_varlen, fm_attn_paged and fm_attn_tree (with a mask).
 int attn_seqs(const char *name, bool paged, const TreeMask *mask, const fm_tensor *q, const fm_tensor *k, const fm_tensor *v, const fm_seqs *seqs,
               const fm_seqs_opts *opts, const fm_tensor *o_out, float *lse, void *workspace, size_t workspace_bytes,
@@ -261,6 +275,50 @@ int fm_tree_mask(const fm_seqs *seqs, const int32_t *parent, int64_t T, uint32_t
   if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
   const cudaError_t e = launch_tree_mask(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_tree_mask launch");
+}
+
+int fm_tree_verify(const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q, const int32_t *tokens,
+                   const int32_t *parent, const float *u, const float *u_last, int64_t max_path, int32_t *path, int32_t *kept,
+                   int32_t *next_token, fm_stream_t stream) {
+  clear_error();
+  TreeVerifyArgs a;
+  int rc;
+  if ((rc = check_probabilities(target, "target"))) return rc;
+  if (draft) {
+    if ((rc = check_probabilities(draft, "draft"))) return rc;
+    if (draft->dtype != target->dtype) return fail(FM_ERR_DTYPE, "target and draft must share one dtype");
+    if (draft->S != target->S || draft->D != target->D) return fail(FM_ERR_SHAPE, "the shapes of target and draft differ");
+  }
+  if (n_seqs < 0 || max_path < 1) return fail(FM_ERR_ARG, "n_seqs = %lld, max_path = %lld", (long long)n_seqs, (long long)max_path);
+  if (n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)n_seqs, kMaxSeqs);
+  if (max_path > FM_MAX_NODES) return fail(FM_ERR_UNSUPPORTED, "paths of %lld nodes: at most %d", (long long)max_path, FM_MAX_NODES);
+  if (n_seqs == 0) return FM_OK;
+  if (!cu_q || !u_last || !path || !kept || !next_token || (target->S > 0 && (!tokens || !parent || !u)))
+    return fail(FM_ERR_ARG, "every array of fm_tree_verify but draft must be given");
+  if (misaligned(cu_q, 4) || misaligned(tokens, 4) || misaligned(parent, 4) || misaligned(u, 4) || misaligned(u_last, 4) ||
+      misaligned(path, 4) || misaligned(kept, 4) || misaligned(next_token, 4))
+    return fail(FM_ERR_ARG, "the arrays of fm_tree_verify must be aligned to their elements");
+  a.p = target->ptr;
+  a.q = draft ? draft->ptr : nullptr;
+  a.dtype = target->dtype;
+  a.sp = target->stride[2];
+  a.sq = draft ? draft->stride[2] : 0;
+  a.T = target->S;
+  a.V = target->D;
+  a.n = n_seqs;
+  a.max_path = max_path;
+  a.cu_q = cu_q;
+  a.tokens = tokens;
+  a.parent = parent;
+  a.u = u;
+  a.u_last = u_last;
+  a.path = path;
+  a.kept = kept;
+  a.next = next_token;
+  a.err = dev_error_ptr();
+  if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
+  const cudaError_t e = launch_tree_verify(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_tree_verify launch");
 }
 
 int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const uint8_t *release, int64_t max_tokens,

@@ -545,6 +545,34 @@ FM_API int fm_attn_tree(const fm_tensor *q, const fm_tensor *k_cache, const fm_t
                         const uint32_t *mask, int64_t mask_words, int64_t mask_stride, const fm_seqs_opts *opts,
                         const fm_tensor *o_out, float *lse, void *workspace, size_t workspace_bytes, fm_stream_t stream);
 
+/* fm_tree_verify -- the nodes of each tree that the target model keeps, and the token after them.
+ * Row t of target is the target's distribution of the token after node t, row t of draft the one that t's
+ * children were drawn from, independently, whatever their number.  The walk begins at node 0 and tries a
+ * node's children in order; with p, q the rows after the node that it stands at, A = 0 and S = 1 when it
+ * comes there, a child of token x and number u is kept if
+ *     u q(x) S < max(p(x) - A q(x), 0);  else A += S, S = sum_y max(p(y) - A q(y), 0)  (0: A = 0, S = 1).
+ * draft NULL: the children were chosen, not drawn; one is kept if u S < p(x), else S -= p(x) (not below 0)
+ * and p(x) = 0 for what follows at that node.  At a node that keeps no child the next token is the least x with
+ * sum_{y <= x} R(y) > u_last sum_y R(y), R what is left there of p: max(p - A q, 0), or p without the
+ * refused tokens (p itself where that leaves nothing).  With uniform numbers the tokens kept and the next
+ * one are distributed as the target's own.
+ *   target, draft  [1, 1, T, V], FM_F32, FM_BF16 or FM_F16 alike, adjacent along V, rows any distance apart.
+ *              They are taken to sum to 1 and are not scaled.  What is negative, infinite or NaN counts as 0
+ *   cu_q       int32 [n+1]: request i has nodes cu_q[i] .. cu_q[i+1]-1, at most FM_MAX_NODES
+ *   tokens, parent  int32 [T]; a node whose parent is not an earlier one is never tried
+ *   u          float [T], u_last float [n]: random numbers of [0, 1); 1 and more count as 1, NaN as 0
+ *   max_path   1 to FM_MAX_NODES: the walk ends after so many nodes
+ *   path       int32 [n, max_path] written: the nodes kept, node 0 first, -1 behind them
+ *   kept       int32 [n] written: their number; 0 for a request without nodes
+ *   next_token int32 [n] written: -1 for a request without nodes, or whose last row of p is all 0
+ * Tests and sums are made in 64 bits, so that the result is the definition's unless a number lies within
+ * some 2^-45 of a border.  A token outside the vocabulary is never kept, more than FM_MAX_NODES nodes are
+ * none; fm_sync_status reports both (FM_ERR_INDEX).  Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE,
+ * FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+FM_API int fm_tree_verify(const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q,
+                          const int32_t *tokens, const int32_t *parent, const float *u, const float *u_last,
+                          int64_t max_path, int32_t *path, int32_t *kept, int32_t *next_token, fm_stream_t stream);
+
 /* The state of a paged cache's bookkeeping (host struct of device arrays). */
 typedef struct {
   int64_t n_seqs, page_size, num_pages;

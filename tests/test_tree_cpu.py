@@ -63,3 +63,82 @@ def test_binding_refusals(lib, monkeypatch):  # noqa: F811
         with pytest.raises(fm.FMError, match="mask must be"):
             fm._mask(bad, 4, -1)
     assert fm._mask(torch.zeros(4, 5, dtype=torch.int32)[:, 1:3], 4, -1)[1:] == (2, 5)
+
+
+# ---------------------------------------------------------------- verification
+def rows(T=50, V=1000, dtype=fm.FM_F32, ptr=FAKE, step=1):
+    t = view(1, 1, T, V, dtype, ptr)
+    t.stride[3] = step
+    return t
+
+
+def verify(lib, p=None, q=None, n=3, max_path=8, **kw):  # noqa: F811
+    a = dict(cu=FAKE, tokens=FAKE, parent=FAKE, u=FAKE, u_last=FAKE, path=FAKE, kept=FAKE, nxt=FAKE)
+    a.update(kw)
+    return lib.fm_tree_verify(ctypes.byref(p or rows()), None if q is None else ctypes.byref(q), n, a["cu"], a["tokens"], a["parent"],
+                              a["u"], a["u_last"], max_path, a["path"], a["kept"], a["nxt"], None)
+
+
+def test_verify_refusals(lib):  # noqa: F811
+    assert lib.fm_tree_verify(None, None, 1, FAKE, FAKE, FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, None) == fm.FM_ERR_ARG
+    assert verify(lib, p=view(2, 1, 50, 1000, fm.FM_F32)) == fm.FM_ERR_SHAPE
+    assert verify(lib, p=view(1, 2, 50, 1000, fm.FM_F32)) == fm.FM_ERR_SHAPE
+    assert verify(lib, p=rows(V=0)) == fm.FM_ERR_ARG
+    assert verify(lib, p=rows(ptr=None)) == fm.FM_ERR_ARG
+    assert verify(lib, p=rows(ptr=FAKE + 2)) == fm.FM_ERR_UNSUPPORTED
+    assert verify(lib, p=rows(step=2)) == fm.FM_ERR_UNSUPPORTED
+    assert verify(lib, p=rows(V=2 ** 30 + 1)) == fm.FM_ERR_UNSUPPORTED
+    assert verify(lib, p=rows(dtype=fm.FM_F8E4M3)) == fm.FM_ERR_DTYPE
+    assert verify(lib, q=rows(dtype=fm.FM_BF16)) == fm.FM_ERR_DTYPE
+    assert verify(lib, q=rows(T=49)) == fm.FM_ERR_SHAPE
+    assert verify(lib, q=rows(V=999)) == fm.FM_ERR_SHAPE
+    assert verify(lib, n=-1) == fm.FM_ERR_ARG
+    assert verify(lib, n=fm.FM_MAX_SEQS + 1) == fm.FM_ERR_UNSUPPORTED
+    assert verify(lib, max_path=0) == fm.FM_ERR_ARG
+    assert verify(lib, max_path=fm.FM_MAX_NODES + 1) == fm.FM_ERR_UNSUPPORTED
+    for name in ("cu", "tokens", "parent", "u", "u_last", "path", "kept", "nxt"):
+        assert verify(lib, **{name: None}) == fm.FM_ERR_ARG, name
+        assert verify(lib, **{name: FAKE + 2}) == fm.FM_ERR_ARG, name
+    assert verify(lib, n=0, cu=None) == fm.FM_OK  # no request: nothing to do
+
+
+def test_verify_binding_refusals(lib, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # (where get_device() says that host tensors are)
+    i, f = (lambda *s: torch.zeros(s, dtype=torch.int32)), (lambda *s: torch.zeros(s))
+    good = [f(4, 10), f(4, 10), i(3), i(4), i(4), f(4), f(2), i(2, 5), i(2), i(2)]
+    for at, bad in ((0, f(4)), (2, i(3).long()), (3, i(3)), (4, i(4).long()), (5, i(4)), (6, f(1)), (7, i(10)), (7, i(1, 5)),
+                    (7, i(5, 2).t()), (8, i(1)), (9, f(2))):
+        with pytest.raises(fm.FMError):
+            fm.fm_tree_verify(*good[:at], bad, *good[at + 1:], stream=0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(fm.FMError, match="CUDA device"):
+        fm.fm_tree_verify(*good)
+
+
+def test_the_definition_is_lossless():
+    """Whatever the draft, the first new token is distributed as the target's row: children drawn from q, each kept or
+    refused by the definition, summed over every way that it can go, in exact fractions."""
+    from fractions import Fraction as F
+    p, q = [F(1, 2), F(1, 8), F(3, 8), F(0)], [F(1, 8), F(1, 2), F(1, 4), F(1, 8)]
+    for children in (0, 1, 2, 3):
+        got = [F(0)] * 4
+
+        def go(weight, a, mass, left_children):
+            left = [max(x - a * y, F(0)) for x, y in zip(p, q)]
+            if left_children == 0:
+                total = sum(left)
+                for x in range(4):
+                    got[x] += weight * left[x] / total
+                return
+            refused = F(0)
+            for x in range(4):  # the child's token, drawn from q; kept where u q S < what is left of p
+                keep = min(F(1), left[x] / (q[x] * mass))
+                got[x] += weight * q[x] * keep
+                refused += q[x] * (1 - keep)
+            if refused:
+                nxt = a + mass
+                rest = sum(max(x - nxt * y, F(0)) for x, y in zip(p, q))
+                go(weight * refused, *((nxt, rest) if rest else (F(0), F(1))), left_children - 1)
+
+        go(F(1), F(0), F(1), children)
+        assert got == p, children

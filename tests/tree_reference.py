@@ -8,7 +8,7 @@ import torch
 def random_tree(nodes, seed, back=8):
     """Parents of a tree: node 0 the root, each other node's parent among the `back` nodes before it."""
     r = random.Random(seed)
-    return [-1] + [r.randrange(max(0, t - back), t) for t in range(1, nodes)]
+    return ([-1] + [r.randrange(max(0, t - back), t) for t in range(1, nodes)])[:nodes]
 
 
 def ancestors(parent):
@@ -65,3 +65,48 @@ def attend_seen(q, k, v, seen, scale):
         a[rows, h] = p @ vh.abs()
         lse[h, rows] = torch.logsumexp(x[rows], 1)
     return o, lse, a, big
+
+
+def _some(row):
+    row = row.double().cpu()
+    return torch.where((row > 0) & (row < math.inf), row, torch.zeros_like(row))
+
+
+def walk(target, draft, tokens, parent, u, u_last, max_path):
+    """One request by the definition, in 64 bits: target, draft [nodes, V] (draft may be None); (path, next token).  The
+    refusals follow one another, each from what the last one left."""
+    V = target.shape[1]
+    one = lambda x: 0.0 if math.isnan(x) else min(max(x, 0.0), 1.0)  # noqa: E731
+    if len(tokens) == 0:
+        return [], -1
+    path = [0]
+    while True:
+        at, grown = path[-1], False
+        p = _some(target[at])
+        q = _some(draft[at]) if draft is not None else None
+        left, mass = p.clone(), 1.0
+        for t in range(at + 1, len(tokens)):
+            if parent[t] != at or not 0 <= tokens[t] < V or len(path) >= max_path:
+                continue
+            x = tokens[t]
+            if one(u[t]) * (1.0 if q is None else float(q[x])) * mass < float(left[x]):
+                path.append(t)
+                grown = True
+                break
+            if q is None:
+                mass = max(mass - float(left[x]), 0.0)
+                left[x] = 0.0
+            else:
+                left = (left - mass * q).clamp(min=0)
+                mass = float(left.sum())
+                if not mass > 0:
+                    left, mass = p.clone(), 1.0
+        if not grown:
+            break
+    if not float(left.sum()) > 0:
+        left = p
+    have = torch.nonzero(left).flatten()
+    if len(have) == 0:
+        return path, -1
+    upto = left.cumsum(0)
+    return path, min(int((upto <= one(u_last) * float(upto[-1])).sum()), int(have[-1]))
