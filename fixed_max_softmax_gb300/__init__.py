@@ -13,12 +13,14 @@ Functions with the ABI's names (same arguments, torch tensors in place of pointe
 ``fm_probe_wait_timeout``,
 ``fm_last_error``, ``fm_version``; and for requests of different lengths
 ``fm_attn_seqs_workspace_size``, ``fm_attn_varlen``, ``fm_attn_paged``, ``fm_paged_extend``,
-``fm_paged_write``; for trees of drafted tokens ``fm_tree_mask``, ``fm_attn_tree``, ``fm_tree_verify``.
+``fm_paged_write``; for trees of drafted tokens ``fm_tree_mask``, ``fm_attn_tree``, ``fm_tree_verify``,
+``fm_paged_keep``, ``fm_paged_move``.
 
 ``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
 (bounds, one ``fm_attn_chunk`` per KV chunk, finalize); ``attention()`` is the
 one-call form.  ``attention_varlen()`` is the one-call form of packed prompts, ``PagedKVCache``
-owns a paged cache with its bookkeeping (extend, write, attention).
+owns a paged cache with its bookkeeping (extend, write, attention; for drafted tokens tree,
+tree_attention, keep, move), ``verify_tree()`` is the one-call form of the verification.
 
 There is no CPU path: if the library is not built, ``load()`` raises.
 """
@@ -48,7 +50,7 @@ ABI_SYMBOLS = ("fm_bounds_workspace_size", "fm_bounds", "fm_attn_chunk", "fm_fin
                "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
                "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree",
-               "fm_tree_verify")
+               "fm_tree_verify", "fm_paged_keep", "fm_paged_move")
 FM_MAX_CHUNKS = 8
 FM_MAX_SINKS = 8
 FM_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -151,6 +153,8 @@ def load(path: str | None = None):
     lib.fm_tree_mask.argtypes = [P, P, i64, P, i64, i64, P, P]
     lib.fm_attn_tree.argtypes = [P, P, P, P, P, i64, i64, P, P, P, P, ctypes.c_size_t, P]
     lib.fm_tree_verify.argtypes = [P, P, i64, P, P, P, P, P, i64, P, P, P, P]
+    lib.fm_paged_keep.argtypes = [P, P, i64, P, P, P, P, P, P]
+    lib.fm_paged_move.argtypes = [i64, i64, P, P, P, P, P]
     lib.fm_sync_status.argtypes = [P]
     lib.fm_last_error.restype = ctypes.c_char_p
     lib.fm_last_error.argtypes = []
@@ -160,7 +164,7 @@ def load(path: str | None = None):
                  "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                  "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
                  "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree",
-                 "fm_tree_verify"):
+                 "fm_tree_verify", "fm_paged_keep", "fm_paged_move"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -678,6 +682,37 @@ def fm_paged_write(k, v, slots, k_cache, v_cache, stream=None):
     return rc if rc == FM_OK else _check(rc)
 
 
+def fm_paged_keep(cu_q, path, kept, kv_len, kv_len_out, block_table, free_pages, free_count, free_count_out, page_size: int,
+                  src, dst, status, stream=None):
+    """Of each request's new tokens only the first kept[i] of path[i] stay (-1: all): lengths, pages back to the list,
+    and the moves src, dst int64 [n, max_path] that fm_paged_move makes in each layer; see include/fm.h."""
+    dev, n, i32, i64 = torch.cuda.current_device(), kept.numel(), torch.int32, torch.int64
+    if path.dim() != 2 or path.shape[0] < n:
+        raise FMError(FM_ERR_ARG, f"path must be a contiguous int32 [{n}, max_path] tensor, got {tuple(path.shape)}")
+    width = path.shape[1]
+    table, stride, cols = _table(block_table, n, dev)
+    st = _STATE_BYTES(n, page_size, free_pages.numel(), table, stride, cols,
+                      _ints(free_pages, i32, 0, "free_pages", dev), _ints(free_count, i32, 1, "free_count", dev),
+                      _ints(free_count_out, i32, 1, "free_count_out", dev), _ints(kv_len, i32, n, "kv_len", dev),
+                      _ints(kv_len_out, i32, n, "kv_len_out", dev))
+    rc = load().fm_paged_keep(st, _ints(cu_q, i32, n + 1, "cu_q", dev), width, _ints(path, i32, 0, "path", dev),
+                              _ints(kept, i32, n, "kept", dev), _ints(src, i64, n * width, "src", dev),
+                              _ints(dst, i64, n * width, "dst", dev), _ints(status, i32, 1, "status", dev),
+                              _stream_handle(stream, dev))
+    return rc if rc == FM_OK else _check(rc)
+
+
+def fm_paged_move(src, dst, k_cache, v_cache, stream=None):
+    """One layer's rows moved: src, dst int64 [n, max_path] from fm_paged_keep."""
+    dev = torch.cuda.current_device()
+    if src.dim() != 2 or src.shape != dst.shape:
+        raise FMError(FM_ERR_SHAPE, f"src and dst must be [n, max_path] tensors, got {tuple(src.shape)} and {tuple(dst.shape)}")
+    rc = load().fm_paged_move(src.shape[0], src.shape[1], _ints(src, torch.int64, 0, "src", dev),
+                              _ints(dst, torch.int64, 0, "dst", dev), _cache(k_cache, "k_cache", dev),
+                              _cache(v_cache, "v_cache", dev), _stream_handle(stream, dev))
+    return rc if rc == FM_OK else _check(rc)
+
+
 def _on_stream(stream):
     """Context whose current stream is `stream` (None: as it is), so that what it allocates belongs to it."""
     if stream is None:
@@ -699,6 +734,16 @@ def attention_varlen(q, k, v, cu_q, cu_k=None, causal=True, window=0, softmax_sc
     return (o, lse) if with_lse else o
 
 
+def verify_tree(target, tokens, parent, cu_q, u, u_last, draft=None, max_path=16, stream=None):
+    """One-call verification of trees of drafted tokens (fm_tree_verify): returns path int32 [n, max_path], kept and
+    next_token int32 [n]."""
+    with _on_stream(stream):
+        n, make = cu_q.numel() - 1, lambda *shape: torch.empty(shape, dtype=torch.int32, device=target.device)
+        path, kept, next_token = make(n, max_path), make(n), make(n)
+        fm_tree_verify(target, draft, cu_q, tokens, parent, u, u_last, path, kept, next_token)
+    return path, kept, next_token
+
+
 class PagedKVCache:
     """A paged key/value cache of one layer and the bookkeeping of up to max_seqs requests.
 
@@ -707,7 +752,12 @@ class PagedKVCache:
     stays on the device: nothing here waits for the GPU, and status (0: the last extend fitted) is read
     when the caller chooses.  Several layers share one bookkeeping by sharing it: PagedKVCache(...,
     shared=first) keeps pages of its own (heads, head dimension and type as it likes) and uses the first
-    layer's tables, so that its num_pages, page_size and limits have to be the first one's."""
+    layer's tables, so that its num_pages, page_size and limits have to be the first one's.
+
+    New tokens may be drafted trees: after extend, mask = tree(parent) says what each node sees and sets
+    positions by depth, tree_attention(q, mask) takes attention's place, and when verify_tree() has told
+    what is kept, moves = keep(path, kept) cuts the lengths back and each layer's move(moves) puts the
+    kept rows in their places, before the next extend."""
 
     def __init__(self, num_pages, page_size, kv_heads, head_dim, max_seqs, max_pages_per_seq, max_tokens,
                  dtype=torch.bfloat16, device="cuda", shared: "PagedKVCache | None" = None):
@@ -760,3 +810,41 @@ class PagedKVCache:
             fm_attn_paged(q, self.k, self.v, self.cu_q, self.kv_len, self.block_table,
                           seqs_opts(causal, window, softmax_scale), out, lse, ws)
         return out
+
+    def tree(self, parent, words=None, stream=None):
+        """parent int32 [T]: each new token's parent among its request's new tokens, -1 for a root.  Returns the mask int32
+        [T, words] (words: of 32 nodes, by default enough for T nodes in one tree, at most 32); positions become those of
+        the nodes' depths.  A request of more than 32 * words new tokens (a prompt chunk) is causal."""
+        T = parent.numel()
+        words = max(1, min(FM_MAX_NODES, T + 31) // 32) if words is None else words
+        with _on_stream(stream):
+            mask = torch.zeros(T, words, dtype=torch.int32, device=parent.device)  # rows behind the last token stay zero
+            fm_tree_mask(parent, self.cu_q, self.kv_len, mask, self.positions)
+        return mask
+
+    def tree_attention(self, q, mask, out=None, lse=None, softmax_scale=0.0, stream=None):
+        """As attention, of new tokens that see their request's earlier ones as mask says."""
+        T, Hq, D = q.shape
+        with _on_stream(stream):
+            if out is None:
+                out = torch.zeros(T, Hq, D, dtype=q.dtype, device=q.device)
+            ws = torch.empty(fm_attn_seqs_workspace_size(self.kv_len.numel(), T, Hq, self.k.shape[1], D),
+                             dtype=torch.uint8, device=q.device)
+            fm_attn_tree(q, self.k, self.v, self.cu_q, self.kv_len, self.block_table, mask, seqs_opts(softmax_scale=softmax_scale),
+                         out, lse, ws)
+        return out
+
+    def keep(self, path, kept, stream=None):
+        """path int32 [max_seqs, max_path], kept int32 [max_seqs] from verify_tree (kept -1: a row keeps all its new
+        tokens).  Returns the moves that move() makes in each layer; status counts the rows whose path could not be."""
+        if kept.numel() != self.kv_len.numel():
+            raise FMError(FM_ERR_SHAPE, f"kept must have one entry for each of the {self.kv_len.numel()} rows")
+        with _on_stream(stream):
+            moves = torch.empty(2, *path.shape, dtype=torch.int64, device=path.device)
+            fm_paged_keep(self.cu_q, path, kept, self.kv_len, self.kv_len, self.block_table, self.free_pages, self.free_count,
+                          self.free_count, self.page_size, moves[0], moves[1], self.status)
+        return moves
+
+    def move(self, moves, stream=None):
+        """This layer's rows of the tokens kept, put in their places."""
+        fm_paged_move(moves[0], moves[1], self.k, self.v, stream)

@@ -264,6 +264,20 @@ struct PagedExtendArgs {
   int slots_apart = 0;  // the tokens' slots are written by a kernel of their own
 };
 cudaError_t launch_paged_extend(const PagedExtendArgs &a, cudaStream_t st);
+struct PagedKeepArgs {
+  int64_t n, page_size, num_pages, table_stride, table_width, max_path;
+  const int32_t *cu_q, *path, *kept, *kv_len;
+  int32_t *kv_out;
+  const int32_t *table;
+  int32_t *free_pages;
+  const int32_t *free_count;
+  int32_t *free_out;
+  int64_t *src, *dst;
+  int32_t *status;
+};
+cudaError_t launch_paged_keep(const PagedKeepArgs &a, cudaStream_t st);
+cudaError_t launch_paged_move(const View &kc, const View &vc, const int64_t *src, const int64_t *dst, int64_t n, int64_t width,
+                              unsigned int *err, cudaStream_t st);
 cudaError_t launch_paged_write(const View &k, const View &v, const int64_t *slots, const View &kc, const View &vc,
                                unsigned int *err, cudaStream_t st);
 

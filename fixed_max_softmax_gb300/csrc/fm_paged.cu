@@ -16,6 +16,17 @@
 // cluster alone, 11.1 by the two).  The room decides, not the tokens, whose number is on the device: all of it is
 // filled, with -1 behind the last token.  Bound by the latency of a few dependent loads, then by 12 bytes a slot.
 //
+// fm_paged_keep: after a tree of drafted tokens was verified a request keeps `kept` of its q new tokens, those
+// at path[0] < path[1] < ... among them: with base = kv - q
+//   kv_out = base + kept;  pages P(kv_out) .. P(kv) - 1 of its table row pushed on the list of free pages;
+//   move j (where path[j] != j): the row of position base + path[j] to position base + j
+// in one CTA, or a cluster of 8 where there is room for more than 8,192 moves, with prefix sums of all requests
+// in each CTA as above.  Bound by the latency of four dependent loads (lengths, path, table, list).
+//
+// fm_paged_move: the rows of one layer moved.  path[j] >= j, and ascending: the place that move j writes is the
+// source of none that follows.  So a thread that takes one 16-byte piece of a request's rows through all its
+// moves in order needs nothing from another thread, and may read 8 rows before it writes the first of them.
+//
 // fm_paged_write: a copy of rows to their slots, bound by HBM (each row read and written once): 53,013
 // tokens of 8 heads, D = 128, in 72.5 us, 89 % of the copy rate.
 #include <cuda_bf16.h>
@@ -239,6 +250,170 @@ __global__ void __launch_bounds__(256) paged_slots_kernel(const PagedExtendArgs 
              [&](int i, int j) { return a.table[i * a.table_stride + j]; });
 }
 
+// ---------------------------------------------------------------- what is kept of a tree
+__global__ void __launch_bounds__(kExtThreads) paged_keep_kernel(const PagedKeepArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int32_t smem[];
+  const int n = (int)a.n, ps = (int)a.page_size, width = (int)a.max_path;
+  int32_t *kv_s = smem;                 // [n] keys
+  int32_t *base_s = smem + n;           // [n] keys before the new ones
+  int32_t *kept_s = smem + 2 * n;       // [n] tokens kept, -1: all, and nothing moves
+  int32_t *give_pre = smem + 3 * n;     // [n + 1] exclusive prefix sums of the pages given back
+  __shared__ long long warp_sum[kExtWarps], carry_s;
+  __shared__ int bad_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x, nctas = gridDim.x;  // the grid is one cluster
+  if (tid == 0) carry_s = 0, bad_s = 0;
+  const int count = a.free_count[0];
+  __syncthreads();
+  for (int c0 = 0; c0 < n; c0 += kExtThreads) {
+    const int i = c0 + tid;
+    int give = 0;
+    if (i < n) {
+      const int kv = a.kv_len[i], k = a.kept[i];
+      const long long q = (long long)a.cu_q[i + 1] - a.cu_q[i];
+      bool ok = kv >= 0 && q >= 0 && q <= kv && kv <= INT_MAX - ps && pages_of(kv, ps) <= a.table_width && k >= -1 && k <= q &&
+                k <= width;
+      if (ok && k > 0) {  // ascending, inside the new tokens (8 loads under way at a time)
+        const int32_t *path = a.path + (int64_t)i * width;
+        int before = -1;
+        for (int j0 = 0; j0 < k; j0 += 8) {
+          int x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) x[u] = j0 + u < k ? path[j0 + u] : INT_MAX;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            if (j0 + u >= k) break;
+            ok &= x[u] > before && x[u] < q;
+            before = x[u];
+          }
+        }
+      }
+      if (!ok) atomicAdd(&bad_s, 1);
+      const int base = ok ? kv - (int)q : kv, stay = ok ? k : -1;
+      kv_s[i] = kv;
+      base_s[i] = base;
+      kept_s[i] = stay;
+      if (stay >= 0) give = pages_of(kv, ps) - pages_of(base + stay, ps);
+    }
+    long long inc = give;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      long long w = warp_sum[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w += u;
+      }
+      warp_sum[lane] = w;
+    }
+    __syncthreads();
+    const long long carry = carry_s;
+    // (sums past 2^31 are refused below; what is stored for them is never used)
+    if (i < n) give_pre[i] = (int)(carry + (warp > 0 ? warp_sum[warp - 1] : 0) + inc - give);
+    __syncthreads();
+    if (tid == 0) carry_s = carry + warp_sum[kExtWarps - 1];
+    __syncthreads();
+  }
+  const bool ok = count >= 0 && count <= a.num_pages && count + carry_s <= a.num_pages;
+  const int back = ok ? (int)carry_s : 0;
+  if (tid == 0) give_pre[n] = back;
+  // every CTA has read the old lengths and the count
+  cluster_sync();
+  const int g0 = rank * kExtThreads + tid, gstep = nctas * kExtThreads;
+  for (int e = g0; e < back; e += gstep) {
+    const int i = owner(give_pre, n, e);
+    a.free_pages[count + e] = a.table[i * a.table_stride + pages_of(base_s[i] + kept_s[i], ps) + (e - give_pre[i])];
+  }
+  for (int i = g0; i < n; i += gstep) {
+    const int kv = ok && kept_s[i] >= 0 ? base_s[i] + kept_s[i] : kv_s[i];
+    if (kv != kv_s[i] || a.kv_out != a.kv_len) a.kv_out[i] = kv;
+  }
+  if (rank == 0 && tid == 0) {
+    *a.free_out = count + back;
+    *a.status = ok ? bad_s : -1;
+  }
+  const long long moves = (long long)n * width;
+  for (long long e = g0; e < moves; e += gstep) {
+    const int i = (int)(e / width), j = (int)(e - (long long)i * width);
+    long long src = -1, dst = -1;
+    if (ok && j < kept_s[i]) {
+      const int x = a.path[e];
+      if (x != j) {
+        auto slot = [&](int p) -> long long { return (long long)a.table[i * a.table_stride + p / ps] * ps + p % ps; };
+        src = slot(base_s[i] + x);
+        dst = slot(base_s[i] + j);
+      }
+    }
+    a.src[e] = src;
+    a.dst[e] = dst;
+  }
+}
+
+struct MoveArgs {
+  View kc, vc;
+  const int64_t *src, *dst;
+  int64_t n, width;
+  unsigned int *err;
+};
+
+// A piece of VEC elements (16 bytes, or one element where layout or alignment ask for it) of a request's
+// rows of K or V a thread, through all its moves.
+template <typename E, int VEC>
+__global__ void __launch_bounds__(256) paged_move_kernel(const MoveArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  using V = typename std::conditional<sizeof(E) * VEC == 16, uint4, E>::type;
+  constexpr int AHEAD = 8;
+  const unsigned per_head = (unsigned)(a.kc.D / VEC), per_row = per_head * (unsigned)a.kc.H;
+  const unsigned piece = blockIdx.y * 256 + threadIdx.x;
+  if (piece >= 2 * per_row) return;
+  const View &x = piece < per_row ? a.kc : a.vc;
+  const unsigned c = piece < per_row ? piece : piece - per_row, h = c / per_head, d = (c - h * per_head) * VEC;
+  E *at = reinterpret_cast<E *>(const_cast<void *>(x.ptr)) + h * x.sH + (int64_t)d * x.sD;
+  const int64_t ps = x.S, n_slots = x.B * ps;
+  auto where = [&](int64_t slot) -> E * {
+    const int64_t page = slot / ps;
+    return at + page * x.sB + (slot - page * ps) * x.sS;
+  };
+  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+    const int64_t *src = a.src + i * a.width, *dst = a.dst + i * a.width;
+    for (int64_t j0 = 0; j0 < a.width; j0 += AHEAD) {
+      V row[AHEAD];
+      int64_t from[AHEAD], to[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        from[u] = j0 + u < a.width ? src[j0 + u] : -1;
+        to[u] = j0 + u < a.width ? dst[j0 + u] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (from[u] >= n_slots || to[u] >= n_slots) {  // never touched: reported by fm_sync_status
+          if (a.err && atomicCAS(a.err, 0u, (unsigned)kDevErrSlot) == 0u) {
+            const int64_t bad = from[u] >= n_slots ? from[u] : to[u];
+            a.err[1] = (unsigned)(i * a.width + j0 + u);
+            a.err[2] = (unsigned)(bad & 0xffffffffll);
+            a.err[3] = (unsigned)(bad >> 32);
+          }
+          to[u] = -1;
+        }
+        if (from[u] < 0) to[u] = -1;
+        if (to[u] >= 0) row[u] = *reinterpret_cast<const V *>(where(from[u]));
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (to[u] >= 0) *reinterpret_cast<V *>(where(to[u])) = row[u];
+    }
+  }
+}
+
 // ---------------------------------------------------------------- cache writes
 struct WriteArgs {
   View k, v, kc, vc;
@@ -339,6 +514,57 @@ cudaError_t launch_paged_extend(const PagedExtendArgs &args, cudaStream_t st) {
   if (e != cudaSuccess || !a.slots_apart) return e;
   const int64_t want = (a.max_tokens + 1023) / 1024, cap = (int64_t)current_device_sm_count() * 8;
   return launch_pdl(paged_slots_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, a);
+}
+
+cudaError_t launch_paged_keep(const PagedKeepArgs &a, cudaStream_t st) {
+  const size_t smem = (size_t)(4 * a.n + 1) * 4;
+  static std::atomic<bool> attr_set[64] = {};  // as above
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(paged_keep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (4 * kMaxSeqs + 1) * 4);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const unsigned ctas = a.n * a.max_path > 8192 ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kExtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_keep_kernel, a);
+}
+
+cudaError_t launch_paged_move(const View &kc, const View &vc, const int64_t *src, const int64_t *dst, int64_t n, int64_t width,
+                              unsigned int *err, cudaStream_t st) {
+  MoveArgs a;
+  a.kc = kc;
+  a.vc = vc;
+  a.src = src;
+  a.dst = dst;
+  a.n = n;
+  a.width = width;
+  a.err = err;
+  const int64_t es = kc.dtype == FM_F32 ? 4 : 2;
+  const bool vec = rows16(kc, es) && rows16(vc, es);
+  const int64_t pieces = 2 * kc.H * (vec ? kc.D * es / 16 : kc.D);
+  if (n == 0 || width == 0 || pieces == 0) return cudaSuccess;
+  const dim3 grid((unsigned)n, (unsigned)((pieces + 255) / 256));
+  if (es == 4)
+    return vec ? launch_pdl(paged_move_kernel<float, 4>, grid, dim3(256), 0, st, a)
+               : launch_pdl(paged_move_kernel<float, 1>, grid, dim3(256), 0, st, a);
+  return vec ? launch_pdl(paged_move_kernel<uint16_t, 8>, grid, dim3(256), 0, st, a)
+             : launch_pdl(paged_move_kernel<uint16_t, 1>, grid, dim3(256), 0, st, a);
 }
 
 cudaError_t launch_paged_write(const View &k, const View &v, const int64_t *slots, const View &kc, const View &vc,

@@ -104,6 +104,22 @@ int check_mask(const TreeMask &m, int64_t rows) {
   return FM_OK;
 }
 
+// The sizes of a paged cache's state, and the tokens of a call.
+int check_state(const fm_page_state *state, int64_t tokens) {
+  if (!state) return fail(FM_ERR_ARG, "state is NULL");
+  const fm_page_state &s = *state;
+  if (s.n_seqs < 0 || s.num_pages < 0 || s.table_width < 0 || s.table_stride < 0 || tokens < 0)
+    return fail(FM_ERR_ARG, "negative size");
+  if (s.page_size < 1) return fail(FM_ERR_ARG, "page_size = %lld", (long long)s.page_size);
+  if (s.n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)s.n_seqs, kMaxSeqs);
+  if (s.page_size > kMaxRows || s.num_pages > kMaxRows || s.table_width > kMaxRows || tokens > kMaxRows)
+    return fail(FM_ERR_UNSUPPORTED, "page size, pages, table width and tokens of a call are limited to 2^30");
+  if (s.n_seqs > 1 && s.table_stride < s.table_width)
+    return fail(FM_ERR_ARG, "block_table: rows of %lld entries %lld apart", (long long)s.table_width,
+                (long long)s.table_stride);
+  return FM_OK;
+}
+
 // A row of probabilities a token: [1, 1, T, V], adjacent along V.
 int check_probabilities(const fm_tensor *t, const char *what) {
   if (!t) return fail(FM_ERR_ARG, "%s: NULL tensor", what);
@@ -324,17 +340,9 @@ int fm_tree_verify(const fm_tensor *target, const fm_tensor *draft, int64_t n_se
 int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const uint8_t *release, int64_t max_tokens,
                     int32_t *cu_q, int64_t *slots, int32_t *positions, int32_t *status, fm_stream_t stream) {
   clear_error();
-  if (!state) return fail(FM_ERR_ARG, "state is NULL");
+  const int rc = check_state(state, max_tokens);
+  if (rc) return rc;
   const fm_page_state &s = *state;
-  if (s.n_seqs < 0 || s.num_pages < 0 || s.table_width < 0 || s.table_stride < 0 || max_tokens < 0)
-    return fail(FM_ERR_ARG, "negative size");
-  if (s.page_size < 1) return fail(FM_ERR_ARG, "page_size = %lld", (long long)s.page_size);
-  if (s.n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)s.n_seqs, kMaxSeqs);
-  if (s.page_size > kMaxRows || s.num_pages > kMaxRows || s.table_width > kMaxRows || max_tokens > kMaxRows)
-    return fail(FM_ERR_UNSUPPORTED, "page size, pages, table width and tokens of a call are limited to 2^30");
-  if (s.n_seqs > 1 && s.table_stride < s.table_width)
-    return fail(FM_ERR_ARG, "block_table: rows of %lld entries %lld apart", (long long)s.table_width,
-                (long long)s.table_stride);
   if (!cu_q || !status || !s.free_count || !s.free_count_out || (s.num_pages > 0 && !s.free_pages) ||
       (max_tokens > 0 && (!slots || !positions)) ||
       (s.n_seqs > 0 && (!new_len || !s.kv_len || !s.kv_len_out || (s.table_width > 0 && !s.block_table))))
@@ -364,6 +372,64 @@ int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const ui
   a.status = status;
   const cudaError_t e = launch_paged_extend(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_paged_extend launch");
+}
+
+int fm_paged_keep(const fm_page_state *state, const int32_t *cu_q, int64_t max_path, const int32_t *path, const int32_t *kept,
+                  int64_t *src, int64_t *dst, int32_t *status, fm_stream_t stream) {
+  clear_error();
+  if (max_path < 1) return fail(FM_ERR_ARG, "max_path = %lld", (long long)max_path);
+  if (max_path > FM_MAX_NODES) return fail(FM_ERR_UNSUPPORTED, "paths of %lld nodes: at most %d", (long long)max_path, FM_MAX_NODES);
+  const int rc = check_state(state, 0);
+  if (rc) return rc;
+  const fm_page_state &s = *state;
+  if (!status || !s.free_count || !s.free_count_out || (s.num_pages > 0 && !s.free_pages) ||
+      (s.n_seqs > 0 && (!cu_q || !path || !kept || !src || !dst || !s.kv_len || !s.kv_len_out || (s.table_width > 0 && !s.block_table))))
+    return fail(FM_ERR_ARG, "every array of fm_paged_keep must be given");
+  if (misaligned(cu_q, 4) || misaligned(path, 4) || misaligned(kept, 4) || misaligned(src, 8) || misaligned(dst, 8) ||
+      misaligned(status, 4) || misaligned(s.free_count, 4) || misaligned(s.free_count_out, 4) || misaligned(s.free_pages, 4) ||
+      misaligned(s.kv_len, 4) || misaligned(s.kv_len_out, 4) || misaligned(s.block_table, 4))
+    return fail(FM_ERR_ARG, "the arrays of fm_paged_keep must be aligned to their elements");
+  PagedKeepArgs a;
+  a.n = s.n_seqs;
+  a.page_size = s.page_size;
+  a.num_pages = s.num_pages;
+  a.table_stride = s.table_stride;
+  a.table_width = s.table_width;
+  a.max_path = max_path;
+  a.cu_q = cu_q;
+  a.path = path;
+  a.kept = kept;
+  a.kv_len = s.kv_len;
+  a.kv_out = s.kv_len_out;
+  a.table = s.block_table;
+  a.free_pages = s.free_pages;
+  a.free_count = s.free_count;
+  a.free_out = s.free_count_out;
+  a.src = src;
+  a.dst = dst;
+  a.status = status;
+  const cudaError_t e = launch_paged_keep(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_paged_keep launch");
+}
+
+int fm_paged_move(int64_t n_seqs, int64_t max_path, const int64_t *src, const int64_t *dst, const fm_tensor *k_cache,
+                  const fm_tensor *v_cache, fm_stream_t stream) {
+  clear_error();
+  View kc, vc;
+  int rc;
+  if ((rc = seqs_view(k_cache, "k_cache", &kc)) || (rc = seqs_view(v_cache, "v_cache", &vc))) return rc;
+  if (kc.dtype != vc.dtype) return fail(FM_ERR_DTYPE, "the caches must share one dtype");
+  if (kc.B != vc.B || kc.H != vc.H || kc.S != vc.S || kc.D != vc.D) return fail(FM_ERR_SHAPE, "the shapes of the caches differ");
+  if (n_seqs < 0 || max_path < 0) return fail(FM_ERR_ARG, "negative size");
+  if (n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)n_seqs, kMaxSeqs);
+  if (max_path > FM_MAX_NODES) return fail(FM_ERR_UNSUPPORTED, "paths of %lld nodes: at most %d", (long long)max_path, FM_MAX_NODES);
+  if (n_seqs == 0 || max_path == 0 || kc.H == 0) return FM_OK;
+  if (kc.S < 1) return fail(FM_ERR_SHAPE, "the cache's page size (its S) must be at least 1");
+  if (!src || !dst || misaligned(src, 8) || misaligned(dst, 8)) return fail(FM_ERR_ARG, "src and dst must be given, 8-byte aligned");
+  unsigned int *err = dev_error_ptr();
+  if (!err) return fail(FM_ERR_CUDA, "no CUDA device");
+  const cudaError_t e = launch_paged_move(kc, vc, src, dst, n_seqs, max_path, err, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_paged_move launch");
 }
 
 int fm_paged_write(const fm_tensor *k, const fm_tensor *v, const int64_t *slots, const fm_tensor *k_cache,

@@ -615,6 +615,30 @@ FM_API int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, c
 FM_API int fm_paged_write(const fm_tensor *k, const fm_tensor *v, const int64_t *slots, const fm_tensor *k_cache,
                           const fm_tensor *v_cache, fm_stream_t stream);
 
+/* fm_paged_keep -- the bookkeeping after fm_tree_verify: of each request's new tokens (the nodes of a tree, whose
+ * keys and values are in the cache) only the path that was kept stays, as if it alone had been appended.
+ *   state     kv_len: keys with the new tokens counted; kv_len_out: kv_len - (new tokens) + kept.  Pages that hold
+ *             none of them go to the end of the list of free pages, in request and table order (their
+ *             entries stay in the table, behind the request's last key)
+ *   cu_q      int32 [n+1]: request i has cu_q[i+1] - cu_q[i] new tokens
+ *   path      int32 [n, max_path], kept int32 [n]: the first kept[i] entries of path[i], ascending, are the new
+ *             tokens that stay; 0: none does; -1: all do (a prompt chunk in the same call)
+ *   src, dst  int64 [n, max_path] written: the slots that fm_paged_move reads and writes, -1 where nothing moves
+ *   status    int32 [1] written: 0, or the number of requests whose kept or path cannot be (they keep all they
+ *             have), or -1: free_count and the pages given back do not fit the list, and the call changes nothing
+ * Errors: FM_ERR_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+FM_API int fm_paged_keep(const fm_page_state *state, const int32_t *cu_q, int64_t max_path, const int32_t *path,
+                         const int32_t *kept, int64_t *src, int64_t *dst, int32_t *status, fm_stream_t stream);
+
+/* fm_paged_move -- one layer's rows of the tokens kept moved to their places, after fm_paged_keep and before the
+ * next fm_paged_extend (the pages given back still hold rows).  src, dst int64 [n, max_path] from fm_paged_keep:
+ * moves of one row are made in order, none reading what an earlier one wrote; rows do not share slots.  Negative
+ * slots are skipped, ones past the cache too, and reported by fm_sync_status (FM_ERR_INDEX).
+ *   k_cache, v_cache  [num_pages, H, page_size, D], any strides
+ * Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+FM_API int fm_paged_move(int64_t n_seqs, int64_t max_path, const int64_t *src, const int64_t *dst, const fm_tensor *k_cache,
+                         const fm_tensor *v_cache, fm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

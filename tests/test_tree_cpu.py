@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fixed_max_softmax_gb300 as fm
-from tests.test_seqs_cpu import FAKE, ROOT, lib, view  # noqa: F401
+from tests.test_seqs_cpu import FAKE, ROOT, lib, state, view  # noqa: F401
 
 
 def tree(lib, q=None, k=None, o=None, opt=None, seqs=None, mask=FAKE, words=2, stride=2, nbytes=1 << 40):  # noqa: F811
@@ -142,3 +142,58 @@ def test_the_definition_is_lossless():
 
         go(F(1), F(0), F(1), children)
         assert got == p, children
+
+
+# ---------------------------------------------------------------- what is kept
+def keep(lib, st, width=4, cu=FAKE, path=FAKE, kept=FAKE, src=FAKE, dst=FAKE, status=FAKE):  # noqa: F811
+    return lib.fm_paged_keep(ctypes.byref(st), cu, width, path, kept, src, dst, status, None)
+
+
+def test_keep_refusals(lib):  # noqa: F811
+    assert lib.fm_paged_keep(None, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, None) == fm.FM_ERR_ARG
+    for kw in (dict(n_seqs=-1), dict(page_size=0), dict(num_pages=-1), dict(table_width=-1), dict(table_stride=7), dict(free_pages=None),
+               dict(free_count=None), dict(free_count_out=None), dict(kv_len=None), dict(kv_len_out=None), dict(block_table=None),
+               dict(kv_len=FAKE + 2)):
+        assert keep(lib, state(**kw)) == fm.FM_ERR_ARG, kw
+    assert keep(lib, state(n_seqs=fm.FM_MAX_SEQS + 1)) == fm.FM_ERR_UNSUPPORTED
+    assert keep(lib, state(), width=fm.FM_MAX_NODES + 1) == fm.FM_ERR_UNSUPPORTED
+    for kw in (dict(width=0), dict(cu=None), dict(path=None), dict(kept=None), dict(src=None), dict(dst=None), dict(status=None),
+               dict(src=FAKE + 4), dict(dst=FAKE + 4), dict(cu=FAKE + 1), dict(path=FAKE + 2), dict(kept=FAKE + 3), dict(status=FAKE + 1)):
+        assert keep(lib, state(), **kw) == fm.FM_ERR_ARG, kw
+
+
+def test_move_refusals(lib):  # noqa: F811
+    def move(kc=None, vc=None, n=3, width=4, src=FAKE, dst=FAKE):
+        kc = kc or view(9, 2, 16, 128)
+        return lib.fm_paged_move(n, width, src, dst, ctypes.byref(kc), ctypes.byref(vc or kc), None)
+    assert move(vc=view(9, 2, 32, 128)) == fm.FM_ERR_SHAPE
+    assert move(vc=view(9, 2, 16, 128, fm.FM_F16)) == fm.FM_ERR_DTYPE
+    assert move(kc=view(9, 2, 16, 96)) == fm.FM_ERR_UNSUPPORTED
+    assert move(kc=view(9, 2, 0, 128)) == fm.FM_ERR_SHAPE
+    assert move(n=-1) == fm.FM_ERR_ARG and move(width=-1) == fm.FM_ERR_ARG
+    assert move(n=fm.FM_MAX_SEQS + 1) == fm.FM_ERR_UNSUPPORTED and move(width=fm.FM_MAX_NODES + 1) == fm.FM_ERR_UNSUPPORTED
+    for bad in (None, FAKE + 4):
+        assert move(src=bad) == fm.FM_ERR_ARG and move(dst=bad) == fm.FM_ERR_ARG
+    assert move(n=0, src=None) == fm.FM_OK and move(width=0, src=None) == fm.FM_OK  # nothing to do
+
+
+def test_keep_and_move_binding_refusals(lib, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # (where get_device() says that host tensors are)
+    i, w = (lambda *s: torch.zeros(s, dtype=torch.int32)), (lambda *s: torch.zeros(s, dtype=torch.int64))
+    good = [i(3), i(2, 5), i(2), i(2), i(2), i(2, 4), i(8), i(1), i(1), 16, w(2, 5), w(2, 5), i(1)]
+    for at, bad in ((0, i(2)), (1, i(10)), (1, i(1, 5)), (1, i(5, 2).t()), (1, w(2, 5)), (2, i(4)[::2]), (3, i(1)), (4, w(2)), (5, i(8)),
+                    (6, w(8)), (7, i(0)), (8, i(0)), (10, i(2, 5)), (11, w(9)), (12, i(0))):
+        with pytest.raises(fm.FMError):
+            fm.fm_paged_keep(*good[:at], bad, *good[at + 1:], stream=0)
+    cache = torch.zeros(3, 2, 16, 128)
+    for src, dst in ((w(2, 5), w(2, 4)), (w(10), w(10)), (i(2, 5), w(2, 5)), (w(5, 2).t(), w(2, 5))):
+        with pytest.raises(fm.FMError):
+            fm.fm_paged_move(src, dst, cache, cache, stream=0)
+    c = fm.PagedKVCache(6, 4, 2, 64, 3, 5, 7, device="cpu")
+    with pytest.raises(fm.FMError, match="each of the 3 rows"):
+        c.keep(i(2, 4), i(2))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(fm.FMError, match="CUDA device"):
+        fm.fm_paged_keep(*good)
+    with pytest.raises(fm.FMError, match="CUDA device"):
+        fm.fm_paged_move(w(2, 5), w(2, 5), cache, cache)
