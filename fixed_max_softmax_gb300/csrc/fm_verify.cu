@@ -12,12 +12,16 @@
 // x with sum_{y <= x} R(y) > u_last sum_y R(y).
 //
 // A cluster of up to 8 CTAs a request.  Its first CTA gathers the nodes' parents, tokens, numbers and
-// the p and q that their tests compare into every CTA's shared memory; from there all CTAs
-// walk alike, and meet only to sum what is left over the vocabulary, once a refused child and
-// once at the end: each sums an even part of the row, and the parts' sums go to every CTA's shared
-// memory.  A walk without a refusal reads one row of the vocabulary in all.
-// Sums are 64-bit, as are the tests: they are compared with a random number, and a sum that is off by
-// 2^-24 would pick another token than the definition does at every border that the number falls next to.
+// the p and q that their tests compare into every CTA's shared memory; from there the first warp of each
+// CTA walks, all alike, and the CTAs meet only to sum what is left over the vocabulary, once a
+// refused child and once at the end: each sums an even part of the row, and the parts' sums go to every
+// CTA's shared memory.  A walk without a refusal reads one row of the vocabulary in all.
+// Sums and tests are compared with random numbers, and a sum that is off by 2^-24 would pick another token
+// than the definition does at every border that the number falls next to.  The tests are made in 64 bits, by
+// that one warp: an SM adds two 64-bit numbers a clock, so that a row's elements, and what every warp
+// would do again, are not (64 chains over 128,000 tokens: 152 us with 64-bit sums, 98 with the walk's
+// tests still made by all 16 warps).  A thread sums pairs of fp32 numbers, value and error, in some dozen
+// fp32 operations an element, good to about 2^-45; the warps' sums are joined in 64 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -61,14 +65,24 @@ __device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
 // A probability: what is negative, infinite or no number counts as 0.
 __device__ __forceinline__ float some(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
 
+// x + e, e the error of x: a pair of fp32 numbers holds what a sum in fp32 would lose.
+struct Pair {
+  float x, e;
+};
+
 struct Shared {
   int parent[FM_MAX_NODES], token[FM_MAX_NODES];  // token -1: outside the vocabulary
   float u[FM_MAX_NODES], p[FM_MAX_NODES], q[FM_MAX_NODES];
   int first, nodes;             // as the first CTA read them
   int refused[FM_MAX_NODES];    // tokens taken out of p (children that were chosen)
   double cta[2][kMostCtas];     // the CTAs' sums, of alternate passes
-  double warp[kWarps];          // this CTA's warps' sums
+  Pair warp[kWarps];            // this CTA's warps' sums
+  // what the first warp has the others do: sum the row after node `cur` (A, n_refused tokens taken out),
+  // or look for the border in the blocks [part0, part1) of it, or nothing more
+  int what, cur, n_refused, part0, part1;
+  Pair A;
 };
+enum : int { kSum, kFind, kDone };
 
 // A row of one model in blocks of 16 bytes, block 0 beginning at the boundary before the row's start:
 // element `e` of block b is element b * VEC - shift + e of the row.
@@ -76,31 +90,59 @@ template <typename E>
 struct Row {
   static constexpr int VEC = 16 / (int)sizeof(E);
   const E *at;  // of block 0
-  int64_t shift, V;
+  int shift, V;
 
-  __device__ __forceinline__ Row(const void *base, int64_t stride, int64_t row, int64_t V_) : V(V_) {
+  __device__ __forceinline__ Row(const void *base, int64_t stride, int64_t row, int V_) : V(V_) {
     const E *p = reinterpret_cast<const E *>(base) + row * stride;
-    shift = (int64_t)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(E));
+    shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(E));
     at = p - shift;
   }
-  __device__ __forceinline__ int64_t blocks() const { return (V + shift + VEC - 1) / VEC; }
-  // block b as another row of alignment `s` has it
-  __device__ __forceinline__ void load(int64_t b, int64_t s, float (&x)[VEC]) const {
-    const int64_t i = b * VEC - s;  // in the row
-    if (s == shift && i >= 0 && i + VEC <= V) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(at + b * VEC);
-      const E *e = reinterpret_cast<const E *>(&w);
+  __device__ __forceinline__ int blocks() const { return (V + shift + VEC - 1) / VEC; }
+  // block b as a row of alignment `s` has it
+  __device__ __forceinline__ uint4 load(int b, int s) const {
+    const int i = b * VEC - s;  // in the row
+    if (s == shift && i >= 0 && i + VEC <= V) return *reinterpret_cast<const uint4 *>(at + i + shift);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    E *e = reinterpret_cast<E *>(&w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) x[j] = some(as_f32(e[j]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) x[j] = i + j >= 0 && i + j < V ? some(as_f32(at[shift + i + j])) : 0.f;
-    }
+    for (int j = 0; j < VEC; ++j)
+      if (i + j >= 0 && i + j < V) e[j] = at[shift + i + j];
+    return w;
   }
 };
 
+// The pair a + b: s = a + b rounded, and exactly what that lost (Knuth's two-sum).
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fadd_rn(s, -a);
+  return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb))};
+}
+__device__ __forceinline__ void add(Pair &sum, Pair v) {
+  const Pair s = two_sum(sum.x, v.x);
+  sum.x = s.x;
+  sum.e = __fadd_rn(sum.e, __fadd_rn(s.e, v.e));
+}
+__device__ __forceinline__ Pair over_warp(Pair v) {  // the warp's sum, in every lane
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) add(v, {__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.e, d)});
+  return v;
+}
+__device__ __forceinline__ double value(Pair v) { return (double)v.x + (double)v.e; }
+__device__ __forceinline__ void add(Pair &sum, float v) {
+  const Pair s = two_sum(sum.x, v);
+  sum.x = s.x;
+  sum.e = __fadd_rn(sum.e, s.e);
+}
+// max(p - A q, 0), A a pair; the product's rounding is what an FMA gives back.
+__device__ __forceinline__ Pair residual(float p, float q, Pair A) {
+  const float m = __fmul_rn(q, A.x), lost = __fmaf_rn(q, A.e, __fmaf_rn(q, A.x, -m));
+  Pair d = two_sum(p, -m);
+  d.e = __fadd_rn(d.e, -lost);
+  if (!(__fadd_rn(d.x, d.e) > 0.f)) d.x = d.e = 0.f;
+  return d;
+}
+
 template <typename E, bool DRAFT>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const TreeVerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVerifyArgs a) {
   constexpr int VEC = Row<E>::VEC;
   extern __shared__ __align__(16) uint8_t raw[];
   Shared &s = *reinterpret_cast<Shared *>(raw);
@@ -159,188 +201,266 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const TreeVerifyA
     }
     return;
   }
-  int cur = 0, kept = 1, n_refused = 0, passes = 0;
-  double A = 0.0, S = 1.0;
-  bool summed = false;  // S and the warps' sums are those of (cur, A)
-  if (rank == 0 && tid == 0) path[0] = 0;
-
-  // this warp's blocks of the row
-  int64_t w0 = 0, w1 = 0;
-  // What is left of block b of the row, given A and the refused tokens.
-  auto left = [&](const Row<E> &p, const Row<E> &q, int64_t b, double (&x)[VEC]) {
-    float f[VEC];
-    p.load(b, p.shift, f);
+  // What is left of the elements of block b of the row after node cur.
+  auto left = [&](uint4 pw, uint4 qw, Pair A, int n_refused, int b, int shift, Pair (&x)[VEC]) {
+    const E *pe = reinterpret_cast<const E *>(&pw), *qe = reinterpret_cast<const E *>(&qw);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) x[j] = (double)f[j];
-    if (DRAFT && A > 0.0) {
-      q.load(b, p.shift, f);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) x[j] = fmax(x[j] - A * (double)f[j], 0.0);
+    for (int j = 0; j < VEC; ++j) {
+      x[j] = {some(as_f32(pe[j])), 0.f};
+      if (DRAFT && A.x > 0.f) x[j] = residual(x[j].x, some(as_f32(qe[j])), A);
     }
-    for (int i = 0; i < n_refused; ++i) {
-      const int64_t at = (int64_t)s.refused[i] + p.shift - b * VEC;
-      if (at >= 0 && at < VEC) {
+    if (!DRAFT) {
+#pragma unroll 1
+      for (int i = 0; i < n_refused; ++i) {
+        const int at = s.refused[i] + shift - b * VEC;
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-          if (j == at) x[j] = 0.0;
+          if (j == at) x[j].x = 0.f;
       }
     }
   };
-  // S = sum of what is left of row cur; every thread of the cluster.
-  auto sum_up = [&]() {
-    const Row<E> p(a.p, a.sp, first + cur, a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, first + cur, a.V);
-    const int64_t nb = p.blocks(), parts = (int64_t)ctas * kWarps, mine = (int64_t)rank * kWarps + warp;
-    w0 = nb * mine / parts;
-    w1 = nb * (mine + 1) / parts;
-    double sum = 0.0;
-    for (int64_t b = w0 + lane; b < w1; b += 32) {
-      double x[VEC];
-      left(p, q, b, x);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) sum += x[j];
+  // The warp's sum of what is left of the blocks [w0, w1).
+  auto sum_blocks = [&](const Row<E> &p, const Row<E> &q, Pair A, int n_refused, int w0, int w1) -> Pair {
+    constexpr int U = DRAFT ? 2 : 4;  // blocks under way at a time
+    if (!DRAFT) {
+      bool here = false;  // a refused token lies in them
+      for (int i = lane; i < n_refused; i += 32) {
+        const int at = (s.refused[i] + p.shift) / VEC;
+        here |= at >= w0 && at < w1;
+      }
+      if (!__any_sync(0xffffffffu, here)) n_refused = 0;
     }
+    Pair sum = {0.f, 0.f};
+    for (int b0 = w0 + lane; b0 < w1; b0 += 32 * U) {
+      uint4 pw[U], qw[U];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) s.warp[warp] = sum;
-    __syncthreads();
-    double *slot = s.cta[passes & 1];
-    if (tid < (int)ctas) {
-      double x = 0.0;
-      for (int w = 0; w < kWarps; ++w) x += s.warp[w];
-      put_remote(in_cta(smem_at(slot + rank), tid), x);
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + 32 * u;
+        pw[u] = qw[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (b < w1) {
+          pw[u] = p.load(b, p.shift);
+          if (DRAFT && A.x > 0.f) qw[u] = q.load(b, p.shift);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Pair x[VEC];
+        left(pw[u], qw[u], A, n_refused, b0 + 32 * u, p.shift, x);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (DRAFT) add(sum, x[j]);
+          else add(sum, x[j].x);
+        }
+      }
     }
-    cluster_arrive();
-    cluster_wait();
-    S = 0.0;
-    for (uint32_t c = 0; c < ctas; ++c) S += slot[c];
-    ++passes;
+    return over_warp(sum);
   };
+  // Part `i` of `n` even ones of the blocks [b0, b1).
+  auto part = [](int b0, int b1, int i, int n) -> int { return b0 + (int)((int64_t)(b1 - b0) * i / n); };
 
-  int t = 0;
-  while (kept < a.max_path) {
-    // the next child of cur behind node t
-    int child = -1;
-    for (int b = (t + 1) & ~31; b < nodes; b += 32) {
-      const int i = b + lane;
-      const unsigned m = __ballot_sync(0xffffffffu, i > t && i < nodes && s.parent[i] == cur && s.token[i] >= 0);
-      if (m) {
-        child = b + __ffs(m) - 1;
+  // The first warp's walk.
+  int cur = 0, kept = 1, n_refused = 0, passes = 0, t = 0, part0 = 0, part1 = 0;
+  double A = 0.0, S = 1.0, border = 0.0, before = 0.0;
+  bool summed = false;  // S and the warps' sums are those of (cur, A)
+  bool ended = false;   // no child is left to try
+  if (rank == 0 && tid == 0) path[0] = 0;
+
+  // Goes on with the walk until a sum is wanted; the next order to the CTA's warps.
+  auto walk = [&]() -> int {
+    while (!ended) {
+      int child = -1;  // the next child of cur behind node t
+      if (kept < a.max_path)
+        for (int b = (t + 1) & ~31; b < nodes; b += 32) {
+          const int i = b + lane;
+          const unsigned m = __ballot_sync(0xffffffffu, i > t && i < nodes && s.parent[i] == cur && s.token[i] >= 0);
+          if (m) {
+            child = b + __ffs(m) - 1;
+            break;
+          }
+        }
+      if (child < 0) {
+        ended = true;
         break;
       }
+      t = child;
+      const double u = (double)fminf(fmaxf(s.u[t], 0.f), 1.f), p = (double)s.p[t];
+      const int token = s.token[t];
+      bool take;
+      double rest = p;
+      if (DRAFT) {
+        const double q = (double)s.q[t];
+        take = u * q * S < fmax(p - A * q, 0.0);
+      } else {
+        bool gone = false;
+        for (int i = lane; i < n_refused; i += 32) gone |= s.refused[i] == token;
+        if (__any_sync(0xffffffffu, gone)) rest = 0.0;
+        take = u * S < rest;
+      }
+      if (take) {
+        if (rank == 0 && lane == 0) path[kept] = t;
+        cur = t;
+        ++kept;
+        A = 0.0;
+        S = 1.0;
+        n_refused = 0;
+        summed = false;
+      } else if (DRAFT) {
+        A += S;
+        return kSum;
+      } else {
+        S = fmax(S - rest, 0.0);
+        if (lane == 0) s.refused[n_refused] = token;
+        ++n_refused;
+        __syncwarp();
+      }
     }
-    if (child < 0) break;
-    t = child;
-    const double u = (double)fminf(fmaxf(s.u[t], 0.f), 1.f), p = (double)s.p[t], q = (double)s.q[t];
-    const int token = s.token[t];
-    bool take;
-    double rest = 0.0;
-    if (DRAFT) {
-      take = u * q * S < fmax(p - A * q, 0.0);
-    } else {
-      rest = p;
-      for (int i = 0; i < n_refused; ++i)
-        if (s.refused[i] == token) rest = 0.0;
-      take = u * S < rest;
-    }
-    if (take) {
-      if (rank == 0 && tid == 0) path[kept] = t;
-      cur = t;
-      ++kept;
+    return summed ? kFind : kSum;
+  };
+  // After a sum: its value; false if the row is to be summed again.
+  auto after_sum = [&]() {
+    const double *slot = s.cta[(passes - 1) & 1];
+    S = 0.0;
+    for (uint32_t c = 0; c < ctas; ++c) S += slot[c];
+    summed = S > 0.0;
+    if (!summed && (!ended || n_refused > 0)) {  // nothing is left: the target's row as it was
       A = 0.0;
       S = 1.0;
       n_refused = 0;
-      summed = false;
-      __syncthreads();  // (the refused tokens have been read)
-    } else if (DRAFT) {
-      A += S;
-      sum_up();
-      summed = S > 0.0;
-      if (!summed) A = 0.0, S = 1.0;  // nothing is left: the target's row as it was
-    } else {
-      S = fmax(S - rest, 0.0);
-      __syncthreads();
-      if (tid == 0) s.refused[n_refused] = token;
-      ++n_refused;
-      __syncthreads();
+    } else if (!summed) {  // the row itself is empty
+      S = 0.0;
     }
-  }
-  if (!summed) {
-    sum_up();
-    if (!(S > 0.0) && n_refused > 0) {
-      __syncthreads();
-      n_refused = 0;
-      sum_up();
+  };
+  // The lane (of the first `n`) whose value takes the sum past the border, else the last with one above 0; `before`
+  // becomes the sum of the lanes before it.  -1: every value is 0.
+  auto past_border = [&](double v, int n) -> int {
+    double inc = lane < n ? v : 0.0;
+    const unsigned any = __ballot_sync(0xffffffffu, inc > 0.0);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {  // (n is at most 16)
+      const double y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
     }
+    const unsigned past = __ballot_sync(0xffffffffu, ((any >> lane) & 1u) && before + inc > border);
+    if (!any) return -1;
+    const int at = past ? __ffs(past) - 1 : 31 - __clz(any);
+    const double upto = __shfl_sync(0xffffffffu, inc, max(at - 1, 0));
+    if (at > 0) before += upto;
+    return at;
+  };
+
+  for (;;) {
+    if (warp == 0) {
+      int what = passes == 0 || !ended ? walk() : (summed ? kFind : kSum);
+      if (ended && passes > 0 && !(S > 0.0)) what = kDone;
+      if (what == kFind) {
+        // the CTA, then the warp, whose part holds the border
+        const float ul = a.u_last[req];
+        border = (double)fminf(fmaxf(ul, 0.f), 1.f) * S;
+        before = 0.0;
+        const double *slot = s.cta[(passes - 1) & 1];
+        if (past_border(lane < (int)ctas ? slot[lane] : 0.0, (int)ctas) != (int)rank) {
+          what = kDone;
+        } else {
+          const int w = max(past_border(lane < kWarps ? value(s.warp[lane]) : 0.0, kWarps), 0);
+          const Row<E> p(a.p, a.sp, first + cur, (int)a.V);
+          part0 = part(0, p.blocks(), (int)rank * kWarps + w, (int)ctas * kWarps);
+          part1 = part(0, p.blocks(), (int)rank * kWarps + w + 1, (int)ctas * kWarps);
+        }
+      }
+      if (lane == 0) {
+        s.what = what;
+        s.cur = cur;
+        s.n_refused = n_refused;
+        s.part0 = part0;
+        s.part1 = part1;
+        s.A.x = (float)A;
+        s.A.e = (float)(A - (double)(float)A);
+      }
+    }
+    __syncthreads();
+    const int what = s.what;
+    if (what == kDone) break;
+    const int row = first + s.cur, refused = s.n_refused;
+    const Pair A2 = s.A;
+    const Row<E> p(a.p, a.sp, row, (int)a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, row, (int)a.V);
+    const int b0 = what == kSum ? 0 : s.part0, b1 = what == kSum ? p.blocks() : s.part1;
+    const int i = what == kSum ? (int)rank * kWarps + warp : warp, n = what == kSum ? (int)ctas * kWarps : kWarps;
+    const Pair sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, n), part(b0, b1, i + 1, n));
+    if (lane == 0) s.warp[warp] = sum;
+    __syncthreads();
+    if (what == kSum) {
+      if (warp == 0) {
+        double x = lane < kWarps ? value(s.warp[lane]) : 0.0;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (lane < (int)ctas) put_remote(in_cta(smem_at(&s.cta[passes & 1][rank]), lane), x);
+      }
+      cluster_arrive();
+      cluster_wait();
+      if (warp == 0) {
+        ++passes;
+        after_sum();
+      }
+      continue;
+    }
+    // The border lies in a sixteenth of the part: the first warp takes it block by block.
+    if (warp == 0) {
+      const int w = max(past_border(lane < kWarps ? value(s.warp[lane]) : 0.0, kWarps), 0);
+      const int w0 = part(b0, b1, w, kWarps), w1 = part(b0, b1, w + 1, kWarps);
+      int last = -1;  // the last token so far of which anything is left
+      for (int c0 = w0; c0 < w1; c0 += 32) {
+        const int b = c0 + lane;
+        uint4 pw = make_uint4(0u, 0u, 0u, 0u), qw = pw;
+        if (b < w1) {
+          pw = p.load(b, p.shift);
+          if (DRAFT && A2.x > 0.f) qw = q.load(b, p.shift);
+        }
+        Pair x[VEC], sum = {0.f, 0.f};
+        left(pw, qw, A2, refused, b, p.shift, x);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) add(sum, x[j]);
+        const double mine = value(sum);
+        double inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, inc, d);
+          if (lane >= d) inc += y;
+        }
+        const unsigned any = __ballot_sync(0xffffffffu, mine > 0.0);
+        const unsigned past = __ballot_sync(0xffffffffu, mine > 0.0 && before + inc > border);
+        if (any) {
+          const int from = past ? __ffs(past) - 1 : 31 - __clz(any);
+          // in that lane: the first token past the border, else the last with anything left
+          double run = __shfl_up_sync(0xffffffffu, inc, 1);
+          run = before + (lane > 0 ? run : 0.0);
+          int pick = -1;
+          if (lane == from) {
+            bool done = false;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              run += value(x[j]);
+              if (value(x[j]) > 0.0 && !done) {
+                pick = b * VEC - p.shift + j;
+                done = run > border;
+              }
+            }
+          }
+          last = __shfl_sync(0xffffffffu, pick, from);
+          if (past) break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) a.next[req] = last;
+    }
+    break;
   }
-  if (rank == 0) {
-    for (int64_t j = kept + tid; j < a.max_path; j += kThreads) path[j] = -1;
-    if (tid == 0) {
+  if (rank == 0 && warp == 0) {
+    for (int j = kept + lane; j < a.max_path; j += 32) path[j] = -1;
+    if (lane == 0) {
       a.kept[req] = kept;
       if (!(S > 0.0)) a.next[req] = -1;
     }
   }
-  if (!(S > 0.0)) return;
-  // the CTA, then the warp, whose part holds the border
-  const float ul = a.u_last[req];
-  const double border = (double)fminf(fmaxf(ul, 0.f), 1.f) * S;
-  const double *slot = s.cta[(passes - 1) & 1];
-  double upto = 0.0, before = 0.0;
-  int owner = -1;
-  bool found = false;
-  for (int c = 0; c < (int)ctas && !found; ++c) {
-    if (slot[c] > 0.0) owner = c, before = upto;
-    upto += slot[c];
-    found = upto > border;
-  }
-  if ((int)rank != owner) return;
-  upto = before;
-  found = false;
-  owner = -1;
-  for (int w = 0; w < kWarps && !found; ++w) {
-    if (s.warp[w] > 0.0) owner = w, before = upto;
-    upto += s.warp[w];
-    found = upto > border;
-  }
-  if (warp != owner) return;
-  const Row<E> p(a.p, a.sp, first + cur, a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, first + cur, a.V);
-  int64_t last = -1;  // the last token so far of which anything is left
-  for (int64_t b0 = w0; b0 < w1; b0 += 32) {
-    const int64_t b = b0 + lane;
-    double x[VEC], sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) x[j] = 0.0;
-    if (b < w1) left(p, q, b, x);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sum += x[j];
-    double inc = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += y;
-    }
-    const unsigned any = __ballot_sync(0xffffffffu, sum > 0.0);
-    const unsigned past = __ballot_sync(0xffffffffu, sum > 0.0 && before + inc > border);
-    if (any) {
-      const int from = past ? __ffs(past) - 1 : 31 - __clz(any);
-      // in that lane: the first token past the border, else the last with anything left
-      double run = __shfl_up_sync(0xffffffffu, inc, 1);
-      run = before + (lane > 0 ? run : 0.0);
-      int64_t pick = -1;
-      bool done = false;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        run += x[j];
-        if (x[j] > 0.0 && !done) {
-          pick = b * VEC - p.shift + j;
-          done = run > border;
-        }
-      }
-      last = __shfl_sync(0xffffffffu, pick, from);
-      if (past) break;
-    }
-    before += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  if (lane == 0) a.next[req] = (int32_t)last;
 }
 
 template <typename E, bool DRAFT>
