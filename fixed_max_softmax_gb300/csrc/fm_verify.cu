@@ -17,11 +17,11 @@
 // refused child and once at the end: each sums an even part of the row, and the parts' sums go to every
 // CTA's shared memory.  A walk without a refusal reads one row of the vocabulary in all.
 // Sums and tests are compared with random numbers, and a sum that is off by 2^-24 would pick another token
-// than the definition does at every border that the number falls next to.  The tests are made in 64 bits, by
-// that one warp: an SM adds two 64-bit numbers a clock, so that a row's elements, and what every warp
-// would do again, are not (64 chains over 128,000 tokens: 152 us with 64-bit sums, 98 with the walk's
-// tests still made by all 16 warps).  A thread sums pairs of fp32 numbers, value and error, in some dozen
-// fp32 operations an element, good to about 2^-45; the warps' sums are joined in 64 bits.
+// than the definition does at every border that the number falls next to.  All of it is done in pairs of fp32
+// numbers, a value and its error, good to about 2^-45: an SM adds two 64-bit numbers a clock, and one takes
+// some hundred clocks, a pair's addition a dozen fp32 operations (64 chains over 128,000 tokens: 152 us with
+// 64-bit sums, 98 with pairs for the elements and 64 bits in every warp's tests, 29 with 64 bits in one warp of a
+// CTA, LATER without).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -55,9 +55,6 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {  // t
 __device__ __forceinline__ void put_remote(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void put_remote(uint32_t addr, double v) {
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
-}
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -75,7 +72,7 @@ struct Shared {
   float u[FM_MAX_NODES], p[FM_MAX_NODES], q[FM_MAX_NODES];
   int first, nodes;             // as the first CTA read them
   int refused[FM_MAX_NODES];    // tokens taken out of p (children that were chosen)
-  double cta[2][kMostCtas];     // the CTAs' sums, of alternate passes
+  Pair cta[2][kMostCtas];       // the CTAs' sums, of alternate passes
   Pair warp[kWarps];            // this CTA's warps' sums
   // what the first warp has the others do: sum the row after node `cur` (A, n_refused tokens taken out),
   // or look for the border in the blocks [part0, part1) of it, or nothing more
@@ -121,12 +118,33 @@ __device__ __forceinline__ void add(Pair &sum, Pair v) {
   sum.x = s.x;
   sum.e = __fadd_rn(sum.e, __fadd_rn(s.e, v.e));
 }
+__device__ __forceinline__ bool positive(Pair v) { return __fadd_rn(v.x, v.e) > 0.f; }
+__device__ __forceinline__ bool less(Pair a, Pair b) {
+  Pair d = two_sum(b.x, -a.x);
+  d.e = __fadd_rn(d.e, __fadd_rn(b.e, -a.e));
+  return positive(d);
+}
+__device__ __forceinline__ Pair times(Pair a, float b) {
+  const float m = __fmul_rn(a.x, b);
+  return {m, __fmaf_rn(a.e, b, __fmaf_rn(a.x, b, -m))};
+}
+__device__ __forceinline__ Pair shuffle(Pair v, int lane) {
+  return {__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.e, lane)};
+}
+__device__ __forceinline__ Pair scan(Pair v, int lanes) {  // inclusive, over the first `lanes` lanes (a power of two)
+  const int lane = threadIdx.x & 31;
+  for (int d = 1; d < lanes; d <<= 1) {
+    const Pair y = {__shfl_up_sync(0xffffffffu, v.x, d), __shfl_up_sync(0xffffffffu, v.e, d)};
+    if (lane >= d) add(v, y);
+  }
+  return v;
+}
 __device__ __forceinline__ Pair over_warp(Pair v) {  // the warp's sum, in every lane
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) add(v, {__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.e, d)});
-  return v;
+  // (the lanes' additions differ in their order, and so may the last bits)
+  return {__shfl_sync(0xffffffffu, v.x, 0), __shfl_sync(0xffffffffu, v.e, 0)};
 }
-__device__ __forceinline__ double value(Pair v) { return (double)v.x + (double)v.e; }
 __device__ __forceinline__ void add(Pair &sum, float v) {
   const Pair s = two_sum(sum.x, v);
   sum.x = s.x;
@@ -137,7 +155,7 @@ __device__ __forceinline__ Pair residual(float p, float q, Pair A) {
   const float m = __fmul_rn(q, A.x), lost = __fmaf_rn(q, A.e, __fmaf_rn(q, A.x, -m));
   Pair d = two_sum(p, -m);
   d.e = __fadd_rn(d.e, -lost);
-  if (!(__fadd_rn(d.x, d.e) > 0.f)) d.x = d.e = 0.f;
+  if (!positive(d)) d.x = d.e = 0.f;
   return d;
 }
 
@@ -260,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
 
   // The first warp's walk.
   int cur = 0, kept = 1, n_refused = 0, passes = 0, t = 0, part0 = 0, part1 = 0;
-  double A = 0.0, S = 1.0, border = 0.0, before = 0.0;
+  Pair A = {0.f, 0.f}, S = {1.f, 0.f}, border = {0.f, 0.f}, before = {0.f, 0.f};
   bool summed = false;  // S and the warps' sums are those of (cur, A)
   bool ended = false;   // no child is left to try
   if (rank == 0 && tid == 0) path[0] = 0;
@@ -283,32 +301,38 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
         break;
       }
       t = child;
-      const double u = (double)fminf(fmaxf(s.u[t], 0.f), 1.f), p = (double)s.p[t];
+      const float u = fminf(fmaxf(s.u[t], 0.f), 1.f);
+      float p = s.p[t], q = s.q[t];
       const int token = s.token[t];
       bool take;
-      double rest = p;
       if (DRAFT) {
-        const double q = (double)s.q[t];
-        take = u * q * S < fmax(p - A * q, 0.0);
+        // (both sides scale with p and q, whose products would lose bits below 2^-126)
+        if (fmaxf(p, q) < 1.f) p *= 0x1p64f, q *= 0x1p64f;
+        const float m = __fmul_rn(u, q), lost = __fmaf_rn(u, q, -m);
+        Pair wanted = times(S, m);
+        wanted.e = __fmaf_rn(S.x, lost, wanted.e);
+        take = less(wanted, residual(p, q, A));
       } else {
         bool gone = false;
         for (int i = lane; i < n_refused; i += 32) gone |= s.refused[i] == token;
-        if (__any_sync(0xffffffffu, gone)) rest = 0.0;
-        take = u * S < rest;
+        if (__any_sync(0xffffffffu, gone)) p = 0.f;
+        take = less(times(S, u), {p, 0.f});
       }
       if (take) {
         if (rank == 0 && lane == 0) path[kept] = t;
         cur = t;
         ++kept;
-        A = 0.0;
-        S = 1.0;
+        A = {0.f, 0.f};
+        S = {1.f, 0.f};
         n_refused = 0;
         summed = false;
       } else if (DRAFT) {
-        A += S;
+        add(A, S);
+        A = two_sum(A.x, A.e);
         return kSum;
       } else {
-        S = fmax(S - rest, 0.0);
+        add(S, -p);
+        if (!positive(S)) S = {0.f, 0.f};
         if (lane == 0) s.refused[n_refused] = token;
         ++n_refused;
         __syncwarp();
@@ -318,50 +342,47 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
   };
   // After a sum: its value; false if the row is to be summed again.
   auto after_sum = [&]() {
-    const double *slot = s.cta[(passes - 1) & 1];
-    S = 0.0;
-    for (uint32_t c = 0; c < ctas; ++c) S += slot[c];
-    summed = S > 0.0;
+    S = over_warp(lane < (int)ctas ? s.cta[(passes - 1) & 1][lane] : Pair{0.f, 0.f});
+    S = two_sum(S.x, S.e);
+    summed = S.x > 0.f;
     if (!summed && (!ended || n_refused > 0)) {  // nothing is left: the target's row as it was
-      A = 0.0;
-      S = 1.0;
+      A = {0.f, 0.f};
+      S = {1.f, 0.f};
       n_refused = 0;
     } else if (!summed) {  // the row itself is empty
-      S = 0.0;
+      S = {0.f, 0.f};
     }
   };
   // The lane (of the first `n`) whose value takes the sum past the border, else the last with one above 0; `before`
   // becomes the sum of the lanes before it.  -1: every value is 0.
-  auto past_border = [&](double v, int n) -> int {
-    double inc = lane < n ? v : 0.0;
-    const unsigned any = __ballot_sync(0xffffffffu, inc > 0.0);
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) {  // (n is at most 16)
-      const double y = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += y;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, ((any >> lane) & 1u) && before + inc > border);
+  auto past_border = [&](Pair v, int n) -> int {
+    if (lane >= n) v = {0.f, 0.f};
+    const bool some_left = positive(v);
+    const unsigned any = __ballot_sync(0xffffffffu, some_left);
+    const Pair inc = scan(v, kWarps);  // (n is at most that)
+    Pair upto = before;
+    add(upto, inc);
+    const unsigned past = __ballot_sync(0xffffffffu, some_left && less(border, upto));
     if (!any) return -1;
     const int at = past ? __ffs(past) - 1 : 31 - __clz(any);
-    const double upto = __shfl_sync(0xffffffffu, inc, max(at - 1, 0));
-    if (at > 0) before += upto;
+    upto = shuffle(inc, max(at - 1, 0));
+    if (at > 0) add(before, upto);
     return at;
   };
 
   for (;;) {
     if (warp == 0) {
       int what = passes == 0 || !ended ? walk() : (summed ? kFind : kSum);
-      if (ended && passes > 0 && !(S > 0.0)) what = kDone;
+      if (ended && passes > 0 && !(S.x > 0.f)) what = kDone;
       if (what == kFind) {
         // the CTA, then the warp, whose part holds the border
         const float ul = a.u_last[req];
-        border = (double)fminf(fmaxf(ul, 0.f), 1.f) * S;
-        before = 0.0;
-        const double *slot = s.cta[(passes - 1) & 1];
-        if (past_border(lane < (int)ctas ? slot[lane] : 0.0, (int)ctas) != (int)rank) {
+        border = times(S, fminf(fmaxf(ul, 0.f), 1.f));
+        before = {0.f, 0.f};
+        if (past_border(s.cta[(passes - 1) & 1][lane & (kMostCtas - 1)], (int)ctas) != (int)rank) {
           what = kDone;
         } else {
-          const int w = max(past_border(lane < kWarps ? value(s.warp[lane]) : 0.0, kWarps), 0);
+          const int w = max(past_border(s.warp[lane & (kWarps - 1)], kWarps), 0);
           const Row<E> p(a.p, a.sp, first + cur, (int)a.V);
           part0 = part(0, p.blocks(), (int)rank * kWarps + w, (int)ctas * kWarps);
           part1 = part(0, p.blocks(), (int)rank * kWarps + w + 1, (int)ctas * kWarps);
@@ -373,27 +394,31 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
         s.n_refused = n_refused;
         s.part0 = part0;
         s.part1 = part1;
-        s.A.x = (float)A;
-        s.A.e = (float)(A - (double)(float)A);
+        s.A = A;
       }
     }
     __syncthreads();
     const int what = s.what;
     if (what == kDone) break;
+    // (a short part is taken block by block at once)
+    const bool at_once = what == kFind && s.part1 - s.part0 <= 64;
     const int row = first + s.cur, refused = s.n_refused;
     const Pair A2 = s.A;
     const Row<E> p(a.p, a.sp, row, (int)a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, row, (int)a.V);
     const int b0 = what == kSum ? 0 : s.part0, b1 = what == kSum ? p.blocks() : s.part1;
     const int i = what == kSum ? (int)rank * kWarps + warp : warp, n = what == kSum ? (int)ctas * kWarps : kWarps;
-    const Pair sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, n), part(b0, b1, i + 1, n));
-    if (lane == 0) s.warp[warp] = sum;
-    __syncthreads();
+    if (!at_once) {
+      const Pair sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, n), part(b0, b1, i + 1, n));
+      if (lane == 0) s.warp[warp] = sum;
+      __syncthreads();
+    }
     if (what == kSum) {
       if (warp == 0) {
-        double x = lane < kWarps ? value(s.warp[lane]) : 0.0;
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        if (lane < (int)ctas) put_remote(in_cta(smem_at(&s.cta[passes & 1][rank]), lane), x);
+        const Pair x = over_warp(lane < kWarps ? s.warp[lane] : Pair{0.f, 0.f});
+        if (lane < (int)ctas) {
+          put_remote(in_cta(smem_at(&s.cta[passes & 1][rank].x), lane), __float_as_uint(x.x));
+          put_remote(in_cta(smem_at(&s.cta[passes & 1][rank].e), lane), __float_as_uint(x.e));
+        }
       }
       cluster_arrive();
       cluster_wait();
@@ -405,8 +430,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     }
     // The border lies in a sixteenth of the part: the first warp takes it block by block.
     if (warp == 0) {
-      const int w = max(past_border(lane < kWarps ? value(s.warp[lane]) : 0.0, kWarps), 0);
-      const int w0 = part(b0, b1, w, kWarps), w1 = part(b0, b1, w + 1, kWarps);
+      int w0 = b0, w1 = b1;
+      if (!at_once) {
+        const int w = max(past_border(s.warp[lane & (kWarps - 1)], kWarps), 0);
+        w0 = part(b0, b1, w, kWarps);
+        w1 = part(b0, b1, w + 1, kWarps);
+      }
       int last = -1;  // the last token so far of which anything is left
       for (int c0 = w0; c0 < w1; c0 += 32) {
         const int b = c0 + lane;
@@ -419,36 +448,32 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
         left(pw, qw, A2, refused, b, p.shift, x);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) add(sum, x[j]);
-        const double mine = value(sum);
-        double inc = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, inc, d);
-          if (lane >= d) inc += y;
-        }
-        const unsigned any = __ballot_sync(0xffffffffu, mine > 0.0);
-        const unsigned past = __ballot_sync(0xffffffffu, mine > 0.0 && before + inc > border);
+        const Pair inc = scan(sum, 32);
+        Pair run = before;
+        add(run, inc);
+        const bool some_left = positive(sum);
+        const unsigned any = __ballot_sync(0xffffffffu, some_left);
+        const unsigned past = __ballot_sync(0xffffffffu, some_left && less(border, run));
         if (any) {
           const int from = past ? __ffs(past) - 1 : 31 - __clz(any);
           // in that lane: the first token past the border, else the last with anything left
-          double run = __shfl_up_sync(0xffffffffu, inc, 1);
-          run = before + (lane > 0 ? run : 0.0);
+          const Pair prior = shuffle(inc, max(from - 1, 0));
+          run = before;
+          if (from > 0) add(run, prior);
           int pick = -1;
-          if (lane == from) {
-            bool done = false;
+          bool done = false;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              run += value(x[j]);
-              if (value(x[j]) > 0.0 && !done) {
-                pick = b * VEC - p.shift + j;
-                done = run > border;
-              }
+          for (int j = 0; j < VEC; ++j) {
+            add(run, x[j]);
+            if (positive(x[j]) && !done) {
+              pick = b * VEC - p.shift + j;
+              done = less(border, run);
             }
           }
           last = __shfl_sync(0xffffffffu, pick, from);
           if (past) break;
         }
-        before += __shfl_sync(0xffffffffu, inc, 31);
+        add(before, shuffle(inc, 31));
       }
       if (lane == 0) a.next[req] = last;
     }
@@ -458,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     for (int j = kept + lane; j < a.max_path; j += 32) path[j] = -1;
     if (lane == 0) {
       a.kept[req] = kept;
-      if (!(S > 0.0)) a.next[req] = -1;
+      if (!(S.x > 0.f)) a.next[req] = -1;
     }
   }
 }
