@@ -59,8 +59,35 @@ __device__ __forceinline__ void put_remote(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
-// A probability: what is negative, infinite or no number counts as 0.
-__device__ __forceinline__ float some(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
+// A probability: what is negative, infinite or no number counts as 0 (by its bits: all of these lie at or
+// above infinity's).
+__device__ __forceinline__ float some(float x) { return __float_as_uint(x) < 0x7f800000u ? x : 0.f; }
+
+// Two fp32 lanes in one 64-bit register, added and multiplied in one instruction.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {  // a - b, rounded once
+  return f2_fma(b, 0xbf800000bf800000ull, a);
+}
 
 // x + e, e the error of x: a pair of fp32 numbers holds what a sum in fp32 would lose.
 struct Pair {
@@ -70,7 +97,8 @@ struct Pair {
 struct Shared {
   int parent[FM_MAX_NODES], token[FM_MAX_NODES];  // token -1: outside the vocabulary
   float u[FM_MAX_NODES], p[FM_MAX_NODES], q[FM_MAX_NODES];
-  int first, nodes;             // as the first CTA read them
+  int first, nodes;             // as the first CTA read them, and the last random number
+  float u_last;
   int refused[FM_MAX_NODES];    // tokens taken out of p (children that were chosen)
   Pair cta[2][kMostCtas];       // the CTAs' sums, of alternate passes
   Pair warp[kWarps];            // this CTA's warps' sums
@@ -145,6 +173,32 @@ __device__ __forceinline__ Pair over_warp(Pair v) {  // the warp's sum, in every
   // (the lanes' additions differ in their order, and so may the last bits)
   return {__shfl_sync(0xffffffffu, v.x, 0), __shfl_sync(0xffffffffu, v.e, 0)};
 }
+// Two pairs side by side.
+struct Pair2 {
+  uint64_t x, e;
+};
+__device__ __forceinline__ Pair2 two_sum(uint64_t a, uint64_t b) {
+  const uint64_t s = f2_add(a, b), bb = f2_sub(s, a);
+  return {s, f2_add(f2_sub(a, f2_sub(s, bb)), f2_sub(b, bb))};
+}
+__device__ __forceinline__ Pair2 two_difference(uint64_t a, uint64_t b) {  // a - b
+  const uint64_t s = f2_sub(a, b), bb = f2_sub(s, a);
+  return {s, f2_sub(f2_sub(a, f2_sub(s, bb)), f2_add(b, bb))};
+}
+__device__ __forceinline__ void add(Pair2 &sum, Pair2 v) {
+  const Pair2 s = two_sum(sum.x, v.x);
+  sum.x = s.x;
+  sum.e = f2_add(sum.e, f2_add(s.e, v.e));
+}
+__device__ __forceinline__ void add(Pair2 &sum, uint64_t v) {
+  const Pair2 s = two_sum(sum.x, v);
+  sum.x = s.x;
+  sum.e = f2_add(sum.e, s.e);
+}
+__device__ __forceinline__ void split(Pair2 v, Pair &lo, Pair &hi) {
+  f2_split(v.x, lo.x, hi.x);
+  f2_split(v.e, lo.e, hi.e);
+}
 __device__ __forceinline__ void add(Pair &sum, float v) {
   const Pair s = two_sum(sum.x, v);
   sum.x = s.x;
@@ -157,6 +211,28 @@ __device__ __forceinline__ Pair residual(float p, float q, Pair A) {
   d.e = __fadd_rn(d.e, -lost);
   if (!positive(d)) d.x = d.e = 0.f;
   return d;
+}
+__device__ __forceinline__ Pair2 residual(uint64_t p, uint64_t q, Pair A) {
+  Pair2 d;
+  if (A.x == 1.f && A.e == 0.f) {  // after one refusal
+    d = two_difference(p, q);
+  } else {
+    const uint64_t ax = f2(A.x, A.x), m = f2_mul(q, ax);
+    d = two_difference(p, m);
+    d.e = f2_sub(d.e, f2_fma(q, f2(A.e, A.e), f2_fma(q, ax, f2_sub(0ull, m))));
+  }
+  Pair lo, hi;
+  split(d, lo, hi);
+  float slo, shi;
+  f2_split(f2_add(d.x, d.e), slo, shi);
+  return {f2(slo > 0.f ? lo.x : 0.f, shi > 0.f ? hi.x : 0.f), f2(slo > 0.f ? lo.e : 0.f, shi > 0.f ? hi.e : 0.f)};
+}
+// 16 bytes of a row as probabilities, two by two.
+template <typename E>
+__device__ __forceinline__ void unpack(uint4 w, uint64_t (&x)[8 / sizeof(E)]) {
+  const E *e = reinterpret_cast<const E *>(&w);
+#pragma unroll
+  for (int j = 0; j < 8 / (int)sizeof(E); ++j) x[j] = f2(some(as_f32(e[2 * j])), some(as_f32(e[2 * j + 1])));
 }
 
 template <typename E, bool DRAFT>
@@ -172,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
   pdl_trigger();
   if (rank == 0) {
     const Rows r = rows_of(a.cu_q, req, a.T, tid == 0 ? a.err : nullptr);
+    const float u_last = a.u_last[req];
     int nodes = r.count;
     if (nodes > FM_MAX_NODES) {
       if (tid == 0) report(a.err, kDevErrLength, (unsigned)req, (unsigned)r.first, (unsigned)(r.first + r.count), 0u);
@@ -181,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     if (tid < (int)ctas) {
       put_remote(in_cta(smem_at(&s.first), tid), (uint32_t)r.first);
       put_remote(in_cta(smem_at(&s.nodes), tid), (uint32_t)nodes);
+      put_remote(in_cta(smem_at(&s.u_last), tid), __float_as_uint(fminf(fmaxf(u_last, 0.f), 1.f)));
     }
     for (int t = tid; t < nodes; t += kThreads) {
       const int row = r.first + t;
@@ -220,21 +298,27 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     return;
   }
   // What is left of the elements of block b of the row after node cur.
-  auto left = [&](uint4 pw, uint4 qw, Pair A, int n_refused, int b, int shift, Pair (&x)[VEC]) {
-    const E *pe = reinterpret_cast<const E *>(&pw), *qe = reinterpret_cast<const E *>(&qw);
+  auto left = [&](uint4 pw, uint4 qw, Pair A, int n_refused, int b, int shift, Pair2 (&x)[VEC / 2]) {
+    uint64_t p2[VEC / 2];
+    unpack<E>(pw, p2);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      x[j] = {some(as_f32(pe[j])), 0.f};
-      if (DRAFT && A.x > 0.f) x[j] = residual(x[j].x, some(as_f32(qe[j])), A);
+    for (int j = 0; j < VEC / 2; ++j) x[j] = {p2[j], 0ull};
+    if (DRAFT && A.x > 0.f) {
+      uint64_t q2[VEC / 2];
+      unpack<E>(qw, q2);
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j) x[j] = residual(p2[j], q2[j], A);
     }
-    if (!DRAFT) {
+    if (!DRAFT && n_refused > 0) {
+      uint32_t gone = 0u;  // elements of the block
 #pragma unroll 1
       for (int i = 0; i < n_refused; ++i) {
         const int at = s.refused[i] + shift - b * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (j == at) x[j].x = 0.f;
+        if (at >= 0 && at < VEC) gone |= 1u << at;
       }
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j)
+        x[j].x &= ((gone >> (2 * j)) & 1u ? 0ull : 0xffffffffull) | ((gone >> (2 * j + 1)) & 1u ? 0ull : 0xffffffff00000000ull);
     }
   };
   // The warp's sum of what is left of the blocks [w0, w1).
@@ -248,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
       }
       if (!__any_sync(0xffffffffu, here)) n_refused = 0;
     }
-    Pair sum = {0.f, 0.f};
-    for (int b0 = w0 + lane; b0 < w1; b0 += 32 * U) {
+    Pair2 sum = {0ull, 0ull};
+    for (int b0 = w0 + lane; b0 - lane < w1; b0 += 32 * U) {
       uint4 pw[U], qw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -262,19 +346,27 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        Pair x[VEC];
-        left(pw[u], qw[u], A, n_refused, b0 + 32 * u, p.shift, x);
+        if (u == 0 || b0 - lane + 32 * u < w1) {
+          Pair2 x[VEC / 2];
+          left(pw[u], qw[u], A, n_refused, b0 + 32 * u, p.shift, x);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (DRAFT) add(sum, x[j]);
-          else add(sum, x[j].x);
+          for (int j = 0; j < VEC / 2; ++j) {
+            if (DRAFT) add(sum, x[j]);
+            else add(sum, x[j].x);
+          }
         }
       }
     }
-    return over_warp(sum);
+    Pair lo, hi;
+    split(sum, lo, hi);
+    add(lo, hi);
+    return over_warp(lo);
   };
-  // Part `i` of `n` even ones of the blocks [b0, b1).
-  auto part = [](int b0, int b1, int i, int n) -> int { return b0 + (int)((int64_t)(b1 - b0) * i / n); };
+  // Where part `i` of 2^k even ones of the blocks [b0, b1) begins.
+  auto part = [](int b0, int b1, int i, int k) -> int { return b0 + (int)((int64_t)(b1 - b0) * i >> k); };
+  constexpr int kLogWarps = 4;
+  static_assert(1 << kLogWarps == kWarps, "");
+  const int log_parts = kLogWarps + 31 - __clz((int)ctas);  // (the cluster's size is a power of two)
 
   // The first warp's walk.
   int cur = 0, kept = 1, n_refused = 0, passes = 0, t = 0, part0 = 0, part1 = 0;
@@ -376,16 +468,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
       if (ended && passes > 0 && !(S.x > 0.f)) what = kDone;
       if (what == kFind) {
         // the CTA, then the warp, whose part holds the border
-        const float ul = a.u_last[req];
-        border = times(S, fminf(fmaxf(ul, 0.f), 1.f));
+        border = times(S, s.u_last);
         before = {0.f, 0.f};
         if (past_border(s.cta[(passes - 1) & 1][lane & (kMostCtas - 1)], (int)ctas) != (int)rank) {
           what = kDone;
         } else {
           const int w = max(past_border(s.warp[lane & (kWarps - 1)], kWarps), 0);
           const Row<E> p(a.p, a.sp, first + cur, (int)a.V);
-          part0 = part(0, p.blocks(), (int)rank * kWarps + w, (int)ctas * kWarps);
-          part1 = part(0, p.blocks(), (int)rank * kWarps + w + 1, (int)ctas * kWarps);
+          part0 = part(0, p.blocks(), (int)rank * kWarps + w, log_parts);
+          part1 = part(0, p.blocks(), (int)rank * kWarps + w + 1, log_parts);
         }
       }
       if (lane == 0) {
@@ -406,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     const Pair A2 = s.A;
     const Row<E> p(a.p, a.sp, row, (int)a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, row, (int)a.V);
     const int b0 = what == kSum ? 0 : s.part0, b1 = what == kSum ? p.blocks() : s.part1;
-    const int i = what == kSum ? (int)rank * kWarps + warp : warp, n = what == kSum ? (int)ctas * kWarps : kWarps;
+    const int i = what == kSum ? (int)rank * kWarps + warp : warp, k = what == kSum ? log_parts : kLogWarps;
     if (!at_once) {
-      const Pair sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, n), part(b0, b1, i + 1, n));
+      const Pair sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, k), part(b0, b1, i + 1, k));
       if (lane == 0) s.warp[warp] = sum;
       __syncthreads();
     }
@@ -433,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
       int w0 = b0, w1 = b1;
       if (!at_once) {
         const int w = max(past_border(s.warp[lane & (kWarps - 1)], kWarps), 0);
-        w0 = part(b0, b1, w, kWarps);
-        w1 = part(b0, b1, w + 1, kWarps);
+        w0 = part(b0, b1, w, kLogWarps);
+        w1 = part(b0, b1, w + 1, kLogWarps);
       }
       int last = -1;  // the last token so far of which anything is left
       for (int c0 = w0; c0 < w1; c0 += 32) {
@@ -444,8 +535,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
           pw = p.load(b, p.shift);
           if (DRAFT && A2.x > 0.f) qw = q.load(b, p.shift);
         }
+        Pair2 x2[VEC / 2];
         Pair x[VEC], sum = {0.f, 0.f};
-        left(pw, qw, A2, refused, b, p.shift, x);
+        left(pw, qw, A2, refused, b, p.shift, x2);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) split(x2[j], x[2 * j], x[2 * j + 1]);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) add(sum, x[j]);
         const Pair inc = scan(sum, 32);
