@@ -100,8 +100,9 @@ struct Shared {
   int first, nodes;             // as the first CTA read them, and the last random number
   float u_last;
   int refused[FM_MAX_NODES];    // tokens taken out of p (children that were chosen)
-  Pair cta[2][kMostCtas];       // the CTAs' sums, of alternate passes
-  Pair warp[kWarps];            // this CTA's warps' sums
+  Pair part[2][kMostCtas * kWarps];  // the sums of all CTAs' warps, of alternate passes
+  Pair upto[32];                // the first warp's prefix sums over them
+  Pair warp[kWarps];            // this CTA's warps' sums of a part
   // what the first warp has the others do: sum the row after node `cur` (A, n_refused tokens taken out),
   // or look for the border in the blocks [part0, part1) of it, or nothing more
   int what, cur, n_refused, part0, part1;
@@ -109,29 +110,34 @@ struct Shared {
 };
 enum : int { kSum, kFind, kDone };
 
-// A row of one model in blocks of 16 bytes, block 0 beginning at the boundary before the row's start:
-// element `e` of block b is element b * VEC - shift + e of the row.
+// A row of one model in blocks of 16 bytes, block 0 beginning `shift` elements before the row: element `e`
+// of block b is element b * VEC - shift + e of the row.  A target's row has the shift that puts its blocks on
+// 16-byte boundaries; the draft's row is cut like it, and its blocks may lie anywhere.
 template <typename E>
 struct Row {
   static constexpr int VEC = 16 / (int)sizeof(E);
   const E *at;  // of block 0
   int shift, V;
+  int full0;             // the blocks that one load takes: on a boundary, and inside the row
+  unsigned full;
 
-  __device__ __forceinline__ Row(const void *base, int64_t stride, int64_t row, int V_) : V(V_) {
+  __device__ __forceinline__ Row(const void *base, int64_t stride, int64_t row, int V_, int shift_ = -1) : V(V_) {
     const E *p = reinterpret_cast<const E *>(base) + row * stride;
-    shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(E));
+    const int own = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(E));
+    shift = shift_ < 0 ? own : shift_;
     at = p - shift;
+    full0 = shift > 0 ? 1 : 0;
+    full = own == shift ? (unsigned)max((V + shift) / VEC - full0, 0) : 0u;
   }
   __device__ __forceinline__ int blocks() const { return (V + shift + VEC - 1) / VEC; }
-  // block b as a row of alignment `s` has it
-  __device__ __forceinline__ uint4 load(int b, int s) const {
-    const int i = b * VEC - s;  // in the row
-    if (s == shift && i >= 0 && i + VEC <= V) return *reinterpret_cast<const uint4 *>(at + i + shift);
+  __device__ __forceinline__ uint4 load(int b) const {
+    if ((unsigned)(b - full0) < full) return *reinterpret_cast<const uint4 *>(at + b * VEC);
+    const int i = b * VEC - shift;  // in the row
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     E *e = reinterpret_cast<E *>(&w);
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
-      if (i + j >= 0 && i + j < V) e[j] = at[shift + i + j];
+      if (i + j >= 0 && i + j < V) e[j] = at[b * VEC + j];
     return w;
   }
 };
@@ -212,27 +218,31 @@ __device__ __forceinline__ Pair residual(float p, float q, Pair A) {
   if (!positive(d)) d.x = d.e = 0.f;
   return d;
 }
+// (a p that is no probability gives no residual: it is not above 0, or its error is no number)
 __device__ __forceinline__ Pair2 residual(uint64_t p, uint64_t q, Pair A) {
-  Pair2 d;
-  if (A.x == 1.f && A.e == 0.f) {  // after one refusal
-    d = two_difference(p, q);
-  } else {
-    const uint64_t ax = f2(A.x, A.x), m = f2_mul(q, ax);
-    d = two_difference(p, m);
-    d.e = f2_sub(d.e, f2_fma(q, f2(A.e, A.e), f2_fma(q, ax, f2_sub(0ull, m))));
-  }
   Pair lo, hi;
+  if (A.x == 1.f && A.e == 0.f) {  // after one refusal: the difference's sign is its value's, and its error's when that is 0
+    split(two_difference(p, q), lo, hi);
+    const bool l = lo.x > 0.f && lo.x < INFINITY, h = hi.x > 0.f && hi.x < INFINITY;
+    return {f2(l ? lo.x : 0.f, h ? hi.x : 0.f), f2(l ? lo.e : 0.f, h ? hi.e : 0.f)};
+  }
+  const uint64_t ax = f2(A.x, A.x), m = f2_mul(q, ax);
+  Pair2 d = two_difference(p, m);
+  d.e = f2_sub(d.e, f2_fma(q, f2(A.e, A.e), f2_fma(q, ax, f2_sub(0ull, m))));
   split(d, lo, hi);
-  float slo, shi;
-  f2_split(f2_add(d.x, d.e), slo, shi);
-  return {f2(slo > 0.f ? lo.x : 0.f, shi > 0.f ? hi.x : 0.f), f2(slo > 0.f ? lo.e : 0.f, shi > 0.f ? hi.e : 0.f)};
+  float l, h;
+  f2_split(f2_add(d.x, d.e), l, h);
+  return {f2(l > 0.f ? lo.x : 0.f, h > 0.f ? hi.x : 0.f), f2(l > 0.f ? lo.e : 0.f, h > 0.f ? hi.e : 0.f)};
 }
 // 16 bytes of a row as probabilities, two by two.
-template <typename E>
+template <typename E, bool ALL>
 __device__ __forceinline__ void unpack(uint4 w, uint64_t (&x)[8 / sizeof(E)]) {
   const E *e = reinterpret_cast<const E *>(&w);
 #pragma unroll
-  for (int j = 0; j < 8 / (int)sizeof(E); ++j) x[j] = f2(some(as_f32(e[2 * j])), some(as_f32(e[2 * j + 1])));
+  for (int j = 0; j < 8 / (int)sizeof(E); ++j) {
+    const float a = as_f32(e[2 * j]), b = as_f32(e[2 * j + 1]);
+    x[j] = ALL ? f2(a, b) : f2(some(a), some(b));
+  }
 }
 
 template <typename E, bool DRAFT>
@@ -300,15 +310,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
   // What is left of the elements of block b of the row after node cur.
   auto left = [&](uint4 pw, uint4 qw, Pair A, int n_refused, int b, int shift, Pair2 (&x)[VEC / 2]) {
     uint64_t p2[VEC / 2];
-    unpack<E>(pw, p2);
-#pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) x[j] = {p2[j], 0ull};
     if (DRAFT && A.x > 0.f) {
       uint64_t q2[VEC / 2];
-      unpack<E>(qw, q2);
+      unpack<E, true>(pw, p2);
+      unpack<E, false>(qw, q2);
 #pragma unroll
       for (int j = 0; j < VEC / 2; ++j) x[j] = residual(p2[j], q2[j], A);
+      return;
     }
+    unpack<E, false>(pw, p2);
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) x[j] = {p2[j], 0ull};
     if (!DRAFT && n_refused > 0) {
       uint32_t gone = 0u;  // elements of the block
 #pragma unroll 1
@@ -340,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
         const int b = b0 + 32 * u;
         pw[u] = qw[u] = make_uint4(0u, 0u, 0u, 0u);
         if (b < w1) {
-          pw[u] = p.load(b, p.shift);
-          if (DRAFT && A.x > 0.f) qw[u] = q.load(b, p.shift);
+          pw[u] = p.load(b);
+          if (DRAFT && A.x > 0.f) qw[u] = q.load(b);
         }
       }
 #pragma unroll
@@ -432,9 +444,18 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     }
     return summed ? kFind : kSum;
   };
-  // After a sum: its value; false if the row is to be summed again.
+  // The sums of all CTAs' warps, a power of two of them a lane.
+  const int log_each = max(log_parts - 5, 0), each = 1 << log_each;
+  auto part_sum = [&](int i) -> Pair { return i < 1 << log_parts ? s.part[(passes - 1) & 1][i] : Pair{0.f, 0.f}; };
+  unsigned nonzero = 0u;  // lanes whose parts hold anything
+  // After a sum: its value.
   auto after_sum = [&]() {
-    S = over_warp(lane < (int)ctas ? s.cta[(passes - 1) & 1][lane] : Pair{0.f, 0.f});
+    Pair mine = part_sum(lane << log_each);
+    for (int j = 1; j < each; ++j) add(mine, part_sum((lane << log_each) + j));
+    nonzero = __ballot_sync(0xffffffffu, positive(mine));
+    const Pair inc = scan(mine, 32);
+    s.upto[lane] = inc;
+    S = shuffle(inc, 31);
     S = two_sum(S.x, S.e);
     summed = S.x > 0.f;
     if (!summed && (!ended || n_refused > 0)) {  // nothing is left: the target's row as it was
@@ -444,6 +465,23 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     } else if (!summed) {  // the row itself is empty
       S = {0.f, 0.f};
     }
+    __syncwarp();
+  };
+  // The part of the row that holds the border, and in `before` the sum of the parts before it.
+  auto part_of_border = [&]() -> int {
+    const unsigned past = __ballot_sync(0xffffffffu, less(border, s.upto[lane])) & nonzero;
+    const int at = past ? __ffs(past) - 1 : 31 - __clz(nonzero | 1u);
+    Pair upto = at > 0 ? s.upto[at - 1] : Pair{0.f, 0.f};
+    int found = at << log_each;
+    for (int j = 0; j < each; ++j) {
+      const Pair v = part_sum((at << log_each) + j);
+      if (!positive(v)) continue;
+      found = (at << log_each) + j;
+      before = upto;
+      add(upto, v);
+      if (less(border, upto)) break;
+    }
+    return found;
   };
   // The lane (of the first `n`) whose value takes the sum past the border, else the last with one above 0; `before`
   // becomes the sum of the lanes before it.  -1: every value is 0.
@@ -467,16 +505,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
       int what = passes == 0 || !ended ? walk() : (summed ? kFind : kSum);
       if (ended && passes > 0 && !(S.x > 0.f)) what = kDone;
       if (what == kFind) {
-        // the CTA, then the warp, whose part holds the border
         border = times(S, s.u_last);
-        before = {0.f, 0.f};
-        if (past_border(s.cta[(passes - 1) & 1][lane & (kMostCtas - 1)], (int)ctas) != (int)rank) {
+        const int w = part_of_border();
+        if (w / kWarps != (int)rank) {
           what = kDone;
         } else {
-          const int w = max(past_border(s.warp[lane & (kWarps - 1)], kWarps), 0);
           const Row<E> p(a.p, a.sp, first + cur, (int)a.V);
-          part0 = part(0, p.blocks(), (int)rank * kWarps + w, log_parts);
-          part1 = part(0, p.blocks(), (int)rank * kWarps + w + 1, log_parts);
+          part0 = part(0, p.blocks(), w, log_parts);
+          part1 = part(0, p.blocks(), w + 1, log_parts);
         }
       }
       if (lane == 0) {
@@ -495,30 +531,25 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
     const bool at_once = what == kFind && s.part1 - s.part0 <= 64;
     const int row = first + s.cur, refused = s.n_refused;
     const Pair A2 = s.A;
-    const Row<E> p(a.p, a.sp, row, (int)a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, row, (int)a.V);
+    const Row<E> p(a.p, a.sp, row, (int)a.V), q(DRAFT ? a.q : a.p, DRAFT ? a.sq : a.sp, row, (int)a.V, p.shift);
     const int b0 = what == kSum ? 0 : s.part0, b1 = what == kSum ? p.blocks() : s.part1;
     const int i = what == kSum ? (int)rank * kWarps + warp : warp, k = what == kSum ? log_parts : kLogWarps;
-    if (!at_once) {
-      const Pair sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, k), part(b0, b1, i + 1, k));
-      if (lane == 0) s.warp[warp] = sum;
-      __syncthreads();
-    }
+    Pair sum = {0.f, 0.f};
+    if (!at_once) sum = sum_blocks(p, q, A2, refused, part(b0, b1, i, k), part(b0, b1, i + 1, k));
     if (what == kSum) {
-      if (warp == 0) {
-        const Pair x = over_warp(lane < kWarps ? s.warp[lane] : Pair{0.f, 0.f});
-        if (lane < (int)ctas) {
-          put_remote(in_cta(smem_at(&s.cta[passes & 1][rank].x), lane), __float_as_uint(x.x));
-          put_remote(in_cta(smem_at(&s.cta[passes & 1][rank].e), lane), __float_as_uint(x.e));
-        }
+      if (lane < (int)ctas) {
+        Pair *to = &s.part[passes & 1][i];
+        put_remote(in_cta(smem_at(&to->x), lane), __float_as_uint(sum.x));
+        put_remote(in_cta(smem_at(&to->e), lane), __float_as_uint(sum.e));
       }
       cluster_arrive();
       cluster_wait();
-      if (warp == 0) {
-        ++passes;
-        after_sum();
-      }
+      ++passes;
+      if (warp == 0) after_sum();
       continue;
     }
+    if (lane == 0) s.warp[warp] = sum;
+    __syncthreads();
     // The border lies in a sixteenth of the part: the first warp takes it block by block.
     if (warp == 0) {
       int w0 = b0, w1 = b1;
@@ -532,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
         const int b = c0 + lane;
         uint4 pw = make_uint4(0u, 0u, 0u, 0u), qw = pw;
         if (b < w1) {
-          pw = p.load(b, p.shift);
-          if (DRAFT && A2.x > 0.f) qw = q.load(b, p.shift);
+          pw = p.load(b);
+          if (DRAFT && A2.x > 0.f) qw = q.load(b);
         }
         Pair2 x2[VEC / 2];
         Pair x[VEC], sum = {0.f, 0.f};
