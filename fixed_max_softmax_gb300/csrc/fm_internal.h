@@ -211,7 +211,7 @@ struct SeqsSpace {
   int64_t max_items;
 };
 SeqsGeom seqs_geom_simt(int64_t T, int group, int rows);
-SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group);
+SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group, bool tree = false);
 SeqsSpace seqs_space(const SeqsGeom &g, int64_t n, int64_t T, int64_t Hk, int64_t D);
 // The shared memory that every variant may use; once per device, at its first call: a later call that
 // needs another variant may be inside a stream capture.

@@ -219,7 +219,7 @@ int attn_seqs(const char *name, bool paged, const TreeMask *mask, const fm_tenso
     return e;
   };
   e = cudaErrorNotSupported;
-  if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group), mask ? launch_seqs_tree_tc : launch_seqs_tc);
+  if (seqs_tc_supported(a)) e = run(seqs_geom_tc(a.q.S, a.n, group, mask != nullptr), mask ? launch_seqs_tree_tc : launch_seqs_tc);
   // fp32, and layouts that the tensor-core kernel or the tensor-map encoder does not take (a work
   // list made for it then goes unused)
   if (e == cudaErrorNotSupported)

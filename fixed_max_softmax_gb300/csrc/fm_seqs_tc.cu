@@ -15,7 +15,7 @@ bool seqs_tc_supported(const SeqsArgs &a) {
          rows_aligned(a.o, a.o.dtype == FM_F32 ? 4 : 2, 16);
 }
 
-SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
+SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group, bool tree) {
   SeqsGeom g;
   g.group = group;
   g.tq = 2 * (128 / group);
@@ -30,7 +30,11 @@ SeqsGeom seqs_geom_tc(int64_t T, int64_t n, int group) {
   // The rule knows the arrays, not the lengths in them, which are on the device: the decode batch in
   // buffers of 2,048 rows takes the list (146 -> 155 us), a prompt of 6,000 among 255 idle rows even runs
   // (325 -> 351).
-  g.stream = T * group <= 128 * n ? 1 : 0;
+  // Trees have tens of tokens over long contexts, where the list's three launches and uneven pieces cost more:
+  // one tree of 64 over 8k 35 and 39, 4 of 64 over 65k (8 heads to one) 177 and 219, one of 1,024 over 30k 372 and
+  // 444, 3 chunks of 500 beside a tree 85 and 90 (3,100 rows a request); chunks of 2,000 beside a tree 103 and 94
+  // (7,600), of 4,000 112 and 106 (8,000).
+  g.stream = T * group <= (tree ? 4096 : 128) * n ? 1 : 0;
   return g;
 }
 
