@@ -636,9 +636,19 @@ static_assert(sizeof(Shared) <= 48 * 1024, "shared memory without an attribute")
 }  // namespace
 
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t st) {
-  // as many CTAs a request as two a SM allow, each with some thousand tokens at least
+  // As many CTAs a request as two a SM allow, or three where each has 96 KiB to read, and a thousand tokens at
+  // least.  By CTAs a request (us, L2 flushed):
+  //   requests, tokens, rows of                  1     2     4     8
+  //     1   128,000  bf16, target and draft   29.3  22.2  19.1  17.1
+  //    48   100,003  bf16, target             33.4  25.2  21.2  29.3
+  //    64   128,000  fp32, both                126  72.4  49.8  47.7
+  //   100    64,000  fp32, both               86.8  56.0  42.7  49.8
+  //   200    32,000  fp32, both               64.2  47.8  47.8  64.2
+  //   230    64,000  bf16, target             30.8  38.9  49.8  74.4
+  //    16     4,000  fp32, both               23.2  21.2  21.2  23.2
+  const int64_t bytes = a.V * (a.dtype == FM_F32 ? 4 : 2) * (a.q ? 2 : 1), sms = current_device_sm_count();
   unsigned ctas = kMostCtas;
-  while (ctas > 1 && ((int64_t)a.n * ctas > 2 * current_device_sm_count() || a.V < 2048 * (int64_t)ctas)) ctas /= 2;
+  while (ctas > 1 && (a.n * ctas > (bytes / ctas >= 96 * 1024 ? 3 : 2) * sms || a.V < 1024 * (int64_t)ctas)) ctas /= 2;
   const bool draft = a.q != nullptr;
   if (a.dtype == FM_F32) return draft ? launch<float, true>(a, ctas, st) : launch<float, false>(a, ctas, st);
   if (a.dtype == FM_BF16) return draft ? launch<__nv_bfloat16, true>(a, ctas, st) : launch<__nv_bfloat16, false>(a, ctas, st);
