@@ -21,7 +21,9 @@
 // numbers, a value and its error, good to about 2^-45: an SM adds two 64-bit numbers a clock, and one takes
 // some hundred clocks, a pair's addition a dozen fp32 operations (64 chains over 128,000 tokens: 152 us with
 // 64-bit sums, 98 with pairs for the elements and 64 bits in every warp's tests, 29 with 64 bits in one warp of a
-// CTA, LATER without).
+// CTA, 28 without any; 22 with two elements to an instruction).
+// Bound by latency: at that size the row's sum takes 8 us, HBM's rate for its 65 MB, and the way to it and on
+// (nodes, tests, the CTAs' meeting, the search for the border) as long again; a refusal at a row in L2 some 2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
