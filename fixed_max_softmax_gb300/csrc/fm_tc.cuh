@@ -1,6 +1,6 @@
 // fm_tc.cuh -- building blocks of the tensor-core attention kernels (sm_103a): the PTX of
 // mbarriers, bulk tensor copies, tensor memory and tcgen05.mma, and the exponentials and row max
-// of a score tile, as fm_chunk_tc.cu and fm_seqs_tc.cu use them.
+// of a score tile, as fm_chunk_tc.cu and fm_seqs_tc.cuh use them.
 #pragma once
 
 #include <cuda.h>
