@@ -270,3 +270,65 @@ def test_decoding_with_drafts(dev, dtype, drafted, captured):  # noqa: F811
         assert sorted(sum(held, []) + first.free_pages[:first.free_count.item()].tolist()) == list(range(80))
         assert (out[:, T:] == 7.0).all()
     assert moved > 10
+
+
+def test_moves_past_32_bit_offsets(dev):  # noqa: F811
+    pages, ps, H, D = 262152, 16, 4, 128
+    cache = torch.empty(pages, ps, H, D, dtype=BF16, device=dev).transpose(1, 2)  # 2.1e9 elements
+    last, g = pages * ps - 1, torch.Generator(device=dev).manual_seed(73)
+    src, dst = [[last, last - 1, 5]], [[3, last - 40, last - 2]]
+    rows = rand(g, 3, H, D, dtype=BF16)
+    for s, r in zip(src[0], rows):
+        cache[s // ps, :, s % ps] = r
+    fm.fm_paged_move(ints(src, dev, torch.int64), ints(dst, dev, torch.int64), cache, cache)
+    fm.fm_sync_status()
+    for s, r in zip(dst[0], rows):
+        assert torch.equal(cache[s // ps, :, s % ps], r)
+
+
+def test_captured_calls_may_be_the_first_of_their_kind(tmp_path):
+    """After one attention call on the device every call on trees can be captured though none has run: in a process of
+    its own."""
+    import subprocess
+    import sys
+
+    code = """
+import torch, fixed_max_softmax_gb300 as fm
+dev = torch.device("cuda:0")
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+c = {d: fm.PagedKVCache(64, 16, 2, 128, 2, 10, 600, dtype=d, device=dev) for d in (torch.bfloat16, torch.float32)}
+first = c[torch.float32]
+first.extend(i32([1, 1]))
+first.write(torch.ones(2, 2, 128, device=dev), torch.ones(2, 2, 128, device=dev))
+first.attention(torch.ones(2, 4, 128, device=dev))
+big = fm.PagedKVCache(8, 16, 1, 64, 8192, 1, 16, device=dev)
+parent, cu = i32([-1, 0, 0, 1] * 2), None
+p = {d: torch.full((8, 1000), 1e-3, dtype=d, device=dev) for d in (torch.float32, torch.bfloat16, torch.float16)}
+u, last, tok, new = torch.full((8,), .5, device=dev), torch.full((2,), .5, device=dev), i32([1] * 8), i32([4, 4])
+wide, none = torch.zeros(8192, 2, dtype=torch.int32, device=dev), torch.zeros(8192, dtype=torch.int32, device=dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for d, x in c.items():
+        x.extend(new)
+        m = x.tree(parent, 1)
+        rows = torch.ones(8, 2, 128, dtype=d, device=dev)
+        x.write(rows, rows)
+        o = x.tree_attention(torch.ones(8, 4, 128, dtype=d, device=dev), m)
+        for q in p.values():
+            for draft in (None, q):
+                path, kept, nxt = fm.verify_tree(q, tok, parent, x.cu_q, u, last, draft, 4)
+        x.move(x.keep(path, kept))
+    big.move(big.keep(wide, none))
+g.replay()
+fm.fm_sync_status()
+assert ((o - 1).abs() <= 2 * (5 + 8) * 2.0 ** -24).all() and kept.tolist() == [3, 3] and nxt.tolist() == [500, 500], (o, kept, nxt)
+assert c[torch.bfloat16].kv_len.tolist() == [3, 3] and big.kv_len.sum() == 0
+print("captured")
+"""
+    path = tmp_path / "first.py"
+    path.write_text(code)
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, str(path)], capture_output=True, text=True, timeout=300, env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]

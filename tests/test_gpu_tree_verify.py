@@ -236,3 +236,22 @@ def test_verify_captured_and_replayed(dev):  # noqa: F811
             sl = slice(at[i], at[i + 1])
             p, x = walk(c[0][sl], c[1][sl], c[2][sl], c[3][sl], c[4][sl].tolist(), float(u_last[i]), 6)
             assert path[i].tolist() == p + [-1] * (6 - len(p)) and kept[i] == len(p) and nxt[i] == x
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+def test_rows_past_32_bit_offsets(dev, drafted):  # noqa: F811
+    """The last rows of 20,000 by 131,072."""
+    g = torch.Generator(device=dev).manual_seed(68)
+    T, V, counts = 20000, 131072, [9, 7]
+    c = tree_case(g, counts, V, BF16, drafted)
+    far = [torch.empty(T, V, dtype=BF16, device=dev) for _ in range(2 if drafted else 1)]
+    for x, y in zip(far, c[:2]):
+        x[-16:] = y
+    pad = lambda x: torch.cat([torch.zeros(T - 16, dtype=x.dtype, device=dev), x])  # noqa: E731
+    path, kept, nxt = ints([[0] * 8] * 2, dev), ints([0] * 2, dev), ints([0] * 2, dev)
+    fm.fm_tree_verify(far[0], far[1] if drafted else None, ints([T - 16, T - 7, T], dev), pad(ints(c[2], dev)), pad(ints(c[3], dev)),
+                      pad(c[4]), c[5], path, kept, nxt)
+    fm.fm_sync_status()
+    for i, sl in enumerate((slice(0, 9), slice(9, 16))):
+        p, x = walk(c[0][sl], c[1][sl] if drafted else None, c[2][sl], c[3][sl], c[4][sl].tolist(), float(c[5][i]), 8)
+        assert path[i].tolist() == p + [-1] * (8 - len(p)) and kept[i] == len(p) and nxt[i] == x
