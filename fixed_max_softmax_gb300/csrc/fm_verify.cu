@@ -638,19 +638,32 @@ static_assert(sizeof(Shared) <= 48 * 1024, "shared memory without an attribute")
 }  // namespace
 
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t st) {
-  // As many CTAs a request as two a SM allow, or three where each has 96 KiB to read, and a thousand tokens at
-  // least.  By CTAs a request (us, L2 flushed):
-  //   requests, tokens, rows of                  1     2     4     8
-  //     1   128,000  bf16, target and draft   29.3  22.2  19.1  17.1
-  //    48   100,003  bf16, target             33.4  25.2  21.2  29.3
-  //    64   128,000  fp32, both                126  72.4  49.8  47.7
-  //   100    64,000  fp32, both               86.8  56.0  42.7  49.8
-  //   200    32,000  fp32, both               64.2  47.8  47.8  64.2
-  //   230    64,000  bf16, target             30.8  38.9  49.8  74.4
-  //    16     4,000  fp32, both               23.2  21.2  21.2  23.2
-  const int64_t bytes = a.V * (a.dtype == FM_F32 ? 4 : 2) * (a.q ? 2 : 1), sms = current_device_sm_count();
+  // As many CTAs a request as run at once (two a SM; clusters of 4 and 8 leave some SMs out), with a thousand
+  // tokens each at least.  Where trees branch (more nodes than a path has) and children were drawn, a request
+  // sums its row once a refusal, and parts of 16,000 tokens are worth up to four CTAs a SM.  By CTAs a
+  // request (us, L2 flushed; 8 nodes in trees of paths of 4 to 6, chains of 8):
+  //   requests, tokens, rows of                          1     2     4     8
+  //     1   128,000  bf16, target and draft           29.3  22.2  19.1  17.1
+  //    64   128,000  bf16, both, trees                 111  66.2  45.8  41.6
+  //    64   128,000  bf16, both, chains               45.7  31.4  29.3  37.5
+  //    64    32,000  bf16, both, trees                37.5  27.3  25.2  31.4
+  //   100    64,000  fp32, both, trees                86.7  55.9  41.6  49.8
+  //   100    64,000  fp32, both, chains               33.4  27.3  35.5  41.6
+  //   150   128,000  fp32, both, trees                 132  96.9  76.4  80.5
+  //   150   128,000  fp32, both, chains               55.9  45.7  60.0  74.4
+  //   200    32,000  fp32, both, trees                64.2  47.8  47.8  64.2
+  //    48   100,003  bf16, target                     33.4  25.2  21.2  29.3
+  //    76   100,000  fp32, target                     37.4  25.2  29.3  35.5
+  //   150    64,000  bf16, target                     27.3  23.2  37.5  53.9
+  //   230    64,000  bf16, target                     30.8  38.9  49.8  74.4
+  //    16     4,000  fp32, both, trees                23.2  21.2  21.2  23.2
+  const int64_t sms = current_device_sm_count();
+  const bool many_sums = a.q && a.T > a.n * a.max_path;
   unsigned ctas = kMostCtas;
-  while (ctas > 1 && (a.n * ctas > (bytes / ctas >= 96 * 1024 ? 3 : 2) * sms || a.V < 1024 * (int64_t)ctas)) ctas /= 2;
+  for (; ctas > 1; ctas /= 2) {
+    const int64_t most = many_sums && a.V / ctas >= 16000 ? 4 * sms : 2 * sms - (ctas >= 4 ? sms / 10 : 0);
+    if (a.n * ctas <= most && a.V >= 1024 * (int64_t)ctas) break;
+  }
   const bool draft = a.q != nullptr;
   if (a.dtype == FM_F32) return draft ? launch<float, true>(a, ctas, st) : launch<float, false>(a, ctas, st);
   if (a.dtype == FM_BF16) return draft ? launch<__nv_bfloat16, true>(a, ctas, st) : launch<__nv_bfloat16, false>(a, ctas, st);
