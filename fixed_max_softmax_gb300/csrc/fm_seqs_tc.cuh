@@ -318,6 +318,12 @@ __device__ __forceinline__ void mma_output(uint32_t tO, uint32_t tP, uint32_t b,
 // of two (bound by the tensor core and the exponentials), and a unit's start and end.
 constexpr int kTileCost1 = 4, kTileCost2 = 5, kUnitCost1 = 12, kUnitCost2 = 20;
 constexpr int kLeastRun = 12;  // shorter runs would cost more to merge than they save (none is shorter than a tile)
+// (trees, whose units have many rows to store and merge for few tiles: captured, one of 26 over 900 keys 17.4 us
+// with 12, 16.4 with 8, 16.7 with 6, 20.4 with 24; one of 8 over 300 13.7, 11.8, 11.7, 13.3; one of 60 24.3, 22.8,
+// 23.1, 27.0.  A line is at least one unit, 12, so that its parts are at least 8 * 12 / 19 = 5 long, as a tile of
+// two row tiles is: every part of a unit's tiles holds the start of one.  Parts of 6 would not.)
+constexpr int kLeastRunTree = 8;
+static_assert(kLeastRunTree * kUnitCost1 / (kUnitCost1 + kLeastRunTree - 1) >= kTileCost2, "no run is shorter than a tile");
 
 // This CTA's part [x0, x1) of the line, and the unit that x0 falls in: (b, h, t), starting at u0.
 struct StreamRun {
@@ -351,7 +357,7 @@ __device__ __forceinline__ int part_of(int a, int b, int c) {
 // Every thread of the CTA: sums the requests' costs, a run of requests a thread, in one scan, and
 // the thread whose requests hold x0 finds the unit.  A few dependent steps after one round of
 // loads, in as little code as can be: it stands before the first tile of every call.
-__device__ __forceinline__ void stream_run(const Params &p, int *warp_sum, StreamRun *out) {
+__device__ __forceinline__ void stream_run(const Params &p, int least, int *warp_sum, StreamRun *out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (p.n + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(b0 + each, p.n);
   unsigned int *err = blockIdx.x == 0 ? p.err : nullptr;
@@ -388,7 +394,7 @@ __device__ __forceinline__ void stream_run(const Params &p, int *warp_sum, Strea
   if (total == kMostLine && err && tid == 0 && atomicCAS(err, 0u, (unsigned)kDevErrLength) == 0u)
     err[1] = err[2] = err[3] = err[4] = 0u;
   if (none || total == kMostLine) total = 0;
-  const int parts = max(1, min((int)gridDim.x, (total + kLeastRun - 1) / kLeastRun)), c = blockIdx.x;
+  const int parts = max(1, min((int)gridDim.x, (total + least - 1) / least)), c = blockIdx.x;
   int x0 = 0, x1 = 0;
   if (c < parts) {
     x0 = part_of(total, c, parts);
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the work list, and whatever the caller's earlier kernels wrote
   pdl_trigger();
   StreamRun *run_of_cta = reinterpret_cast<StreamRun *>(gbase + C::offStat + 128);
-  if constexpr (MODE == kStream) stream_run(p, reinterpret_cast<int *>(gbase + C::offStat), run_of_cta);
+  if constexpr (MODE == kStream) stream_run(p, TREE ? kLeastRunTree : kLeastRun, reinterpret_cast<int *>(gbase + C::offStat), run_of_cta);
 
   // A wait of a whole warp of which one lane polls: 32 polling lanes take the time of 32 tests.
   auto wait_warp = [&](int i, uint32_t parity, unsigned code, int tag) -> bool {

@@ -622,7 +622,8 @@ FM_API int fm_paged_write(const fm_tensor *k, const fm_tensor *v, const int64_t 
  *             entries stay in the table, behind the request's last key)
  *   cu_q      int32 [n+1]: request i has cu_q[i+1] - cu_q[i] new tokens
  *   path      int32 [n, max_path], kept int32 [n]: the first kept[i] entries of path[i], ascending, are the new
- *             tokens that stay; 0: none does; -1: all do (a prompt chunk in the same call)
+ *             tokens that stay; 0: none does; -1: all do (a prompt chunk in the same call, of which
+ *             fm_tree_verify was given no nodes)
  *   src, dst  int64 [n, max_path] written: the slots that fm_paged_move reads and writes, -1 where nothing moves
  *   status    int32 [1] written: 0, or the number of requests whose kept or path cannot be (they keep all they
  *             have), or -1: free_count and the pages given back do not fit the list, and the call changes nothing
