@@ -120,10 +120,10 @@ def test_any_mask(dev, dtype, Hk, words):  # noqa: F811
 @pytest.mark.parametrize("lens", [[(25, 900)] * 24, [(1, 2600)] * 20, [(40, 4000), (8, 500), (9, 9)] * 6,
                                   ([(70, 900)] + [(1, 5)] * 9) * 6, [(5, 700)] * 90])
 def test_a_chain_is_causal(dev, dtype, lens):  # noqa: F811
-    """Trees without a branch give fm_attn_paged's bits, where both cut their work alike (at most 128 rows a request, and
-    work for the whole GPU)."""
+    """Trees without a branch are causal attention, and give fm_attn_paged's bits where both cut their work alike (at most
+    128 rows a request, and work for the whole GPU)."""
     g = torch.Generator(device=dev).manual_seed(45)
-    _, _, kc, vc, table = paged_case(g, lens, 2, 128, 16, dtype, True)
+    ks, vs, kc, vc, table = paged_case(g, lens, 2, 128, 16, dtype, True)
     q = rand(g, sum(a for a, _ in lens), 10, 128, dtype=dtype)
     words = 2
     mask = mask_of([list(range(-1, a - 1)) if a <= 32 * words else None for a, _ in lens], lens, words, dev)
@@ -131,6 +131,11 @@ def test_a_chain_is_causal(dev, dtype, lens):  # noqa: F811
     o2, lse2 = run_paged(q, kc, vc, table, lens, dev)
     fm.fm_sync_status()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    at = starts([a for a, _ in lens])
+    for i in range(0, len(lens), max(1, len(lens) // 12)):
+        (a, b), sl = lens[i], slice(at[i], at[i + 1])
+        ref = attend_seen(q[sl], ks[i], vs[i], causal_seen(a, b), 128 ** -0.5)
+        assert_close(o[sl], lse[:, sl], *ref, dtype, dtype, 128, b)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
