@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       n += 2 * tiles;
       // rows of a tile's V that are to be zero: before the window in the first, past the end in the last
       auto zero_rows = [&](uint32_t v, int from, int to) {
-        // the MMA warp says when that tile's V has landed (its stage may be rounds ahead of this warp)
+        // the MMA warp says when that tile's V has landed, or is the next to (its stage may be rounds ahead of this warp)
         const int st = (int)(v % C::NS);
         // (every decoding request has one to wait for, and time to poll)
         if (lane == 0)
@@ -720,11 +720,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V of the piece's tile j has landed, and those rows are zero
         auto v_ready = [&](int j, int st, uint32_t ph) -> bool {
           if (!wait(C::KVFull + st, ph, kDevErrTimeoutMma, j)) return false;
+          if constexpr (TREE) return !(tail && j == tiles - 1) || wait(C::VFix, fixes++ & 1u, kDevErrTimeoutMma, j);
           for (int f = (head && j == 0) + (tail && j == tiles - 1); f > 0; --f) {
             mbar_arrive(bar(C::VNeed));
             if (!wait(C::VFix, fixes++ & 1u, kDevErrTimeoutMma, j)) return false;
           }
           return true;
+        };
+        // Trees (no window, so that only a unit's last tile has such rows): warp 2 hears of the tile when its K is
+        // here, and works beside the scores and the softmax (one tree of 26 over 900 keys 16.3 -> 15.3 us,
+        // captured).  K's load is the one before V's, so that every earlier load of V's stage has landed, and the
+        // phase of the stage that warp 2 waits for is the next to complete.
+        auto k_here = [&](int j) {
+          if (TREE && tail && j == tiles - 1) mbar_arrive(bar(C::VNeed));
         };
         int vst = 0;
         uint32_t vph = 0;
@@ -733,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < tiles && ok; ++j) {
             ok = wait(C::KVFull + kst, kph, kDevErrTimeoutMma, j);
             if (!ok) break;
+            k_here(j);
             tc_fence_after();
             mma_s(0, 0, kst);
             if (j == tiles - 1) mma_commit(bar(C::QEmpty));
@@ -784,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < tiles && ok; ++j) {
             ok = wait(C::KVFull + kst, kph, kDevErrTimeoutMma, j);
             if (!ok) break;
+            k_here(j);
             tc_fence_after();
             mma_s(j & 1, qs, kst);
             mma_commit(bar(C::KVEmpty + kst));
