@@ -685,7 +685,8 @@ def fm_paged_write(k, v, slots, k_cache, v_cache, stream=None):
 def fm_paged_keep(cu_q, path, kept, kv_len, kv_len_out, block_table, free_pages, free_count, free_count_out, page_size: int,
                   src, dst, status, stream=None):
     """Of each request's new tokens only the first kept[i] of path[i] stay (-1: all): lengths, pages back to the list,
-    and the moves src, dst int64 [n, max_path] that fm_paged_move makes in each layer; see include/fm.h."""
+    and the moves src, dst int64 [n, max_path] that fm_paged_move makes in each layer (of larger buffers the first
+    n * max_path are filled, and only they are moves); see include/fm.h."""
     dev, n, i32, i64 = torch.cuda.current_device(), kept.numel(), torch.int32, torch.int64
     if path.dim() != 2 or path.shape[0] < n:
         raise FMError(FM_ERR_ARG, f"path must be a contiguous int32 [{n}, max_path] tensor, got {tuple(path.shape)}")
@@ -840,7 +841,8 @@ class PagedKVCache:
         if kept.numel() != self.kv_len.numel():
             raise FMError(FM_ERR_SHAPE, f"kept must have one entry for each of the {self.kv_len.numel()} rows")
         with _on_stream(stream):
-            moves = torch.empty(2, *path.shape, dtype=torch.int64, device=path.device)
+            # (path may be the buffer of a larger batch: only the cache's rows have moves)
+            moves = torch.empty(2, kept.numel(), *path.shape[1:], dtype=torch.int64, device=path.device)
             fm_paged_keep(self.cu_q, path, kept, self.kv_len, self.kv_len, self.block_table, self.free_pages, self.free_count,
                           self.free_count, self.page_size, moves[0], moves[1], self.status)
         return moves

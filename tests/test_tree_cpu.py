@@ -197,3 +197,18 @@ def test_keep_and_move_binding_refusals(lib, monkeypatch):  # noqa: F811
         fm.fm_paged_keep(*good)
     with pytest.raises(fm.FMError, match="CUDA device"):
         fm.fm_paged_move(w(2, 5), w(2, 5), cache, cache)
+
+
+def test_moves_are_of_the_caches_rows_alone(monkeypatch):
+    """A path buffer with more rows than the cache: fm_paged_keep fills the moves of the cache's, so that there are no
+    others for fm_paged_move to make."""
+    c, got = fm.PagedKVCache(6, 4, 2, 64, 3, 5, 7, device="cpu"), {}
+    monkeypatch.setattr(fm, "fm_paged_keep", lambda *a, **kw: got.update(src=a[10], dst=a[11]))
+    for rows in (3, 9):
+        moves = c.keep(torch.zeros(rows, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+        assert moves.shape == (2, 3, 2) and got["src"].shape == got["dst"].shape == (3, 2)
+    monkeypatch.undo()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # (where get_device() says that host tensors are)
+    for bad in (torch.zeros(6, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32), torch.zeros((), dtype=torch.int32)):
+        with pytest.raises(fm.FMError, match="path must be"):
+            c.keep(bad, torch.zeros(3, dtype=torch.int32))
