@@ -758,7 +758,8 @@ class PagedKVCache:
     New tokens may be drafted trees: after extend, mask = tree(parent) says what each node sees and sets
     positions by depth, tree_attention(q, mask) takes attention's place, and when verify_tree() has told
     what is kept, moves = keep(path, kept) cuts the lengths back and each layer's move(moves) puts the
-    kept rows in their places, before the next extend."""
+    kept rows in their places, before the next extend.  A step whose extend did not fit has no new tokens, keeps none,
+    and its status stays until the next extend; keep_status (0: every path could be) is keep's own."""
 
     def __init__(self, num_pages, page_size, kv_heads, head_dim, max_seqs, max_pages_per_seq, max_tokens,
                  dtype=torch.bfloat16, device="cuda", shared: "PagedKVCache | None" = None):
@@ -775,13 +776,13 @@ class PagedKVCache:
                                             f"max_tokens {has}, not {(max_seqs, max_pages_per_seq, max_tokens)}")
             if shared.kv_len.device != pages.device:
                 raise FMError(FM_ERR_ARG, f"layers that share tables are on one device: {shared.kv_len.device}, not {pages.device}")
-            for name in ("block_table", "free_pages", "free_count", "kv_len", "cu_q", "slots", "positions", "status"):
+            for name in ("block_table", "free_pages", "free_count", "kv_len", "cu_q", "slots", "positions", "status", "keep_status"):
                 setattr(self, name, getattr(shared, name))
         else:
             self.block_table = make(max_seqs, max_pages_per_seq)
             self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
             self.free_count = make(1).fill_(num_pages)
-            self.kv_len, self.cu_q, self.status = make(max_seqs), make(max_seqs + 1), make(1)
+            self.kv_len, self.cu_q, self.status, self.keep_status = make(max_seqs), make(max_seqs + 1), make(1), make(1)
             self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
             self.positions = make(max_tokens).fill_(-1)
 
@@ -837,14 +838,15 @@ class PagedKVCache:
 
     def keep(self, path, kept, stream=None):
         """path int32 [max_seqs, max_path], kept int32 [max_seqs] from verify_tree (kept -1: a row keeps all its new
-        tokens).  Returns the moves that move() makes in each layer; status counts the rows whose path could not be."""
+        tokens).  Returns the moves that move() makes in each layer; keep_status (of this call, as status is of extend)
+        counts the rows whose path could not be."""
         if kept.numel() != self.kv_len.numel():
             raise FMError(FM_ERR_SHAPE, f"kept must have one entry for each of the {self.kv_len.numel()} rows")
         with _on_stream(stream):
             # (path may be the buffer of a larger batch: only the cache's rows have moves)
             moves = torch.empty(2, kept.numel(), *path.shape[1:], dtype=torch.int64, device=path.device)
             fm_paged_keep(self.cu_q, path, kept, self.kv_len, self.kv_len, self.block_table, self.free_pages, self.free_count,
-                          self.free_count, self.page_size, moves[0], moves[1], self.status)
+                          self.free_count, self.page_size, moves[0], moves[1], self.keep_status)
         return moves
 
     def move(self, moves, stream=None):

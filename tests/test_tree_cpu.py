@@ -212,3 +212,14 @@ def test_moves_are_of_the_caches_rows_alone(monkeypatch):
     for bad in (torch.zeros(6, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32), torch.zeros((), dtype=torch.int32)):
         with pytest.raises(fm.FMError, match="path must be"):
             c.keep(bad, torch.zeros(3, dtype=torch.int32))
+
+
+def test_keep_has_a_status_of_its_own(monkeypatch):
+    """What extend reported stays until the next one; layers that share tables share both."""
+    c = fm.PagedKVCache(6, 4, 2, 64, 3, 5, 7, device="cpu")
+    other = fm.PagedKVCache(6, 4, 2, 64, 3, 5, 7, device="cpu", shared=c)
+    monkeypatch.setattr(fm, "fm_paged_keep", lambda *a, **kw: a[12].fill_(2))
+    c.status.fill_(5)
+    c.keep(torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+    for x in (c, other):
+        assert x.status.tolist() == [5] and x.keep_status.tolist() == [2]
