@@ -14,7 +14,7 @@ Functions with the ABI's names (same arguments, torch tensors in place of pointe
 ``fm_last_error``, ``fm_version``; and for requests of different lengths
 ``fm_attn_seqs_workspace_size``, ``fm_attn_varlen``, ``fm_attn_paged``, ``fm_paged_extend``,
 ``fm_paged_write``; for trees of drafted tokens ``fm_tree_mask``, ``fm_attn_tree``, ``fm_tree_verify``,
-``fm_paged_keep``, ``fm_paged_move``.
+``fm_tree_verify_rows``, ``fm_paged_keep``, ``fm_paged_move``.
 
 ``FixedMAttention`` owns the buffers of one problem shape and runs the whole path
 (bounds, one ``fm_attn_chunk`` per KV chunk, finalize); ``attention()`` is the
@@ -50,7 +50,7 @@ ABI_SYMBOLS = ("fm_bounds_workspace_size", "fm_bounds", "fm_attn_chunk", "fm_fin
                "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
                "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree",
-               "fm_tree_verify", "fm_paged_keep", "fm_paged_move")
+               "fm_tree_verify", "fm_tree_verify_rows", "fm_paged_keep", "fm_paged_move")
 FM_MAX_CHUNKS = 8
 FM_MAX_SINKS = 8
 FM_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -153,6 +153,7 @@ def load(path: str | None = None):
     lib.fm_tree_mask.argtypes = [P, P, i64, P, i64, i64, P, P]
     lib.fm_attn_tree.argtypes = [P, P, P, P, P, i64, i64, P, P, P, P, ctypes.c_size_t, P]
     lib.fm_tree_verify.argtypes = [P, P, i64, P, P, P, P, P, i64, P, P, P, P]
+    lib.fm_tree_verify_rows.argtypes = [P, P, i64, P, P, i64, P, P, P, P, i64, P, P, P, P]
     lib.fm_paged_keep.argtypes = [P, P, i64, P, P, P, P, P, P]
     lib.fm_paged_move.argtypes = [i64, i64, P, P, P, P, P]
     lib.fm_sync_status.argtypes = [P]
@@ -164,7 +165,7 @@ def load(path: str | None = None):
                  "fm_attn_chunk_final", "fm_attn_chunks", "fm_fold_sinks", "fm_ring_stats_bytes", "fm_ring_key_sums",
                  "fm_bounds_local", "fm_bounds_combine", "fm_attention_host", "fm_attn_seqs_workspace_size",
                  "fm_attn_varlen", "fm_attn_paged", "fm_paged_extend", "fm_paged_write", "fm_tree_mask", "fm_attn_tree",
-                 "fm_tree_verify", "fm_paged_keep", "fm_paged_move"):
+                 "fm_tree_verify", "fm_tree_verify_rows", "fm_paged_keep", "fm_paged_move"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -638,19 +639,22 @@ def _probabilities(t, name, device):
     return _TENSOR_BYTES(t.data_ptr(), _DTYPES.get(t.dtype, -1), 0, 1, 1, T, V, 0, 0, sT, sV)
 
 
-def fm_tree_verify(target, draft, cu_q, tokens, parent, u, u_last, path, kept, next_token, stream=None):
+def fm_tree_verify(target, draft, cu_q, tokens, parent, u, u_last, path, kept, next_token, stream=None, rows=None):
     """target and draft [T, V] probabilities after each node (draft None: the nodes were chosen, not drawn);
     tokens, parent int32 [T], u float32 [T], u_last [n]; fills path int32 [n, max_path], kept and
-    next_token int32 [n]; see include/fm.h."""
-    dev, n, T, i32, f32 = torch.cuda.current_device(), cu_q.numel() - 1, target.shape[0], torch.int32, torch.float32
+    next_token int32 [n].  rows int32 [n] (fm_tree_verify_rows): the row of target and draft after each request's
+    node 0, which then need rows for nodes alone; -1: a request that is no tree (a prompt chunk of any length) is
+    passed over, its kept -1; see include/fm.h."""
+    dev, n, i32, f32 = torch.cuda.current_device(), cu_q.numel() - 1, torch.int32, torch.float32
+    T = target.shape[0] if rows is None else tokens.numel()
     if path.dim() != 2 or path.shape[0] < n:
         raise FMError(FM_ERR_ARG, f"path must be a contiguous int32 [{n}, max_path] tensor, got {tuple(path.shape)}")
-    rc = load().fm_tree_verify(_probabilities(target, "target", dev), None if draft is None else _probabilities(draft, "draft", dev),
-                               n, _ints(cu_q, i32, 1, "cu_q", dev), _ints(tokens, i32, T, "tokens", dev),
-                               _ints(parent, i32, T, "parent", dev), _ints(u, f32, T, "u", dev),
-                               _ints(u_last, f32, n, "u_last", dev), path.shape[1], _ints(path, i32, 0, "path", dev),
-                               _ints(kept, i32, n, "kept", dev), _ints(next_token, i32, n, "next_token", dev),
-                               _stream_handle(stream, dev))
+    fn, at = (load().fm_tree_verify, ()) if rows is None else (load().fm_tree_verify_rows, (_ints(rows, i32, n, "rows", dev), T))
+    rc = fn(_probabilities(target, "target", dev), None if draft is None else _probabilities(draft, "draft", dev),
+            n, _ints(cu_q, i32, 1, "cu_q", dev), *at, _ints(tokens, i32, T, "tokens", dev),
+            _ints(parent, i32, T, "parent", dev), _ints(u, f32, T, "u", dev), _ints(u_last, f32, n, "u_last", dev),
+            path.shape[1], _ints(path, i32, 0, "path", dev), _ints(kept, i32, n, "kept", dev),
+            _ints(next_token, i32, n, "next_token", dev), _stream_handle(stream, dev))
     return rc if rc == FM_OK else _check(rc)
 
 
@@ -735,13 +739,15 @@ def attention_varlen(q, k, v, cu_q, cu_k=None, causal=True, window=0, softmax_sc
     return (o, lse) if with_lse else o
 
 
-def verify_tree(target, tokens, parent, cu_q, u, u_last, draft=None, max_path=16, stream=None):
+def verify_tree(target, tokens, parent, cu_q, u, u_last, draft=None, max_path=16, stream=None, rows=None):
     """One-call verification of trees of drafted tokens (fm_tree_verify): returns path int32 [n, max_path], kept and
-    next_token int32 [n]."""
+    next_token int32 [n].  In a step with prompt chunks beside trees, rows int32 [n] says which row of target and draft
+    comes after each tree's node 0, -1 for a chunk: it needs no rows, and its kept is -1, with which
+    PagedKVCache.keep leaves all its tokens."""
     with _on_stream(stream):
         n, make = cu_q.numel() - 1, lambda *shape: torch.empty(shape, dtype=torch.int32, device=target.device)
         path, kept, next_token = make(n, max_path), make(n), make(n)
-        fm_tree_verify(target, draft, cu_q, tokens, parent, u, u_last, path, kept, next_token)
+        fm_tree_verify(target, draft, cu_q, tokens, parent, u, u_last, path, kept, next_token, rows=rows)
     return path, kept, next_token
 
 
@@ -816,7 +822,8 @@ class PagedKVCache:
     def tree(self, parent, words=None, stream=None):
         """parent int32 [T]: each new token's parent among its request's new tokens, -1 for a root.  Returns the mask int32
         [T, words] (words: of 32 nodes, by default enough for T nodes in one tree, at most 32); positions become those of
-        the nodes' depths.  A request of more than 32 * words new tokens (a prompt chunk) is causal."""
+        the nodes' depths.  A request of more than 32 * words new tokens (a prompt chunk) is causal; a shorter chunk is
+        where each of its tokens has the one before it as its parent."""
         T = parent.numel()
         words = max(1, min(FM_MAX_NODES, T + 31) // 32) if words is None else words
         with _on_stream(stream):

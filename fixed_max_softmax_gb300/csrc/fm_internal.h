@@ -243,8 +243,9 @@ cudaError_t launch_tree_mask(const TreeMaskArgs &a, cudaStream_t st);
 struct TreeVerifyArgs {
   const void *p, *q;  // the target's and the draft's rows (q or nullptr), sp and sq elements apart
   int dtype;
-  int64_t sp, sq, T, V, n, max_path;
+  int64_t sp, sq, R, T, V, n, max_path;  // R rows of probabilities, T tokens
   const int32_t *cu_q, *tokens, *parent;
+  const int32_t *rows;  // each request's first row, negative: it is not verified; nullptr: as cu_q
   const float *u, *u_last;
   int32_t *path, *kept, *next;
   unsigned int *err;

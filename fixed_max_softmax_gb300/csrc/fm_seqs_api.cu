@@ -228,6 +228,53 @@ int attn_seqs(const char *name, bool paged, const TreeMask *mask, const fm_tenso
   return FM_OK;
 }
 
+// The call behind fm_tree_verify and fm_tree_verify_rows (with rows), of T tokens.
+int tree_verify(const char *name, const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q,
+                const int32_t *rows, int64_t T, const int32_t *tokens, const int32_t *parent, const float *u, const float *u_last,
+                int64_t max_path, int32_t *path, int32_t *kept, int32_t *next_token, fm_stream_t stream) {
+  clear_error();
+  TreeVerifyArgs a;
+  int rc;
+  if ((rc = check_probabilities(target, "target"))) return rc;
+  if (draft) {
+    if ((rc = check_probabilities(draft, "draft"))) return rc;
+    if (draft->dtype != target->dtype) return fail(FM_ERR_DTYPE, "target and draft must share one dtype");
+    if (draft->S != target->S || draft->D != target->D) return fail(FM_ERR_SHAPE, "the shapes of target and draft differ");
+  }
+  if (n_seqs < 0 || max_path < 1) return fail(FM_ERR_ARG, "n_seqs = %lld, max_path = %lld", (long long)n_seqs, (long long)max_path);
+  if (n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)n_seqs, kMaxSeqs);
+  if (max_path > FM_MAX_NODES) return fail(FM_ERR_UNSUPPORTED, "paths of %lld nodes: at most %d", (long long)max_path, FM_MAX_NODES);
+  if (n_seqs == 0) return FM_OK;
+  if (!cu_q || !u_last || !path || !kept || !next_token || (T > 0 && (!tokens || !parent || !u)))
+    return fail(FM_ERR_ARG, "every array of %s but draft must be given", name);
+  if (misaligned(cu_q, 4) || misaligned(tokens, 4) || misaligned(parent, 4) || misaligned(u, 4) || misaligned(u_last, 4) ||
+      misaligned(path, 4) || misaligned(kept, 4) || misaligned(next_token, 4))
+    return fail(FM_ERR_ARG, "the arrays of %s must be aligned to their elements", name);
+  a.p = target->ptr;
+  a.q = draft ? draft->ptr : nullptr;
+  a.dtype = target->dtype;
+  a.sp = target->stride[2];
+  a.sq = draft ? draft->stride[2] : 0;
+  a.R = target->S;
+  a.T = T;
+  a.V = target->D;
+  a.n = n_seqs;
+  a.max_path = max_path;
+  a.cu_q = cu_q;
+  a.rows = rows;
+  a.tokens = tokens;
+  a.parent = parent;
+  a.u = u;
+  a.u_last = u_last;
+  a.path = path;
+  a.kept = kept;
+  a.next = next_token;
+  a.err = dev_error_ptr();
+  if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
+  const cudaError_t e = launch_tree_verify(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FM_OK : cuda_fail(e, name);
+}
+
 }  // namespace
 
 extern "C" {
@@ -296,45 +343,19 @@ int fm_tree_mask(const fm_seqs *seqs, const int32_t *parent, int64_t T, uint32_t
 int fm_tree_verify(const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q, const int32_t *tokens,
                    const int32_t *parent, const float *u, const float *u_last, int64_t max_path, int32_t *path, int32_t *kept,
                    int32_t *next_token, fm_stream_t stream) {
+  return tree_verify("fm_tree_verify", target, draft, n_seqs, cu_q, nullptr, target ? target->S : 0, tokens, parent, u, u_last,
+                     max_path, path, kept, next_token, stream);
+}
+
+int fm_tree_verify_rows(const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q, const int32_t *rows,
+                        int64_t T, const int32_t *tokens, const int32_t *parent, const float *u, const float *u_last,
+                        int64_t max_path, int32_t *path, int32_t *kept, int32_t *next_token, fm_stream_t stream) {
   clear_error();
-  TreeVerifyArgs a;
-  int rc;
-  if ((rc = check_probabilities(target, "target"))) return rc;
-  if (draft) {
-    if ((rc = check_probabilities(draft, "draft"))) return rc;
-    if (draft->dtype != target->dtype) return fail(FM_ERR_DTYPE, "target and draft must share one dtype");
-    if (draft->S != target->S || draft->D != target->D) return fail(FM_ERR_SHAPE, "the shapes of target and draft differ");
-  }
-  if (n_seqs < 0 || max_path < 1) return fail(FM_ERR_ARG, "n_seqs = %lld, max_path = %lld", (long long)n_seqs, (long long)max_path);
-  if (n_seqs > kMaxSeqs) return fail(FM_ERR_UNSUPPORTED, "%lld requests: at most %d", (long long)n_seqs, kMaxSeqs);
-  if (max_path > FM_MAX_NODES) return fail(FM_ERR_UNSUPPORTED, "paths of %lld nodes: at most %d", (long long)max_path, FM_MAX_NODES);
-  if (n_seqs == 0) return FM_OK;
-  if (!cu_q || !u_last || !path || !kept || !next_token || (target->S > 0 && (!tokens || !parent || !u)))
-    return fail(FM_ERR_ARG, "every array of fm_tree_verify but draft must be given");
-  if (misaligned(cu_q, 4) || misaligned(tokens, 4) || misaligned(parent, 4) || misaligned(u, 4) || misaligned(u_last, 4) ||
-      misaligned(path, 4) || misaligned(kept, 4) || misaligned(next_token, 4))
-    return fail(FM_ERR_ARG, "the arrays of fm_tree_verify must be aligned to their elements");
-  a.p = target->ptr;
-  a.q = draft ? draft->ptr : nullptr;
-  a.dtype = target->dtype;
-  a.sp = target->stride[2];
-  a.sq = draft ? draft->stride[2] : 0;
-  a.T = target->S;
-  a.V = target->D;
-  a.n = n_seqs;
-  a.max_path = max_path;
-  a.cu_q = cu_q;
-  a.tokens = tokens;
-  a.parent = parent;
-  a.u = u;
-  a.u_last = u_last;
-  a.path = path;
-  a.kept = kept;
-  a.next = next_token;
-  a.err = dev_error_ptr();
-  if (!a.err) return fail(FM_ERR_CUDA, "no CUDA device");
-  const cudaError_t e = launch_tree_verify(a, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? FM_OK : cuda_fail(e, "fm_tree_verify launch");
+  if ((n_seqs > 0 && !rows) || misaligned(rows, 4)) return fail(FM_ERR_ARG, "rows must be given, 4-byte aligned");
+  if (T < 0) return fail(FM_ERR_ARG, "T = %lld", (long long)T);
+  if (T > kMaxRows) return fail(FM_ERR_UNSUPPORTED, "more than 2^30 tokens");
+  return tree_verify("fm_tree_verify_rows", target, draft, n_seqs, cu_q, rows, T, tokens, parent, u, u_last, max_path, path, kept,
+                     next_token, stream);
 }
 
 int fm_paged_extend(const fm_page_state *state, const int32_t *new_len, const uint8_t *release, int64_t max_tokens,

@@ -99,7 +99,7 @@ struct Pair {
 struct Shared {
   int parent[FM_MAX_NODES], token[FM_MAX_NODES];  // token -1: outside the vocabulary
   float u[FM_MAX_NODES], p[FM_MAX_NODES], q[FM_MAX_NODES];
-  int first, nodes;             // as the first CTA read them, and the last random number
+  int first, nodes;             // row of node 0 and nodes (-1: not verified), as the first CTA read them, and the last random number
   float u_last;
   int refused[FM_MAX_NODES];    // tokens taken out of p (children that were chosen)
   Pair part[2][kMostCtas * kWarps];  // the sums of all CTAs' warps, of alternate passes
@@ -261,14 +261,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
   if (rank == 0) {
     const Rows r = rows_of(a.cu_q, req, a.T, tid == 0 ? a.err : nullptr);
     const float u_last = a.u_last[req];
+    const int row0 = a.rows ? a.rows[req] : r.first;
     int nodes = r.count;
-    if (nodes > FM_MAX_NODES) {
-      if (tid == 0) report(a.err, kDevErrLength, (unsigned)req, (unsigned)r.first, (unsigned)(r.first + r.count), 0u);
+    if (row0 < 0) {
+      nodes = -1;  // not verified
+    } else if (nodes > FM_MAX_NODES || (int64_t)row0 + nodes > a.R) {
+      if (tid == 0) report(a.err, kDevErrLength, (unsigned)req, (unsigned)row0, (unsigned)row0 + (unsigned)nodes, 0u);
       nodes = 0;
     }
     cluster_wait();
     if (tid < (int)ctas) {
-      put_remote(in_cta(smem_at(&s.first), tid), (uint32_t)r.first);
+      put_remote(in_cta(smem_at(&s.first), tid), (uint32_t)row0);
       put_remote(in_cta(smem_at(&s.nodes), tid), (uint32_t)nodes);
       put_remote(in_cta(smem_at(&s.u_last), tid), __float_as_uint(fminf(fmaxf(u_last, 0.f), 1.f)));
     }
@@ -283,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
       }
       if (parent < 0 || parent >= t) parent = -1;  // never reached: a child comes behind its parent
       if (parent >= 0 && token >= 0) {
-        p = some(as_f32(reinterpret_cast<const E *>(a.p)[(int64_t)(r.first + parent) * a.sp + token]));
-        if (DRAFT) q = some(as_f32(reinterpret_cast<const E *>(a.q)[(int64_t)(r.first + parent) * a.sq + token]));
+        p = some(as_f32(reinterpret_cast<const E *>(a.p)[(int64_t)(row0 + parent) * a.sp + token]));
+        if (DRAFT) q = some(as_f32(reinterpret_cast<const E *>(a.q)[(int64_t)(row0 + parent) * a.sq + token]));
       }
       for (uint32_t c = 0; c < ctas; ++c) {
         put_remote(in_cta(smem_at(&s.parent[t]), c), (uint32_t)parent);
@@ -302,10 +305,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const TreeVeri
   // (from here on what decides the way is the same in every CTA: they meet equally often)
   const int first = s.first, nodes = s.nodes;
   int32_t *path = a.path + (int64_t)req * a.max_path;
-  if (nodes == 0) {
+  if (nodes <= 0) {
     if (rank == 0) {
       for (int64_t j = tid; j < a.max_path; j += kThreads) path[j] = -1;
-      if (tid == 0) a.kept[req] = 0, a.next[req] = -1;
+      if (tid == 0) a.kept[req] = nodes, a.next[req] = -1;
     }
     return;
   }
@@ -658,7 +661,7 @@ cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t st) {
   //   230    64,000  bf16, target                     30.8  38.9  49.8  74.4
   //    16     4,000  fp32, both, trees                23.2  21.2  21.2  23.2
   const int64_t sms = current_device_sm_count();
-  const bool many_sums = a.q && a.T > a.n * a.max_path;
+  const bool many_sums = a.q && a.R > a.n * a.max_path;
   unsigned ctas = kMostCtas;
   for (; ctas > 1; ctas /= 2) {
     const int64_t most = many_sums && a.V / ctas >= 16000 ? 4 * sms : 2 * sms - (ctas >= 4 ? sms / 10 : 0);

@@ -522,7 +522,8 @@ FM_API int fm_attn_paged(const fm_tensor *q, const fm_tensor *k_cache, const fm_
  *   mask              rows of mask_words 32-bit words, mask_stride words apart, one a token: bit j (of
  *                     word j / 32) of row t says that t sees node j of its request.  Bits of later
  *                     nodes (j > t) and of nodes that the request does not have are not looked at.
- * A request of more new tokens than a mask row has bits (a prompt chunk in the same call) is causal. */
+ * A request of more new tokens than a mask row has bits (a prompt chunk in the same call) is causal; a chunk of
+ * fewer is a tree like any other, and causal where each token's parent is the one before it. */
 #define FM_MAX_NODES 1024 /* bits of a mask row, and nodes of a tree that fm_tree_verify takes */
 
 /* fm_tree_mask -- the mask of trees: every node sees itself and its ancestors.
@@ -573,6 +574,18 @@ FM_API int fm_tree_verify(const fm_tensor *target, const fm_tensor *draft, int64
                           const int32_t *tokens, const int32_t *parent, const float *u, const float *u_last,
                           int64_t max_path, int32_t *path, int32_t *kept, int32_t *next_token, fm_stream_t stream);
 
+/* fm_tree_verify_rows -- the same in a step whose requests are not all trees: prompt chunks of any length beside them are
+ * passed over, and only nodes have rows of probabilities.
+ *   target, draft  [1, 1, R, V]: row rows[i] + t is the one after node t of request i
+ *   rows       int32 [n]; negative: request i is not verified, whatever its tokens are.  Its path is all -1, its
+ *              next_token -1 and kept -1, with which fm_paged_keep leaves all of them in the cache
+ *   T          length of tokens, parent and u, where request i's are cu_q[i] .. cu_q[i+1]-1
+ * Rows that target does not have: the request has no nodes, and fm_sync_status reports it (FM_ERR_INDEX). */
+FM_API int fm_tree_verify_rows(const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q,
+                               const int32_t *rows, int64_t T, const int32_t *tokens, const int32_t *parent, const float *u,
+                               const float *u_last, int64_t max_path, int32_t *path, int32_t *kept, int32_t *next_token,
+                               fm_stream_t stream);
+
 /* The state of a paged cache's bookkeeping (host struct of device arrays). */
 typedef struct {
   int64_t n_seqs, page_size, num_pages;
@@ -622,8 +635,8 @@ FM_API int fm_paged_write(const fm_tensor *k, const fm_tensor *v, const int64_t 
  *             entries stay in the table, behind the request's last key)
  *   cu_q      int32 [n+1]: request i has cu_q[i+1] - cu_q[i] new tokens
  *   path      int32 [n, max_path], kept int32 [n]: the first kept[i] entries of path[i], ascending, are the new
- *             tokens that stay; 0: none does; -1: all do (a prompt chunk in the same call, of which
- *             fm_tree_verify was given no nodes)
+ *             tokens that stay; 0: none does; -1: all do (a prompt chunk in the same call, which
+ *             fm_tree_verify_rows passed over)
  *   src, dst  int64 [n, max_path] written: the slots that fm_paged_move reads and writes, -1 where nothing moves
  *   status    int32 [1] written: 0, or the number of requests whose kept or path cannot be (they keep all they
  *             have), or -1: free_count and the pages given back do not fit the list, and the call changes nothing

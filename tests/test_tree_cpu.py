@@ -223,3 +223,38 @@ def test_keep_has_a_status_of_its_own(monkeypatch):
     c.keep(torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
     for x in (c, other):
         assert x.status.tolist() == [5] and x.keep_status.tolist() == [2]
+
+
+# ---------------------------------------------------------------- verification of steps that are not all trees
+def verify_rows(lib, p=None, n=3, T=70, max_path=8, **kw):  # noqa: F811
+    a = dict(cu=FAKE, rows=FAKE, tokens=FAKE, parent=FAKE, u=FAKE, u_last=FAKE, path=FAKE, kept=FAKE, nxt=FAKE)
+    a.update(kw)
+    return lib.fm_tree_verify_rows(ctypes.byref(p or rows()), None, n, a["cu"], a["rows"], T, a["tokens"], a["parent"], a["u"],
+                                   a["u_last"], max_path, a["path"], a["kept"], a["nxt"], None)
+
+
+def test_verify_rows_refusals(lib):  # noqa: F811
+    for name in ("cu", "rows", "tokens", "parent", "u", "u_last", "path", "kept", "nxt"):
+        assert verify_rows(lib, **{name: None}) == fm.FM_ERR_ARG, name
+        assert verify_rows(lib, **{name: FAKE + 2}) == fm.FM_ERR_ARG, name
+    assert verify_rows(lib, T=-1) == fm.FM_ERR_ARG and verify_rows(lib, n=-1) == fm.FM_ERR_ARG
+    assert verify_rows(lib, T=2 ** 30 + 1) == fm.FM_ERR_UNSUPPORTED
+    assert verify_rows(lib, n=fm.FM_MAX_SEQS + 1) == fm.FM_ERR_UNSUPPORTED
+    assert verify_rows(lib, max_path=0) == fm.FM_ERR_ARG and verify_rows(lib, p=rows(step=2)) == fm.FM_ERR_UNSUPPORTED
+    assert verify_rows(lib, p=view(1, 2, 50, 1000, fm.FM_F32)) == fm.FM_ERR_SHAPE
+    assert verify_rows(lib, n=0, cu=None, rows=None) == fm.FM_OK  # no request: nothing to do
+
+
+def test_verify_rows_binding_refusals(lib, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # (where get_device() says that host tensors are)
+    i, f = (lambda *s: torch.zeros(s, dtype=torch.int32)), (lambda *s: torch.zeros(s))
+    good = [f(4, 10), f(4, 10), i(3), i(9), i(9), f(9), f(2), i(2, 5), i(2), i(2)]
+    for bad in (i(1), i(2).long(), f(2), i(4)[::2]):
+        with pytest.raises(fm.FMError, match="rows"):
+            fm.fm_tree_verify(*good, stream=0, rows=bad)
+    for at, bad in ((4, i(8)), (5, f(8)), (3, i(9).long()), (8, i(1))):
+        with pytest.raises(fm.FMError):
+            fm.fm_tree_verify(*good[:at], bad, *good[at + 1:], stream=0, rows=i(2))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(fm.FMError, match="CUDA device"):
+        fm.fm_tree_verify(*good, rows=i(2))
