@@ -403,7 +403,9 @@ cudaError_t launch_seqs_merge(const SeqsArgs &a, const SeqsGeom &g, const SeqsSp
   m.o = a.o;
   // without a list of cut units, one CTA for each that may be, more where requests have many rows: of one a
   // token up to 8, and of one for each kMergeRows rows up to 32, the larger (one tree of 64 nodes over 30k keys,
-  // 256 rows a unit: 66 us with 8, 55 with 32)
+  // 256 rows a unit: 66 us with 8, 55 with 32; decoding, where one a token was all, with 64 query heads to a key
+  // head: one request over 30k keys 104 -> 36, 64 over 4k 60 -> 50, 8 of two tokens over 8k 61 -> 33; 32 to one: 64
+  // over 8k 121 -> 115, 4 over 65k 86 -> 74; up to 8 to one the same)
   const int64_t tokens = (a.q.S + a.n - 1) / a.n, each = (tokens * g.group + kMergeRows - 1) / kMergeRows;
   const int64_t few = tokens < 8 ? tokens : 8, many = each < 32 ? each : 32;
   const dim3 grid = g.stream ? dim3((unsigned)g.ctas, (unsigned)(few > many ? few : many)) : dim3((unsigned)(8 * g.ctas));

@@ -18,7 +18,12 @@
 // CTA's shared memory.  A walk without a refusal reads one row of the vocabulary in all.
 // Sums and tests are compared with random numbers, and a sum that is off by 2^-24 would pick another token
 // than the definition does at every border that the number falls next to.  All of it is done in pairs of fp32
-// numbers, a value and its error, good to about 2^-45: an SM adds two 64-bit numbers a clock, and one takes
+// numbers, a value and its error.  With u = 2^-24: of p - A q the error is at most u (p + 2 A q), and its two roundings
+// 4 u^2 (p + A q).  A two-sum is exact, and what it lost, at most u of the sum so far, is added to the sum's
+// error, which after N additions of total X, the elements' M = sum (p + 2 A q), is at most u (N X + M): its N
+// roundings are at most (N^2 + N) u^2 M together.  N is V / 1024 + 20 where a request has one CTA; the
+// roundings have either sign, and rows of softmaxes come out to 2^-48 up to 2^21 tokens, 2^-44 at 2^24.  An SM
+// adds two 64-bit numbers a clock, and one takes
 // some hundred clocks, a pair's addition a dozen fp32 operations (64 chains over 128,000 tokens: 152 us with
 // 64-bit sums, 98 with pairs for the elements and 64 bits in every warp's tests, 29 with 64 bits in one warp of a
 // CTA, 28 without any; 22 with two elements to an instruction).
@@ -99,7 +104,7 @@ struct Pair {
 struct Shared {
   int parent[FM_MAX_NODES], token[FM_MAX_NODES];  // token -1: outside the vocabulary
   float u[FM_MAX_NODES], p[FM_MAX_NODES], q[FM_MAX_NODES];
-  int first, nodes;             // row of node 0 and nodes (-1: not verified), as the first CTA read them, and the last random number
+  int first, nodes;             // row of node 0, nodes (-1: not verified) and the last random number, as the first CTA read them
   float u_last;
   int refused[FM_MAX_NODES];    // tokens taken out of p (children that were chosen)
   Pair part[2][kMostCtas * kWarps];  // the sums of all CTAs' warps, of alternate passes
@@ -114,7 +119,8 @@ enum : int { kSum, kFind, kDone };
 
 // A row of one model in blocks of 16 bytes, block 0 beginning `shift` elements before the row: element `e`
 // of block b is element b * VEC - shift + e of the row.  A target's row has the shift that puts its blocks on
-// 16-byte boundaries; the draft's row is cut like it, and its blocks may lie anywhere.
+// 16-byte boundaries; the draft's row is cut like it, and its blocks may lie anywhere: off a boundary they are
+// read by elements (64 chains over 128,000 tokens fp32 19.3 -> 21.3 us, bf16 20.6 -> 25.1).
 template <typename E>
 struct Row {
   static constexpr int VEC = 16 / (int)sizeof(E);
@@ -643,7 +649,9 @@ static_assert(sizeof(Shared) <= 48 * 1024, "shared memory without an attribute")
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t st) {
   // As many CTAs a request as run at once (two a SM; clusters of 4 and 8 leave some SMs out), with a thousand
   // tokens each at least.  Where trees branch (more nodes than a path has) and children were drawn, a request
-  // sums its row once a refusal, and parts of 16,000 tokens are worth up to four CTAs a SM.  By CTAs a
+  // sums its row once a refusal, and parts of 16,000 tokens are worth up to four CTAs a SM.  (max_path is all that
+  // the host knows of the trees' shape: with more room in a path than a tree has nodes, trees of 8 are taken for
+  // chains, 100 over 64,000 tokens 35.5 -> 39.2 us, 150 over 128,000 72 -> 87, 64 of bf16 31.3 -> 32.9.)  By CTAs a
   // request (us, L2 flushed; 8 nodes in trees of paths of 4 to 6, chains of 8):
   //   requests, tokens, rows of                          1     2     4     8
   //     1   128,000  bf16, target and draft           29.3  22.2  19.1  17.1

@@ -566,10 +566,14 @@ FM_API int fm_attn_tree(const fm_tensor *q, const fm_tensor *k_cache, const fm_t
  *   path       int32 [n, max_path] written: the nodes kept, node 0 first, -1 behind them
  *   kept       int32 [n] written: their number; 0 for a request without nodes
  *   next_token int32 [n] written: -1 for a request without nodes, or whose last row of p is all 0
- * Tests and sums are made in 64 bits, so that the result is the definition's unless a number lies within
- * some 2^-45 of a border.  A token outside the vocabulary is never kept, more than FM_MAX_NODES nodes are
- * none; fm_sync_status reports both (FM_ERR_INDEX).  Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE,
- * FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
+ * Tests and sums are made in pairs of fp32 numbers, a value and its error, and the result is the definition's
+ * unless a random number lies as close to a border as they are off: what is left of a token by at most
+ * 2^-46 (p + A q), a sum over V tokens besides by at most (N^2 + N) 2^-48 sum (p + 2 A q), N = V / 1024 + 20 the
+ * numbers that one of its lanes adds (on rows of softmaxes by 2^-48 up to V = 2^21, 2^-44 at 2^24).  A token
+ * outside the vocabulary is never kept, more than FM_MAX_NODES nodes are none; fm_sync_status reports both
+ * (FM_ERR_INDEX).
+ * Rows of draft that lie otherwise to a 16-byte boundary than target's are read an element at a time, which takes
+ * longer.  Errors: FM_ERR_ARG, FM_ERR_SHAPE, FM_ERR_DTYPE, FM_ERR_UNSUPPORTED, FM_ERR_CUDA. */
 FM_API int fm_tree_verify(const fm_tensor *target, const fm_tensor *draft, int64_t n_seqs, const int32_t *cu_q,
                           const int32_t *tokens, const int32_t *parent, const float *u, const float *u_last,
                           int64_t max_path, int32_t *path, int32_t *kept, int32_t *next_token, fm_stream_t stream);
